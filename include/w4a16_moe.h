@@ -352,6 +352,171 @@ int moe_mat_grouped_ffn(const moe_ffn_args* args, float tau, void* stream);
 int moe_mat_decode_layer(const moe_decode_layer_args* args, float tau, void* stream);
 
 /*
+ * Rows sorted by expert and back, around experts that the caller runs itself
+ * (experts of another type or precision, experts in training): the token rows laid
+ * out in the order of moe_align, the weighted sum that brings the experts' rows
+ * back, and the gradient of both.  (ExactMoE, Abstract: every selected expert of a
+ * step runs through fused grouped kernels; the grouped passes above gather and
+ * combine inside their kernels, these calls do it for any other grouped product.)
+ *
+ * Pair p = t*k + j, pos = pair_pos[p] (from moe_align), w = weights[p], or 1 where
+ * weights is NULL:
+ *  moe_permute             rows[pos] = w x[t]
+ *  moe_unpermute           out[t] = sum_j w rows[pos]
+ *  moe_permute_backward    dx[t] = sum_j w drows[pos];  dweights[p] = <x[t], drows[pos]>
+ *  moe_unpermute_backward  drows[pos] = w dout[t];  dweights[p] = <dout[t], rows[pos]>
+ *
+ *  dtype     moe_dtype of every row tensor; weights and dweights are [T][k] float32.
+ *  x, dx, out, dout   [T][d]; rows, drows [num_rows][d], num_rows >= 0.  Each has
+ *            contiguous rows at a stride given in elements: at least d for outputs,
+ *            at least 0 for inputs (0: one row for all).  Pointers need the alignment
+ *            of their type only; 16-byte aligned rows are the fast case.
+ *  pair_pos  [T*k] int32.  Pairs whose position lies outside [0, num_rows) are
+ *            dropped: they write no row, add nothing and have the weight gradient 0;
+ *            a token whose pairs are all dropped gets a row of zeros.  Positions
+ *            inside must be distinct, as moe_align's are.
+ *  Rows of `rows` / `drows` that no pair names are neither read nor written.
+ *  Sums and products in float32 in slot order, one rounding to dtype (moe_permute
+ *  without weights copies the bits).  Deterministic.  Outputs may not overlap inputs.
+ *  dweights may be NULL (not wanted); then x (rows) may be NULL.  weights may be NULL
+ *  with dweights wanted.
+ *  Limits: 1 <= k <= 16, T*k <= 2^24, 1 <= d <= 2^24.  T == 0 is a no-op.
+ */
+enum moe_dtype { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 };
+
+int moe_permute(const void* x, int64_t x_stride, int dtype, int T, int d, int k, const int32_t* pair_pos,
+                const float* weights, void* rows, int64_t rows_stride, int64_t num_rows, void* stream);
+int moe_unpermute(const void* rows, int64_t rows_stride, int64_t num_rows, int dtype, int T, int d, int k,
+                  const int32_t* pair_pos, const float* weights, void* out, int64_t out_stride, void* stream);
+int moe_permute_backward(const void* drows, int64_t drows_stride, int64_t num_rows, const void* x, int64_t x_stride,
+                         int dtype, int T, int d, int k, const int32_t* pair_pos, const float* weights, void* dx,
+                         int64_t dx_stride, float* dweights, void* stream);
+int moe_unpermute_backward(const void* dout, int64_t dout_stride, const void* rows, int64_t rows_stride, int dtype,
+                           int T, int d, int k, const int32_t* pair_pos, const float* weights, void* drows,
+                           int64_t drows_stride, int64_t num_rows, float* dweights, void* stream);
+
+/*
+ * moe_route_backward -- gradient of moe_route: from the gradient of the routing
+ * weights to those of the router's input and weight.  (ExactMoE, Abstract: the
+ * router stays in BF16 and the top-k procedure is unchanged; the selection itself
+ * has no gradient, the weights of the selected experts have.)
+ *
+ *  x, w_router, logits, topk_ids, topk_weights: moe_route's inputs and outputs, with
+ *  its `renormalize`.  With s = sum_j w_j dweights_j over a token's selected experts,
+ *  the gradient of its logits is
+ *    renormalize = 1:  w_j (dweights_j - s) at the selected experts, 0 elsewhere;
+ *    renormalize = 0:  p_e ([e selected] dweights_e - s), p = softmax(logits);
+ *  plus dlogits [T][E] float32 (a loss on the logits themselves), unless NULL.
+ *  dx        [T][d] bf16 output: (gradient of the logits) w_router, plus dx_add [T][d]
+ *            bf16 unless NULL (what reached x on other paths, e.g. through the experts);
+ *            dx_add may be dx itself.  One rounding to bf16.  NULL: not wanted.
+ *  dw_router [E][d] float32 output: (gradient of the logits)^T x.  NULL: not wanted.
+ *  The gradient of the logits enters the matrix cores as a sum of bf16 parts: two for
+ *  dx (relative error 2^-18, under its bf16 rounding), three for dw_router (2^-27),
+ *  with float32 sums.  Deterministic.
+ *  workspace moe_route_backward_workspace_bytes(T, d, E, k) bytes, 256-byte aligned.
+ *  Entries of topk_ids outside [0, E) are ignored; the ids of a token are distinct.
+ *  Limits and errors: those of moe_route; x, w_router, dx and dx_add 16-byte aligned;
+ *  d <= 2^20, T <= 2^24.  T == 0: dw_router is set to zero.
+ */
+typedef struct {
+  const uint16_t* x;           /* [T][d] bf16 */
+  const uint16_t* w_router;    /* [E][d] bf16 */
+  int T, d, E, k;
+  int renormalize;
+  const float* logits;         /* [T][E]; may be NULL when renormalize = 1 */
+  const int32_t* topk_ids;     /* [T][k] */
+  const float* topk_weights;   /* [T][k] */
+  const float* dweights;       /* [T][k] */
+  const float* dlogits;        /* [T][E] or NULL */
+  const uint16_t* dx_add;      /* [T][d] bf16 or NULL */
+  uint16_t* dx;                /* [T][d] bf16 or NULL */
+  float* dw_router;            /* [E][d] or NULL */
+  void* workspace;
+  int64_t workspace_bytes;
+} moe_route_backward_args;
+int64_t moe_route_backward_workspace_bytes(int T, int d, int E, int k);
+int moe_route_backward(const moe_route_backward_args* args, void* stream);
+
+/*
+ * moe_block_norm -- what stands between two blocks: the norm behind a block with its
+ * gate, the scaled residual, and the norm before the next block, in one pass.
+ * (ExactMoE, Abstract: normalization layers stay in BF16 beside the routed experts.)
+ *
+ *    z = rms(y) * norm_out      (y itself where norm_out is NULL)
+ *    h = residual_scale * x + gate * z   (residual_scale * x where y is NULL)
+ *    n = rms(h) * norm_in       (where norm_in is given)
+ *    rms(v) = v / sqrt(mean(v^2) + eps) over the row
+ *
+ *  x         [T][d] residual stream.  y [T][d] block output, or NULL.
+ *  norm_out, norm_in   [d] weights, or NULL: no such norm.  norm_out and gate need y.
+ *  gate      by gate_kind: MOE_GATE_NONE (1; gate NULL), MOE_GATE_CHANNEL [d],
+ *            MOE_GATE_TOKEN [T] at gate_stride elements, MOE_GATE_FULL [T][d] with
+ *            rows at gate_stride.
+ *  h         [T][d] output, or NULL: not wanted.  n [T][d] output, given exactly
+ *            when norm_in is.  At least one of h and n.
+ *  Every tensor has the type `dtype`.  Rows are contiguous at the given strides
+ *  (elements; inputs at least 0, outputs at least d); pointers need the alignment of
+ *  their type only.  Statistics and products in float32; n is computed from h before
+ *  h is rounded.  h may be x or y itself, n may be y; otherwise outputs may not
+ *  overlap inputs or each other.
+ *  eps at least FLT_MIN; residual_scale finite.  Squares are summed in float32: rows
+ *  must have mean squares below 2^127 / d.
+ *  Limits: 1 <= d <= 16384, T <= 2^24.  T == 0 is a no-op.
+ *
+ * moe_block_norm_backward -- its gradient, from dh and dn (either may be NULL: zero;
+ *  dn only where norm_in is given), recomputing the statistics from x and y.
+ *  dx, dy    [T][d], type dtype, or NULL: not wanted.
+ *  dgate     MOE_GATE_CHANNEL: [d] float32; MOE_GATE_TOKEN: [T] float32;
+ *            MOE_GATE_FULL: [T][d], type dtype, rows at dgate_stride.  NULL: not wanted.
+ *  dnorm_out, dnorm_in  [d] float32, or NULL: not wanted.
+ *  The [d] gradients are summed over the rows in float32, in an order that depends on
+ *  T and d alone.  dx may be dh itself and dy may be y or dn itself; otherwise outputs
+ *  may not overlap inputs or each other.  workspace:
+ *  moe_block_norm_backward_workspace_bytes(T, d) bytes, 256-byte aligned, needed for
+ *  the [d] gradients only.  T == 0: they are set to zero.
+ */
+enum moe_gate_kind { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 };
+
+typedef struct {
+  int dtype;                   /* moe_dtype */
+  int T, d;
+  const void* x;
+  int64_t x_stride;
+  const void* y;
+  int64_t y_stride;
+  const void* norm_out;
+  const void* norm_in;
+  const void* gate;
+  int gate_kind;               /* moe_gate_kind */
+  int64_t gate_stride;
+  float residual_scale;
+  float eps;
+} moe_block_norm_args;
+
+typedef struct {
+  const void* dh;
+  int64_t dh_stride;
+  const void* dn;
+  int64_t dn_stride;
+  void* dx;
+  int64_t dx_stride;
+  void* dy;
+  int64_t dy_stride;
+  void* dgate;
+  int64_t dgate_stride;
+  float* dnorm_out;
+  float* dnorm_in;
+  void* workspace;
+  int64_t workspace_bytes;
+} moe_block_norm_grads;
+
+int moe_block_norm(const moe_block_norm_args* args, void* h, int64_t h_stride, void* n, int64_t n_stride,
+                   void* stream);
+int64_t moe_block_norm_backward_workspace_bytes(int T, int d);
+int moe_block_norm_backward(const moe_block_norm_args* args, const moe_block_norm_grads* grads, void* stream);
+
+/*
  * Expert slot cache (ExactMoE, Abstract: quantised experts in pinned host
  * memory, executed from a configurable GPU-resident slot cache).
  *
@@ -466,7 +631,9 @@ int moe_slot_cache_state(const moe_slot_cache* cache, int32_t* slot_expert,
  * Kernel ids: 0 = gate/up (decode), 1 = down (decode), 2 = gate/up (prefill),
  * 3 = down (prefill), 4 = combine, 5 = route logits, 6 = align, 7 = gate/up
  * (BF16 experts), 8 = down (BF16 experts), 9 = gate/up (nested two/four-bit),
- * 10 = down (nested two/four-bit).
+ * 10 = down (nested two/four-bit), 11 = moe_permute and moe_unpermute_backward,
+ * 12 = moe_unpermute and moe_permute_backward, 13 = moe_route_backward (its launches
+ * together), 14 = moe_block_norm, 15 = moe_block_norm_backward (its launches together).
  */
 int moe_timing_enable(int on);
 int moe_timing_reset(void);

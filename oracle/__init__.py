@@ -22,10 +22,11 @@ Modules
   align      expert-sorted permutation (stable counting sort)
   ffn        per-pair SwiGLU expert FFN, routing-weighted combine, whole layer
   slot_cache LRU simulator for the GPU-resident expert slot cache
+  rows       expert-sorted rows, router gradient and block norms, with their gradients
 
 Pinning status: every function here is pinned by a CPU test against brute
 force, closed forms, invariants or an independent formulation (tests/test_oracle_*.py).
 The pages print no worked example and no intermediate value, so no function is
 pinned to numbers from the pages themselves.
 """
-from . import bf16, quant, route, align, ffn, slot_cache  # noqa: F401
+from . import bf16, quant, route, align, ffn, rows, slot_cache  # noqa: F401

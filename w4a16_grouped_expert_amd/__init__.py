@@ -13,5 +13,10 @@ from .api import (MODE_AUTO, active_experts, MODE_DECODE, MODE_PREFILL, AlignOut
                   timing_reset, bf16_expert_bytes, pack_bf16_experts, moe_bf16_grouped_ffn, moe_bf16_grouped_ffn_into,
                   mat_layout, mat_from_w4, moe_mat_grouped_ffn_into, alloc_layer_counters, layer_routing_timed_out,
                   decode_layer_workspace_bytes, moe_decode_layer, moe_decode_layer_into,
-                  moe_mat_decode_layer_into)
+                  moe_mat_decode_layer_into, moe_permute, moe_permute_into, moe_permute_backward_into, moe_unpermute,
+                  moe_unpermute_into, moe_unpermute_backward_into, route_backward_workspace_bytes,
+                  alloc_route_backward_workspace, moe_route_backward, moe_route_backward_into, BlockNorm,
+                  BlockNormGrads, moe_block_norm, moe_block_norm_into, moe_block_norm_backward,
+                  moe_block_norm_backward_into, block_norm_workspace_bytes, alloc_block_norm_workspace,
+                  GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL)
 from ._lib import LIB_PATH, MoeError, lib  # noqa: F401

@@ -58,6 +58,31 @@ class LayerArgs(ctypes.Structure):
     ]
 
 
+class RouteBackwardArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", c_vp), ("w_router", c_vp), ("T", c_int), ("d", c_int), ("E", c_int), ("k", c_int),
+        ("renormalize", c_int), ("logits", c_vp), ("topk_ids", c_vp), ("topk_weights", c_vp), ("dweights", c_vp),
+        ("dlogits", c_vp), ("dx_add", c_vp), ("dx", c_vp), ("dw_router", c_vp),
+        ("workspace", c_vp), ("workspace_bytes", c_i64),
+    ]
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", c_int), ("T", c_int), ("d", c_int), ("x", c_vp), ("x_stride", c_i64), ("y", c_vp),
+        ("y_stride", c_i64), ("norm_out", c_vp), ("norm_in", c_vp), ("gate", c_vp), ("gate_kind", c_int),
+        ("gate_stride", c_i64), ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float),
+    ]
+
+
+class BlockNormGradArgs(ctypes.Structure):
+    _fields_ = [
+        ("dh", c_vp), ("dh_stride", c_i64), ("dn", c_vp), ("dn_stride", c_i64), ("dx", c_vp), ("dx_stride", c_i64),
+        ("dy", c_vp), ("dy_stride", c_i64), ("dgate", c_vp), ("dgate_stride", c_i64), ("dnorm_out", c_vp),
+        ("dnorm_in", c_vp), ("workspace", c_vp), ("workspace_bytes", c_i64),
+    ]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [c_int]),
@@ -81,6 +106,17 @@ SIGNATURES = {
     "moe_decode_layer_workspace_bytes": (c_i64, [c_int, c_int, c_int, c_int, c_int]),
     "moe_decode_layer": (c_int, [ctypes.POINTER(LayerArgs), c_vp]),
     "moe_mat_decode_layer": (c_int, [ctypes.POINTER(LayerArgs), ctypes.c_float, c_vp]),
+    "moe_permute": (c_int, [c_vp, c_i64, c_int, c_int, c_int, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, c_vp]),
+    "moe_unpermute": (c_int, [c_vp, c_i64, c_i64, c_int, c_int, c_int, c_int, c_vp, c_vp, c_vp, c_i64, c_vp]),
+    "moe_permute_backward": (c_int, [c_vp, c_i64, c_i64, c_vp, c_i64, c_int, c_int, c_int, c_int, c_vp, c_vp, c_vp,
+                                     c_i64, c_vp, c_vp]),
+    "moe_unpermute_backward": (c_int, [c_vp, c_i64, c_vp, c_i64, c_int, c_int, c_int, c_int, c_vp, c_vp, c_vp, c_i64,
+                                       c_i64, c_vp, c_vp]),
+    "moe_route_backward_workspace_bytes": (c_i64, [c_int, c_int, c_int, c_int]),
+    "moe_route_backward": (c_int, [ctypes.POINTER(RouteBackwardArgs), c_vp]),
+    "moe_block_norm": (c_int, [ctypes.POINTER(BlockNormArgs), c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "moe_block_norm_backward_workspace_bytes": (c_i64, [c_int, c_int]),
+    "moe_block_norm_backward": (c_int, [ctypes.POINTER(BlockNormArgs), ctypes.POINTER(BlockNormGradArgs), c_vp]),
     "moe_slot_cache_create": (c_int, [c_int, c_int, c_i64, c_vp, c_vp, ctypes.POINTER(c_vp)]),
     "moe_slot_cache_destroy": (c_int, [c_vp]),
     "slot_cache_load": (c_int, [c_vp, c_u64p, c_u64p, c_vp, c_i32p, c_i32p, c_vp, c_vp, c_vp]),

@@ -427,6 +427,362 @@ def moe_w4a16_grouped_ffn(x, route, al, bank, I, mode=MODE_AUTO, slot_of_expert=
     return moe_w4a16_grouped_ffn_into(x, route, al, bank, I, out, ws, mode, True, slot_of_expert, stream=stream)
 
 
+# ---------------------------------------------------------------- rows sorted by expert and back
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # moe_dtype in w4a16_moe.h
+
+
+def _launch(device, stream, call):
+    """status of call(stream handle), issued with `device` current; the stream defaults
+    to that device's current one."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream on {stream.device} for tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        return call(stream.cuda_stream)
+    with torch.cuda.device(device):
+        return call(stream.cuda_stream)
+
+
+def _like(t, name, dtype, shape, device):
+    """A contiguous tensor of this type and shape on `device`: its address."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, T, d, device, output=False):
+    """A [T, d] tensor with contiguous rows at any stride: its address and row stride."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != d:
+        raise ValueError(f"{name} must have shape ({T}, {d}), got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    stride, inner = t.stride()
+    if inner != 1 and d > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if T <= 1:
+        stride = d
+    elif output and stride < d:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.data_ptr(), stride
+
+
+def _row_type(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in DTYPES:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.dtype, t.device
+
+
+def _pairs(pair_pos, weights, dweights, T, k, device):
+    """Addresses of pair_pos (at least T*k positions), weights and dweights ([T, k])."""
+    if pair_pos.dtype != torch.int32:
+        raise TypeError(f"pair_pos must be torch.int32, got {pair_pos.dtype}")
+    if not pair_pos.is_contiguous() or pair_pos.numel() < T * k:
+        raise ValueError(f"pair_pos must be contiguous with at least {T * k} positions")
+    if pair_pos.device != device:
+        raise ValueError(f"pair_pos must be on {device}, got {pair_pos.device}")
+    w = None if weights is None else _like(weights, "weights", torch.float32, (T, k), device)
+    dw = None if dweights is None else _like(dweights, "dweights", torch.float32, (T, k), device)
+    return pair_pos.data_ptr(), w, dw
+
+
+def moe_permute_into(x, pair_pos, k, rows, weights: Optional[torch.Tensor] = None, stream=None):
+    """rows[pair_pos[t*k + j]] = x[t], times weights[t, j] if given.
+
+    x [T, d] and rows [num_rows, d] bf16, fp16 or fp32 with any row stride; pair_pos from
+    moe_align (AlignOut.pair_pos).  Pairs whose position is negative or past the last row
+    are dropped; rows that no pair names keep their contents."""
+    dtype, dev = _row_type(x, "x")
+    T, d = x.shape
+    R = rows.shape[0]
+    xp, xs = _rows(x, "x", dtype, T, d, dev)
+    rp, rs = _rows(rows, "rows", dtype, R, d, dev, True)
+    pp, wp, _ = _pairs(pair_pos, weights, None, T, k, dev)
+    check("moe_permute", _launch(dev, stream, lambda s: lib().moe_permute(
+        xp, xs, DTYPES[dtype], T, d, k, pp, wp, rp, rs, R, s)))
+    return rows
+
+
+def moe_unpermute_into(rows, pair_pos, k, out, weights: Optional[torch.Tensor] = None, stream=None):
+    """out[t] = sum over j of rows[pair_pos[t*k + j]], times weights[t, j] if given
+    (float32 sums in slot order, one rounding; dropped pairs add nothing)."""
+    dtype, dev = _row_type(rows, "rows")
+    R, d = rows.shape
+    T = out.shape[0]
+    rp, rs = _rows(rows, "rows", dtype, R, d, dev)
+    op, os = _rows(out, "out", dtype, T, d, dev, True)
+    pp, wp, _ = _pairs(pair_pos, weights, None, T, k, dev)
+    check("moe_unpermute", _launch(dev, stream, lambda s: lib().moe_unpermute(
+        rp, rs, R, DTYPES[dtype], T, d, k, pp, wp, op, os, s)))
+    return out
+
+
+def moe_permute_backward_into(drows, pair_pos, k, dx, weights: Optional[torch.Tensor] = None,
+                              x: Optional[torch.Tensor] = None, dweights: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of moe_permute: dx[t] = sum over j of w drows[pos]; with x and dweights
+    also dweights[t, j] = <x[t], drows[pos]> (0 for dropped pairs)."""
+    dtype, dev = _row_type(drows, "drows")
+    if (x is None) != (dweights is None):
+        raise ValueError("x and dweights go together")
+    R, d = drows.shape
+    T = dx.shape[0]
+    rp, rs = _rows(drows, "drows", dtype, R, d, dev)
+    op, os = _rows(dx, "dx", dtype, T, d, dev, True)
+    xp, xs = (None, 0) if x is None else _rows(x, "x", dtype, T, d, dev)
+    pp, wp, dwp = _pairs(pair_pos, weights, dweights, T, k, dev)
+    check("moe_permute_backward", _launch(dev, stream, lambda s: lib().moe_permute_backward(
+        rp, rs, R, xp, xs, DTYPES[dtype], T, d, k, pp, wp, op, os, dwp, s)))
+    return dx
+
+
+def moe_unpermute_backward_into(dout, pair_pos, k, drows, weights: Optional[torch.Tensor] = None,
+                                rows: Optional[torch.Tensor] = None, dweights: Optional[torch.Tensor] = None,
+                                stream=None):
+    """Gradient of moe_unpermute: drows[pos] = w dout[t]; with rows and dweights also
+    dweights[t, j] = <dout[t], rows[pos]> (0 for dropped pairs).  Rows of drows that no
+    pair names keep their contents."""
+    dtype, dev = _row_type(dout, "dout")
+    if (rows is None) != (dweights is None):
+        raise ValueError("rows and dweights go together")
+    T, d = dout.shape
+    R = drows.shape[0]
+    op, os = _rows(dout, "dout", dtype, T, d, dev)
+    dp, ds = _rows(drows, "drows", dtype, R, d, dev, True)
+    rp, rs = (None, 0) if rows is None else _rows(rows, "rows", dtype, R, d, dev)
+    pp, wp, dwp = _pairs(pair_pos, weights, dweights, T, k, dev)
+    check("moe_unpermute_backward", _launch(dev, stream, lambda s: lib().moe_unpermute_backward(
+        op, os, rp, rs, DTYPES[dtype], T, d, k, pp, wp, dp, ds, R, dwp, s)))
+    return drows
+
+
+def _alloc_on(device, stream):
+    """Context in which allocations belong to the stream that the call runs on."""
+    return torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def moe_permute(x, pair_pos, k, weights=None, stream=None):
+    """Allocating form of moe_permute_into: rows [T*k, d].  Rows behind the last placed
+    pair (there are some when pairs were dropped) are uninitialised."""
+    _row_type(x, "x")
+    with _alloc_on(x.device, stream):
+        rows = torch.empty((x.shape[0] * k, x.shape[1]), dtype=x.dtype, device=x.device)
+    return moe_permute_into(x, pair_pos, k, rows, weights, stream)
+
+
+def moe_unpermute(rows, pair_pos, k, T, weights=None, stream=None):
+    """Allocating form of moe_unpermute_into: out [T, d]."""
+    _row_type(rows, "rows")
+    with _alloc_on(rows.device, stream):
+        out = torch.empty((T, rows.shape[1]), dtype=rows.dtype, device=rows.device)
+    return moe_unpermute_into(rows, pair_pos, k, out, weights, stream)
+
+
+# ---------------------------------------------------------------- router gradient
+
+def route_backward_workspace_bytes(T, d, E, k) -> int:
+    return int(lib().moe_route_backward_workspace_bytes(T, d, E, k))
+
+
+def alloc_route_backward_workspace(T, d, E, k, device) -> torch.Tensor:
+    return torch.empty(max(route_backward_workspace_bytes(T, d, E, k), 256), dtype=torch.uint8, device=device)
+
+
+def moe_route_backward_into(x, w_router, route: RouteOut, dweights, dx: Optional[torch.Tensor],
+                            dw_router: Optional[torch.Tensor], workspace, renormalize=True,
+                            dlogits: Optional[torch.Tensor] = None, dx_add: Optional[torch.Tensor] = None,
+                            stream=None):
+    """Gradient of moe_route from that of its weights, dweights [T, k] float32 (e.g. from
+    moe_unpermute_backward): dx [T, d] bf16 (plus dx_add, which may be dx itself) and
+    dw_router [E, d] float32; either may be None.  dlogits [T, E] float32 adds the
+    gradient of a loss on the logits themselves.  `route` and `renormalize` as moe_route
+    had them."""
+    _row_type(x, "x")
+    dev = x.device
+    T, d = x.shape
+    E, k = w_router.shape[0], route.ids.shape[1]
+    bf, f32 = torch.bfloat16, torch.float32
+    a = _lib.RouteBackwardArgs()
+    a.x, a.w_router = _like(x, "x", bf, (T, d), dev), _like(w_router, "w_router", bf, (E, d), dev)
+    a.T, a.d, a.E, a.k, a.renormalize = T, d, E, k, int(bool(renormalize))
+    a.logits = _like(route.logits, "route.logits", f32, (T, E), dev)
+    a.topk_ids = _like(route.ids, "route.ids", torch.int32, (T, k), dev)
+    a.topk_weights = _like(route.weights, "route.weights", f32, (T, k), dev)
+    a.dweights = _like(dweights, "dweights", f32, (T, k), dev)
+    a.dlogits = None if dlogits is None else _like(dlogits, "dlogits", f32, (T, E), dev)
+    a.dx_add = None if dx_add is None else _like(dx_add, "dx_add", bf, (T, d), dev)
+    a.dx = None if dx is None else _like(dx, "dx", bf, (T, d), dev)
+    a.dw_router = None if dw_router is None else _like(dw_router, "dw_router", f32, (E, d), dev)
+    a.workspace = _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    a.workspace_bytes = workspace.numel()
+    check("moe_route_backward", _launch(dev, stream, lambda s: lib().moe_route_backward(ctypes.byref(a), s)))
+    return dx, dw_router
+
+
+def moe_route_backward(x, w_router, route: RouteOut, dweights, renormalize=True, dlogits=None, dx_add=None,
+                       stream=None):
+    """Allocating form of moe_route_backward_into: (dx, dw_router)."""
+    _row_type(x, "x")
+    (T, d), E = x.shape, w_router.shape[0]
+    with _alloc_on(x.device, stream):
+        dx = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+        dw = torch.empty((E, d), dtype=torch.float32, device=x.device)
+        ws = alloc_route_backward_workspace(T, d, E, route.ids.shape[1], x.device)
+    return moe_route_backward_into(x, w_router, route, dweights, dx, dw, ws, renormalize, dlogits, dx_add, stream)
+
+
+# ---------------------------------------------------------------- norms around a block
+
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+
+
+@dataclass
+class BlockNorm:
+    """Parameters of moe_block_norm (all of the residual stream's type):
+    z = rms(y) norm_out, h = residual_scale x + gate z, n = rms(h) norm_in."""
+    norm_in: Optional[torch.Tensor] = None   # [d] weights of the norm before the next block
+    norm_out: Optional[torch.Tensor] = None  # [d] weights of the norm behind this block
+    gate: Optional[torch.Tensor] = None      # [d] per channel, [T, 1] per token, or [T, d]
+    residual_scale: float = 1.0
+    eps: float = 1e-6
+
+
+@dataclass
+class BlockNormGrads:
+    """Outputs of moe_block_norm_backward; None: not wanted."""
+    dx: Optional[torch.Tensor] = None         # [T, d]
+    dy: Optional[torch.Tensor] = None         # [T, d]
+    dgate: Optional[torch.Tensor] = None      # [d] or [T, 1] float32, or [T, d] of the rows' type
+    dnorm_out: Optional[torch.Tensor] = None  # [d] float32
+    dnorm_in: Optional[torch.Tensor] = None   # [d] float32
+
+
+def _block_norm_args(norm: BlockNorm, x, y):
+    dtype, dev = _row_type(x, "x")
+    T, d = x.shape
+    a = _lib.BlockNormArgs()
+    a.dtype, a.T, a.d = DTYPES[dtype], T, d
+    a.x, a.x_stride = _rows(x, "x", dtype, T, d, dev)
+    if y is not None:
+        a.y, a.y_stride = _rows(y, "y", dtype, T, d, dev)
+    if norm.norm_out is not None:
+        a.norm_out = _like(norm.norm_out, "norm_out", dtype, (d,), dev)
+    if norm.norm_in is not None:
+        a.norm_in = _like(norm.norm_in, "norm_in", dtype, (d,), dev)
+    g = norm.gate
+    if g is not None:
+        if g.dim() == 1:
+            a.gate_kind, a.gate = GATE_CHANNEL, _like(g, "gate", dtype, (d,), dev)
+        elif g.dim() == 2 and g.shape[1] == 1:
+            a.gate_kind = GATE_TOKEN
+            a.gate, a.gate_stride = _rows(g, "gate", dtype, T, 1, dev)
+        else:
+            a.gate_kind = GATE_FULL
+            a.gate, a.gate_stride = _rows(g, "gate", dtype, T, d, dev)
+    a.residual_scale, a.eps = norm.residual_scale, norm.eps
+    return a, dtype, T, d, dev
+
+
+def moe_block_norm_into(norm: BlockNorm, x, y: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                        n: Optional[torch.Tensor] = None, stream=None):
+    """What stands between two blocks, in one pass: h (residual stream behind this block)
+    and n (input of the next one, exactly when norm.norm_in is given); x [T, d] residual
+    stream, y [T, d] this block's output or None.  h may be x or y itself, n may be y."""
+    a, dtype, T, d, dev = _block_norm_args(norm, x, y)
+    hp, hs = (None, 0) if h is None else _rows(h, "h", dtype, T, d, dev, True)
+    np_, ns = (None, 0) if n is None else _rows(n, "n", dtype, T, d, dev, True)
+    check("moe_block_norm", _launch(dev, stream, lambda s: lib().moe_block_norm(ctypes.byref(a), hp, hs, np_, ns, s)))
+    return h, n
+
+
+def moe_block_norm(norm: BlockNorm, x, y: Optional[torch.Tensor] = None, stream=None):
+    """Allocating form of moe_block_norm_into: (h, n).  Without y, h is None where
+    norm.norm_in is given and the residual scale is 1 (h is x then)."""
+    _row_type(x, "x")
+    with _alloc_on(x.device, stream):
+        alone = y is None and norm.norm_in is not None and norm.residual_scale == 1.0
+        h = None if alone else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        n = None if norm.norm_in is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return moe_block_norm_into(norm, x, y, h, n, stream)
+
+
+def block_norm_workspace_bytes(T, d) -> int:
+    return int(lib().moe_block_norm_backward_workspace_bytes(T, d))
+
+
+def alloc_block_norm_workspace(T, d, device) -> torch.Tensor:
+    return torch.empty(max(block_norm_workspace_bytes(T, d), 256), dtype=torch.uint8, device=device)
+
+
+def moe_block_norm_backward_into(norm: BlockNorm, x, y: Optional[torch.Tensor], grads: BlockNormGrads,
+                                 workspace: Optional[torch.Tensor], dh: Optional[torch.Tensor] = None,
+                                 dn: Optional[torch.Tensor] = None, stream=None) -> BlockNormGrads:
+    """Gradient of moe_block_norm from those of h and n (None: zero), on the x and y of
+    the forward call.  dx may be dh itself, dy may be y or dn itself.  The workspace
+    (alloc_block_norm_workspace) is needed for the [d] gradients only."""
+    a, dtype, T, d, dev = _block_norm_args(norm, x, y)
+    g = _lib.BlockNormGradArgs()
+    if dh is not None:
+        g.dh, g.dh_stride = _rows(dh, "dh", dtype, T, d, dev)
+    if dn is not None:
+        g.dn, g.dn_stride = _rows(dn, "dn", dtype, T, d, dev)
+    if grads.dx is not None:
+        g.dx, g.dx_stride = _rows(grads.dx, "dx", dtype, T, d, dev, True)
+    if grads.dy is not None:
+        g.dy, g.dy_stride = _rows(grads.dy, "dy", dtype, T, d, dev, True)
+    f32 = torch.float32
+    if grads.dgate is not None:
+        if a.gate_kind == GATE_FULL:
+            g.dgate, g.dgate_stride = _rows(grads.dgate, "dgate", dtype, T, d, dev, True)
+        else:
+            shape = (d,) if a.gate_kind == GATE_CHANNEL else (T, 1)
+            g.dgate = _like(grads.dgate, "dgate", f32, shape, dev)
+    if grads.dnorm_out is not None:
+        g.dnorm_out = _like(grads.dnorm_out, "dnorm_out", f32, (d,), dev)
+    if grads.dnorm_in is not None:
+        g.dnorm_in = _like(grads.dnorm_in, "dnorm_in", f32, (d,), dev)
+    if workspace is not None:
+        g.workspace = _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
+        g.workspace_bytes = workspace.numel()
+    check("moe_block_norm_backward", _launch(dev, stream, lambda s: lib().moe_block_norm_backward(
+        ctypes.byref(a), ctypes.byref(g), s)))
+    return grads
+
+
+def moe_block_norm_backward(norm: BlockNorm, x, y: Optional[torch.Tensor] = None,
+                            dh: Optional[torch.Tensor] = None, dn: Optional[torch.Tensor] = None,
+                            stream=None) -> BlockNormGrads:
+    """Allocating form of moe_block_norm_backward_into: every gradient there is."""
+    _row_type(x, "x")
+    (T, d), dev = x.shape, x.device
+    with _alloc_on(dev, stream):
+        def vec(p):
+            return None if p is None else torch.empty(d, dtype=torch.float32, device=dev)
+
+        grads = BlockNormGrads(torch.empty(x.shape, dtype=x.dtype, device=dev),
+                               None if y is None else torch.empty(x.shape, dtype=x.dtype, device=dev),
+                               None, vec(norm.norm_out), vec(norm.norm_in))
+        if norm.gate is not None:
+            full = norm.gate.dim() == 2 and norm.gate.shape[1] != 1
+            grads.dgate = torch.empty(norm.gate.shape, dtype=x.dtype if full else torch.float32, device=dev)
+        ws = alloc_block_norm_workspace(T, d, dev)
+    return moe_block_norm_backward_into(norm, x, y, grads, ws, dh, dn, stream)
+
+
 class MoELayer:
     """One W4A16 MoE layer step with preallocated buffers (no allocation per call).
 
@@ -585,7 +941,8 @@ class SlotCache:
 
 KERNELS = {"gateup_decode": 0, "down_decode": 1, "gateup_prefill": 2, "down_prefill": 3, "combine": 4,
            "gateup_bf16": 7, "down_bf16": 8, "gateup_mat": 9, "down_mat": 10,
-           "route": 5, "align": 6}
+           "route": 5, "align": 6, "permute": 11, "unpermute": 12, "route_backward": 13, "block_norm": 14,
+           "block_norm_backward": 15}
 
 
 def timing_enable(on: bool):

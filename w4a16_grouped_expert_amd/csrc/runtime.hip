@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "common.hpp"
+#include "rows.hpp"
 
 namespace moe {
 
@@ -61,12 +62,12 @@ struct TimedLaunch {
 
 static std::mutex g_timing_mu;
 static bool g_timing_on = false;
-static std::vector<TimedLaunch> g_pending[K_NUM];
+static std::vector<TimedLaunch> g_pending[K_NUM_ALL];
 static std::vector<hipEvent_t> g_event_pool;
-static double g_total_ms[K_NUM];
-static int64_t g_launches[K_NUM];
-static int g_open[K_NUM];
-static hipEvent_t g_open_start[K_NUM];
+static double g_total_ms[K_NUM_ALL];
+static int64_t g_launches[K_NUM_ALL];
+static int g_open[K_NUM_ALL];
+static hipEvent_t g_open_start[K_NUM_ALL];
 
 static hipEvent_t pool_get() {
   if (!g_event_pool.empty()) {
@@ -104,7 +105,7 @@ void timing_end(int id, hipStream_t s) {
 }
 
 static void drain_locked() {
-  for (int id = 0; id < K_NUM; ++id) {
+  for (int id = 0; id < K_NUM_ALL; ++id) {
     for (auto& tl : g_pending[id]) {
       (void)hipEventSynchronize(tl.stop);  // on failure the elapsed-time query fails too and the sample is skipped
       float ms = 0.f;
@@ -170,7 +171,7 @@ int moe_timing_enable(int on) {
 int moe_timing_reset(void) {
   std::lock_guard<std::mutex> lk(g_timing_mu);
   drain_locked();
-  for (int i = 0; i < K_NUM; ++i) {
+  for (int i = 0; i < K_NUM_ALL; ++i) {
     g_total_ms[i] = 0;
     g_launches[i] = 0;
   }
@@ -179,7 +180,7 @@ int moe_timing_reset(void) {
 
 int moe_timing_read(int kernel_id, double* total_ms, int64_t* launches) {
   clear_error();
-  MOE_CHECK_ARG(kernel_id >= 0 && kernel_id < K_NUM, MOE_ERR_INVALID_ARG,
+  MOE_CHECK_ARG(kernel_id >= 0 && kernel_id < K_NUM_ALL, MOE_ERR_INVALID_ARG,
                 "moe_timing_read: kernel id %d out of range", kernel_id);
   std::lock_guard<std::mutex> lk(g_timing_mu);
   drain_locked();
