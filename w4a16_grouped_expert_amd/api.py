@@ -787,10 +787,13 @@ class MoELayer:
     """One W4A16 MoE layer step with preallocated buffers (no allocation per call).
 
     forward(x) = moe_route -> moe_align -> moe_w4a16_grouped_ffn on the current stream.
+    block(x) = the whole block around it: norm before (norm_before [d]), forward, and
+    what follows (after, a BlockNorm whose norm_in is the next block's norm before).
     """
 
     def __init__(self, w_router: torch.Tensor, bank: torch.Tensor, I: int, k: int, T_max: int,
-                 mode=MODE_AUTO, renormalize=True):
+                 mode=MODE_AUTO, renormalize=True, norm_before: Optional[torch.Tensor] = None,
+                 after: Optional[BlockNorm] = None):
         self.w_router, self.bank, self.I, self.k, self.mode = w_router, bank, I, k, mode
         self.renormalize = renormalize
         self.E, self.d = w_router.shape
@@ -802,6 +805,13 @@ class MoELayer:
         self.out = torch.empty((T_max, self.d), dtype=torch.bfloat16, device=dev)
         need = max(ffn_workspace_bytes(t, self.d, I, self.E, k, mode) for t in range(1, T_max + 1))
         self.ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        self.after = after
+        self.before = None
+        if after is not None or norm_before is not None:
+            after = self.after = BlockNorm() if after is None else after
+            self.n, self.h, self.n_next = (torch.empty_like(self.out) for _ in range(3))
+            if norm_before is not None:
+                self.before = BlockNorm(norm_in=norm_before, eps=after.eps)
 
     def views(self, T):
         r = RouteOut(self.route.logits[:T], self.route.ids[:T], self.route.weights[:T])
@@ -820,6 +830,25 @@ class MoELayer:
         moe_w4a16_grouped_ffn_into(x, r, a, self.bank, self.I, o, self.ws[:max(ws_need, 256)], self.mode, True,
                                    stream=stream)
         return o
+
+    def block(self, x: torch.Tensor, n: Optional[torch.Tensor] = None, stream=None):
+        """One block on the residual stream x [T, d]: (h, n_next) with y = forward(n) and
+        moe_block_norm's h and n behind it (n_next is None without after.norm_in).  n, if
+        given, is the normed x that the block before returned; else norm_before is
+        applied here.  The results lie in the layer's own buffers, which the next call
+        overwrites; x and n may be another layer's."""
+        if self.after is None:
+            raise ValueError("block needs norm_before or after")
+        T = x.shape[0]
+        if T > self.T_max:
+            raise ValueError(f"T={T} exceeds T_max={self.T_max}")
+        if n is None:
+            if self.before is None:
+                raise ValueError("block needs n or norm_before")
+            _, n = moe_block_norm_into(self.before, x, None, None, self.n[:T], stream)
+        y = self.forward(n, stream=stream)
+        n_next = self.n_next[:T] if self.after.norm_in is not None else None
+        return moe_block_norm_into(self.after, x, y, self.h[:T], n_next, stream)
 
 
 # ---------------------------------------------------------------- slot cache
