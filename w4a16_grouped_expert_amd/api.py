@@ -432,17 +432,19 @@ def moe_w4a16_grouped_ffn(x, route, al, bank, I, mode=MODE_AUTO, slot_of_expert=
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # moe_dtype in w4a16_moe.h
 
 
-def _launch(device, stream, call):
-    """status of call(stream handle), issued with `device` current; the stream defaults
-    to that device's current one."""
+def _launch(fn, device, stream, *args):
+    """fn(*args, stream handle) with `device` current; the stream defaults to that device's
+    current one (whose handle alone is asked for: a Stream object costs 1.6 us a call)."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
     elif stream.device != device:
         raise ValueError(f"stream on {stream.device} for tensors on {device}")
+    else:
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == device.index:
-        return call(stream.cuda_stream)
+        return fn(*args, handle)
     with torch.cuda.device(device):
-        return call(stream.cuda_stream)
+        return fn(*args, handle)
 
 
 def _like(t, name, dtype, shape, device):
@@ -513,8 +515,8 @@ def moe_permute_into(x, pair_pos, k, rows, weights: Optional[torch.Tensor] = Non
     xp, xs = _rows(x, "x", dtype, T, d, dev)
     rp, rs = _rows(rows, "rows", dtype, R, d, dev, True)
     pp, wp, _ = _pairs(pair_pos, weights, None, T, k, dev)
-    check("moe_permute", _launch(dev, stream, lambda s: lib().moe_permute(
-        xp, xs, DTYPES[dtype], T, d, k, pp, wp, rp, rs, R, s)))
+    check("moe_permute", _launch(
+        lib().moe_permute, dev, stream, xp, xs, DTYPES[dtype], T, d, k, pp, wp, rp, rs, R))
     return rows
 
 
@@ -527,8 +529,8 @@ def moe_unpermute_into(rows, pair_pos, k, out, weights: Optional[torch.Tensor] =
     rp, rs = _rows(rows, "rows", dtype, R, d, dev)
     op, os = _rows(out, "out", dtype, T, d, dev, True)
     pp, wp, _ = _pairs(pair_pos, weights, None, T, k, dev)
-    check("moe_unpermute", _launch(dev, stream, lambda s: lib().moe_unpermute(
-        rp, rs, R, DTYPES[dtype], T, d, k, pp, wp, op, os, s)))
+    check("moe_unpermute", _launch(
+        lib().moe_unpermute, dev, stream, rp, rs, R, DTYPES[dtype], T, d, k, pp, wp, op, os))
     return out
 
 
@@ -545,8 +547,8 @@ def moe_permute_backward_into(drows, pair_pos, k, dx, weights: Optional[torch.Te
     op, os = _rows(dx, "dx", dtype, T, d, dev, True)
     xp, xs = (None, 0) if x is None else _rows(x, "x", dtype, T, d, dev)
     pp, wp, dwp = _pairs(pair_pos, weights, dweights, T, k, dev)
-    check("moe_permute_backward", _launch(dev, stream, lambda s: lib().moe_permute_backward(
-        rp, rs, R, xp, xs, DTYPES[dtype], T, d, k, pp, wp, op, os, dwp, s)))
+    check("moe_permute_backward", _launch(
+        lib().moe_permute_backward, dev, stream, rp, rs, R, xp, xs, DTYPES[dtype], T, d, k, pp, wp, op, os, dwp))
     return dx
 
 
@@ -565,8 +567,8 @@ def moe_unpermute_backward_into(dout, pair_pos, k, drows, weights: Optional[torc
     dp, ds = _rows(drows, "drows", dtype, R, d, dev, True)
     rp, rs = (None, 0) if rows is None else _rows(rows, "rows", dtype, R, d, dev)
     pp, wp, dwp = _pairs(pair_pos, weights, dweights, T, k, dev)
-    check("moe_unpermute_backward", _launch(dev, stream, lambda s: lib().moe_unpermute_backward(
-        op, os, rp, rs, DTYPES[dtype], T, d, k, pp, wp, dp, ds, R, dwp, s)))
+    check("moe_unpermute_backward", _launch(
+        lib().moe_unpermute_backward, dev, stream, op, os, rp, rs, DTYPES[dtype], T, d, k, pp, wp, dp, ds, R, dwp))
     return drows
 
 
@@ -629,7 +631,8 @@ def moe_route_backward_into(x, w_router, route: RouteOut, dweights, dx: Optional
     a.dw_router = None if dw_router is None else _like(dw_router, "dw_router", f32, (E, d), dev)
     a.workspace = _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
     a.workspace_bytes = workspace.numel()
-    check("moe_route_backward", _launch(dev, stream, lambda s: lib().moe_route_backward(ctypes.byref(a), s)))
+    check("moe_route_backward", _launch(
+        lib().moe_route_backward, dev, stream, ctypes.byref(a)))
     return dx, dw_router
 
 
@@ -705,7 +708,8 @@ def moe_block_norm_into(norm: BlockNorm, x, y: Optional[torch.Tensor] = None, h:
     a, dtype, T, d, dev = _block_norm_args(norm, x, y)
     hp, hs = (None, 0) if h is None else _rows(h, "h", dtype, T, d, dev, True)
     np_, ns = (None, 0) if n is None else _rows(n, "n", dtype, T, d, dev, True)
-    check("moe_block_norm", _launch(dev, stream, lambda s: lib().moe_block_norm(ctypes.byref(a), hp, hs, np_, ns, s)))
+    check("moe_block_norm", _launch(
+        lib().moe_block_norm, dev, stream, ctypes.byref(a), hp, hs, np_, ns))
     return h, n
 
 
@@ -758,8 +762,8 @@ def moe_block_norm_backward_into(norm: BlockNorm, x, y: Optional[torch.Tensor], 
     if workspace is not None:
         g.workspace = _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
         g.workspace_bytes = workspace.numel()
-    check("moe_block_norm_backward", _launch(dev, stream, lambda s: lib().moe_block_norm_backward(
-        ctypes.byref(a), ctypes.byref(g), s)))
+    check("moe_block_norm_backward", _launch(
+        lib().moe_block_norm_backward, dev, stream, ctypes.byref(a), ctypes.byref(g)))
     return grads
 
 

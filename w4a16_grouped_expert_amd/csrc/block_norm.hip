@@ -33,22 +33,8 @@ struct NormDev {
   const void *dh, *dn;
   void *dx, *dy, *dgate;
   int64_t dh_stride, dn_stride, dx_stride, dy_stride, dgate_stride;
-  float* part;  // [workgroup][3][d]: sums for v_out, v_in and the channel gate; or null
+  float* part;  // [workgroup][2][d]: column sums for v_out and gate, and for v_in; or null
 };
-
-// sum of v over the workgroup, in every thread
-__device__ __forceinline__ float block_sum(float v, float* lds) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  const int waves = blockDim.x >> 6;
-  if (waves == 1) return v;
-  __syncthreads();  // the last sum has been read
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < waves; ++w) s += lds[w];
-  return s;
-}
 
 template <typename S>
 __device__ __forceinline__ const S* row_ptr(const void* p, int64_t t, int64_t stride) {
@@ -59,206 +45,363 @@ __device__ __forceinline__ S* row_ptr(void* p, int64_t t, int64_t stride) {
   return static_cast<S*>(p) + t * stride;
 }
 
-template <typename S, int R>
-__global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a) {
-  __shared__ float lds[kNormMaxThreads / 64];
-  const int64_t t = blockIdx.x;
+// How the threads of a workgroup share rows: `slots` rows at a time, each by 1 << lt lanes of a wavefront or by `waves` whole wavefronts.
+struct NormSplit {
+  int lt, waves, slots, threads, pieces;
+};
+
+// sums over the threads of a row, in each of them.  Rows of several wavefronts meet in
+// LDS; the caller alternates between two buffers, so that one barrier is enough: a
+// wavefront that writes a buffer again has passed the barrier of the other one, which
+// every wavefront reaches after it has read the first.
+template <int K>
+__device__ __forceinline__ void row_sums(float (&v)[K], const NormSplit& p, float* buf) {
+#pragma unroll
+  for (int i = 0; i < K; ++i) v[i] = lane_sum(v[i], p.lt);
+  if (p.waves == 1) return;
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int i = 0; i < K; ++i) buf[wave * 8 + i] = v[i];
+  __syncthreads();
+  const int first = wave - wave % p.waves;
+#pragma unroll
+  for (int i = 0; i < K; ++i) v[i] = 0.f;
+  for (int w = first; w < first + p.waves; ++w)
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] += buf[w * 8 + i];
+}
+
+// Which row and lane of it a thread is.
+struct RowLane {
+  int slot, lane, lanes;
+};
+// kSub: rows by parts of wavefronts; else a wavefront has one row, whose number and
+// addresses stay in scalar registers.
+template <bool kSub>
+__device__ __forceinline__ RowLane row_lane(const NormSplit& p) {
+  if (kSub) return {(int)threadIdx.x >> p.lt, (int)threadIdx.x & ((1 << p.lt) - 1), 1 << p.lt};
+  const int slot = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) / p.waves);
+  return {slot, (int)threadIdx.x - slot * p.waves * 64, p.waves * 64};
+}
+
+template <typename S>
+__device__ __forceinline__ Raw<S> ones() {
+  float v[kPiece];
+#pragma unroll
+  for (int i = 0; i < kPiece; ++i) v[i] = 1.f;
+  return pack<S>(v);
+}
+
+template <typename S>
+__device__ __forceinline__ Raw<S> masked(Raw<S> r, uint32_t mask) {
+#pragma unroll
+  for (int q = 0; q < (int)(sizeof(r.w) / sizeof(r.w[0])); ++q) r.w[q] &= mask;
+  return r;
+}
+
+template <typename S, int R, bool kSub>
+__global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormSplit p) {
+  __shared__ float lds[2][kNormMaxThreads / 64 * 8];
+  const RowLane rl = row_lane<kSub>(p);
+  const int64_t t = (int64_t)blockIdx.x * p.slots + rl.slot;
+  const bool live = t < a.T;
+  const int64_t tc = live ? t : a.T - 1;
+  const bool channel = a.gate_kind == MOE_GATE_CHANNEL, full = a.gate_kind == MOE_GATE_FULL;
   float h[R][kPiece], z[R][kPiece];
-  float ss = 0.f;
+  Piece c[R];
+  Raw<S> vo[R], vi[R], vg[R];
+  float ss[1] = {0.f};
+  // every load of the row before its first use
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int c = (r * blockDim.x + threadIdx.x) * kPiece, n = a.d - c;
-    if (n <= 0) continue;
-    load_piece(row_ptr<S>(a.x, t, a.x_stride) + c, n, h[r]);
-    if (a.y) load_piece(row_ptr<S>(a.y, t, a.y_stride) + c, n, z[r]);
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) {
-      h[r][i] *= a.scale;
-      if (a.y) ss = fmaf(z[r][i], z[r][i], ss);
-    }
+    c[r] = piece_of((r * rl.lanes + rl.lane) * kPiece, a.d);
+    if (!live) c[r].skip = kPiece;
+    const Raw<S> x = load_raw<kSub>(row_ptr<S>(a.x, tc, a.x_stride), c[r], a.d);
+    unpack<S>(x, h[r]);
+    if (a.y) load_piece<kSub>(row_ptr<S>(a.y, tc, a.y_stride), c[r], a.d, z[r]);
+    vo[r] = vg[r] = vi[r] = ones<S>();
+    if (a.v_out) vo[r] = load_raw<kSub>(static_cast<const S*>(a.v_out), c[r], a.d);
+    if (channel || full)
+      vg[r] = load_raw<kSub>(full ? row_ptr<S>(a.gate, tc, a.gate_stride) : static_cast<const S*>(a.gate), c[r], a.d);
+    if (a.v_in) vi[r] = load_raw<kSub>(static_cast<const S*>(a.v_in), c[r], a.d);
   }
-  const float ry = a.v_out ? rsqrtf(block_sum(ss, lds) / a.d + a.eps) : 1.f;
-  const float gt = a.gate_kind == MOE_GATE_TOKEN ? to_f32(*row_ptr<S>(a.gate, t, a.gate_stride)) : 1.f;
-  float hh = 0.f;
+  const float gt = a.gate_kind == MOE_GATE_TOKEN ? to_f32(*row_ptr<S>(a.gate, tc, a.gate_stride)) : 1.f;
+  float hh[1] = {0.f};
+  if (a.y) {
+    float ry = 1.f;
+    if (a.v_out) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) ss[0] = fmaf(z[r][i], z[r][i], ss[0]);
+      row_sums(ss, p, lds[0]);
+      ry = rsqrtf(ss[0] / a.d + a.eps);
+    }
+    ry *= gt;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float v[kPiece], g[kPiece];
+      unpack<S>(vo[r], v);
+      unpack<S>(vg[r], g);
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) h[r][i] = fmaf(ry * z[r][i], v[i] * g[i], a.scale * h[r][i]);
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) h[r][i] *= a.scale;
+  }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int c = (r * blockDim.x + threadIdx.x) * kPiece, n = a.d - c;
-    if (n <= 0) continue;
-    if (a.y) {
-      float v[kPiece], g[kPiece];
-      if (a.v_out) load_piece(static_cast<const S*>(a.v_out) + c, n, v);
-      if (a.gate_kind == MOE_GATE_CHANNEL) load_piece(static_cast<const S*>(a.gate) + c, n, g);
-      if (a.gate_kind == MOE_GATE_FULL) load_piece(row_ptr<S>(a.gate, t, a.gate_stride) + c, n, g);
+    if (a.h) store_piece<kSub>(row_ptr<S>(a.h, tc, a.h_stride), c[r], a.d, h[r]);
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) {
-        const float zi = a.v_out ? z[r][i] * ry * v[i] : z[r][i];
-        const float gi = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL ? g[i] : gt;
-        h[r][i] = fmaf(gi, zi, h[r][i]);
-      }
-    }
-    if (a.h) store_piece(row_ptr<S>(a.h, t, a.h_stride) + c, n, h[r]);
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) hh = fmaf(h[r][i], h[r][i], hh);
+    for (int i = 0; i < kPiece; ++i) hh[0] = fmaf(h[r][i], h[r][i], hh[0]);
   }
   if (!a.v_in) return;
-  const float rh = rsqrtf(block_sum(hh, lds) / a.d + a.eps);
+  row_sums(hh, p, lds[1]);
+  const float rh = rsqrtf(hh[0] / a.d + a.eps);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int c = (r * blockDim.x + threadIdx.x) * kPiece, n = a.d - c;
-    if (n <= 0) continue;
     float v[kPiece];
-    load_piece(static_cast<const S*>(a.v_in) + c, n, v);
+    unpack<S>(vi[r], v);
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) v[i] *= h[r][i] * rh;
-    store_piece(row_ptr<S>(a.n, t, a.n_stride) + c, n, v);
+    for (int i = 0; i < kPiece; ++i) v[i] *= rh * h[r][i];
+    store_piece<kSub>(row_ptr<S>(a.n, tc, a.n_stride), c[r], a.d, v);
   }
 }
 
-template <typename S, int R>
-__global__ __launch_bounds__(kNormMaxThreads) void k_block_norm_backward(NormDev a) {
-  __shared__ float lds[kNormMaxThreads / 64];
-  float sum_out[R][kPiece], sum_in[R][kPiece], sum_gate[R][kPiece];
+// The rows of the gradient, in registers: what the next row needs is requested before
+// the arithmetic of the current one.  D = dh + r_h (u - mean(u hn) r_h h) is linear in
+// dh, u and h, and with q = g v_out y (g the channel or full gate) the sum over q D that
+// dy and a token's gate need is the same combination of the sums over q dh, q u and q h:
+// so a row takes two rounds of sums (y^2, then the other
+// five) and not four, each of which would wait for the one before.
+// Column sums: only A = sum over rows of D yn (g D yn for a token's or full gate) and
+// B = that of dn hn are kept; dnorm_out and a channel gate's gradient are A times the
+// channel gate and v_out.
+// What a call leaves out is read from a tensor that it has and masked to zero (v_out and
+// the channel gate: ones), so that no load sits under a branch; only a full gate, a
+// fifth stream, has a kernel of its own.
+template <typename S, int R, int kThreads, bool kSub, bool kFull>
+__global__ __launch_bounds__(kThreads, kThreads == 512 && R == 1 ? 4 : 1) void k_block_norm_backward(NormDev a,
+                                                                                                      NormSplit p) {
+  __shared__ float lds[kThreads * kPiece];
+  const RowLane rl = row_lane<kSub>(p);
+  const void* dh_in = a.dh ? a.dh : a.dn;
+  const void* dn_in = a.dn ? a.dn : a.dh;
+  const void* x_in = a.dn ? a.x : dh_in;
+  const void* y_in = a.y ? a.y : x_in;
+  const int64_t dh_ld = a.dh ? a.dh_stride : a.dn_stride, dn_ld = a.dn ? a.dn_stride : a.dh_stride;
+  const int64_t x_ld = a.dn ? a.x_stride : dh_ld, y_ld = a.y ? a.y_stride : x_ld;
+  const uint32_t dh_on = a.dh ? ~0u : 0u, dn_on = a.dn ? ~0u : 0u, y_on = a.y ? ~0u : 0u;
+  float A[R][kPiece], B[R][kPiece];
+  float W[R][kPiece], V[R][kPiece];  // v_out times the channel gate; v_in
+  Piece c[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int r = 0; r < R; ++r) {
+    c[r] = piece_of((r * rl.lanes + rl.lane) * kPiece, a.d);
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) sum_out[r][i] = sum_in[r][i] = sum_gate[r][i] = 0.f;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    float h[R][kPiece], y[R][kPiece], D[R][kPiece], u[R][kPiece], v[R][kPiece], g[R][kPiece];
-    const float gt = a.gate_kind == MOE_GATE_TOKEN ? to_f32(*row_ptr<S>(a.gate, t, a.gate_stride)) : 1.f;
-    float ss = 0.f;
+    for (int i = 0; i < kPiece; ++i) {
+      A[r][i] = B[r][i] = 0.f;
+      W[r][i] = V[r][i] = 1.f;
+    }
+    if (a.v_out) load_piece<kSub>(static_cast<const S*>(a.v_out), c[r], a.d, W[r]);
+    if (a.v_in) load_piece<kSub>(static_cast<const S*>(a.v_in), c[r], a.d, V[r]);
+    if (a.gate_kind == MOE_GATE_CHANNEL) {
+      float g[kPiece];
+      load_piece<kSub>(static_cast<const S*>(a.gate), c[r], a.d, g);
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) W[r][i] *= g[i];
+    }
+  }
+  Raw<S> rx[R], ry_[R], rh_[R], rn[R], rg[R];
+  auto request = [&](int64_t t) {
+    const int64_t tc = t < a.T ? t : a.T - 1;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int c = (r * blockDim.x + threadIdx.x) * kPiece, n = a.d - c;
+      Piece q = c[r];
+      if (t >= a.T) q.skip = kPiece;
+      ry_[r] = load_raw<kSub>(row_ptr<S>(y_in, tc, y_ld), q, a.d);
+      rx[r] = load_raw<kSub>(row_ptr<S>(x_in, tc, x_ld), q, a.d);
+      rn[r] = load_raw<kSub>(row_ptr<S>(dn_in, tc, dn_ld), q, a.d);
+      rh_[r] = load_raw<kSub>(row_ptr<S>(dh_in, tc, dh_ld), q, a.d);
+      if (kFull) rg[r] = load_raw<kSub>(row_ptr<S>(a.gate, tc, a.gate_stride), q, a.d);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * p.slots;
+  const int64_t rounds = (a.T + step - 1) / step;
+  int64_t t = (int64_t)blockIdx.x * p.slots + rl.slot;
+  request(t);
+  for (int64_t it = 0; it < rounds; ++it, t += step) {
+    const bool live = t < a.T;
+    const int64_t tc = live ? t : a.T - 1;
+    Raw<S> x[R], y[R], dh[R], dn[R], g[R];
+    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // y y; then h h, u h, q dh, q u, q h
+    float f[kPiece], e[kPiece];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      x[r] = masked<S>(rx[r], dn_on);
+      y[r] = masked<S>(ry_[r], y_on);
+      dh[r] = masked<S>(rh_[r], dh_on);
+      dn[r] = masked<S>(rn[r], dn_on);
+      if (kFull) g[r] = rg[r];
+      unpack<S>(y[r], f);
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) s[0] = fmaf(f[i], f[i], s[0]);
+    }
+    const float gt = a.gate_kind == MOE_GATE_TOKEN ? to_f32(*row_ptr<S>(a.gate, tc, a.gate_stride)) : 1.f;
+    request(t + step);
+    float ry = 1.f;
+    if (a.v_out) {
+      float sy[1] = {s[0]};
+      row_sums(sy, p, lds);
+      ry = rsqrtf(sy[0] / a.d + a.eps);
+    }
+    float h[R][kPiece], q[R][kPiece], u[R][kPiece], D[R][kPiece];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      unpack<S>(y[r], q[r]);
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) q[r][i] *= W[r][i];
+      if (kFull) {
+        unpack<S>(g[r], e);
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) q[r][i] *= e[i];
+      }
+      unpack<S>(x[r], h[r]);
+      unpack<S>(dn[r], u[r]);
+      unpack<S>(dh[r], D[r]);
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
-        h[r][i] = y[r][i] = D[r][i] = u[r][i] = 0.f;
-        v[r][i] = 1.f;
-        g[r][i] = gt;
+        h[r][i] = fmaf(gt * ry, q[r][i], a.scale * h[r][i]);
+        u[r][i] *= V[r][i];
+        s[1] = fmaf(h[r][i], h[r][i], s[1]);
+        s[2] = fmaf(u[r][i], h[r][i], s[2]);
+        s[3] = fmaf(q[r][i], D[r][i], s[3]);
+        s[4] = fmaf(q[r][i], u[r][i], s[4]);
+        s[5] = fmaf(q[r][i], h[r][i], s[5]);
       }
-      if (n <= 0) continue;
-      load_piece(row_ptr<S>(a.x, t, a.x_stride) + c, n, h[r]);
-      if (a.y) load_piece(row_ptr<S>(a.y, t, a.y_stride) + c, n, y[r]);
-      if (a.dh) load_piece(row_ptr<S>(a.dh, t, a.dh_stride) + c, n, D[r]);
-      if (a.dn) load_piece(row_ptr<S>(a.dn, t, a.dn_stride) + c, n, u[r]);
-      if (a.v_out) load_piece(static_cast<const S*>(a.v_out) + c, n, v[r]);
-      if (a.gate_kind == MOE_GATE_CHANNEL) load_piece(static_cast<const S*>(a.gate) + c, n, g[r]);
-      if (a.gate_kind == MOE_GATE_FULL) load_piece(row_ptr<S>(a.gate, t, a.gate_stride) + c, n, g[r]);
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i) ss = fmaf(y[r][i], y[r][i], ss);
     }
-    const float ry = a.v_out ? rsqrtf(block_sum(ss, lds) / a.d + a.eps) : 1.f;
-    if (a.dn) {
-      float hh = 0.f;
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) {
-          const float z = y[r][i] * ry * v[r][i];
-          h[r][i] = fmaf(g[r][i], z, a.scale * h[r][i]);
-          hh = fmaf(h[r][i], h[r][i], hh);
-        }
-      const float rh = rsqrtf(block_sum(hh, lds) / a.d + a.eps);
-      float m = 0.f;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int c = (r * blockDim.x + threadIdx.x) * kPiece, n = a.d - c;
-        if (n <= 0) continue;
-        float w[kPiece];
-        load_piece(static_cast<const S*>(a.v_in) + c, n, w);
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) {
-          h[r][i] *= rh;
-          sum_in[r][i] = fmaf(u[r][i], h[r][i], sum_in[r][i]);
-          u[r][i] *= w[i];
-          m = fmaf(u[r][i], h[r][i], m);
-        }
-      }
-      m = block_sum(m, lds) / a.d;
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) D[r][i] = fmaf(rh, u[r][i] - h[r][i] * m, D[r][i]);
+    float rh = 0.f, mh = 0.f, qD = 0.f;
+    if (a.dn || a.y) {
+      float sum[5] = {s[1], s[2], s[3], s[4], s[5]};
+      row_sums(sum, p, lds + kThreads / 64 * 8);
+      rh = a.dn ? rsqrtf(sum[0] / a.d + a.eps) : 0.f;
+      mh = rh * (sum[1] / a.d);  // mean(u hn)
+      qD = sum[2] + rh * (sum[3] - mh * (rh * sum[4]));
     }
-    float m = 0.f, dg = 0.f;
+    // mean(g v_out D yn).  (Factors 1 / rms go with the sum or the element that they
+    // scale, one at a time: their cube leaves float32's range for rows of size 1e13.)
+    const float my = a.v_out ? gt * (ry * (qD / a.d)) : 0.f;
+    if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && live && rl.lane == 0) static_cast<float*>(a.dgate)[t] = ry * qD;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int c = (r * blockDim.x + threadIdx.x) * kPiece, n = a.d - c;
-      if (n <= 0) continue;
-      float o[kPiece];
-      if (a.dx) {
+      Piece w = c[r];
+      if (!live) w.skip = kPiece;
+      unpack<S>(dn[r], f);
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) o[i] = a.scale * D[r][i];
-        store_piece(row_ptr<S>(a.dx, t, a.dx_stride) + c, n, o);
+      for (int i = 0; i < kPiece; ++i) {
+        const float hn = rh * h[r][i];
+        B[r][i] = fmaf(f[i], hn, B[r][i]);
+        D[r][i] += rh * (u[r][i] - mh * hn);
+        f[i] = a.scale * D[r][i];
       }
+      if (a.dx) store_piece<kSub>(row_ptr<S>(a.dx, tc, a.dx_stride), w, a.d, f);
       if (!a.y) continue;
+      unpack<S>(y[r], e);
+      float k[kPiece];
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
-        y[r][i] *= ry;
-        o[i] = D[r][i] * y[r][i] * v[r][i];
-        dg += o[i];
-        if (a.gate_kind == MOE_GATE_CHANNEL) sum_gate[r][i] += o[i];
-        D[r][i] *= g[r][i];
-        sum_out[r][i] = fmaf(D[r][i], y[r][i], sum_out[r][i]);
-        D[r][i] *= v[r][i];
-        m = fmaf(D[r][i], y[r][i], m);
+        f[i] = W[r][i] * D[r][i];  // without the full or the token's gate
+        e[i] *= ry;
+        k[i] = gt;
       }
-      if (a.gate_kind == MOE_GATE_FULL && a.dgate) store_piece(row_ptr<S>(a.dgate, t, a.dgate_stride) + c, n, o);
-    }
-    if (!a.y) continue;
-    if (a.gate_kind == MOE_GATE_TOKEN && a.dgate) {
-      dg = block_sum(dg, lds);
-      if (threadIdx.x == 0) static_cast<float*>(a.dgate)[t] = dg;
-    }
-    if (!a.dy) continue;
-    m = a.v_out ? block_sum(m, lds) / a.d : 0.f;
+      if (kFull) {
+        if (a.dgate) {
+          float o[kPiece];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int c = (r * blockDim.x + threadIdx.x) * kPiece, n = a.d - c;
-      if (n <= 0) continue;
+          for (int i = 0; i < kPiece; ++i) o[i] = f[i] * e[i];
+          store_piece<kSub>(row_ptr<S>(a.dgate, tc, a.dgate_stride), w, a.d, o);
+        }
+        unpack<S>(g[r], k);
+      }
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) D[r][i] = ry * (D[r][i] - y[r][i] * m);
-      store_piece(row_ptr<S>(a.dy, t, a.dy_stride) + c, n, D[r]);
+      for (int i = 0; i < kPiece; ++i) {
+        A[r][i] = fmaf(k[i] * D[r][i], e[i], A[r][i]);
+        f[i] = ry * (k[i] * f[i] - my * e[i]);
+      }
+      if (a.dy) store_piece<kSub>(row_ptr<S>(a.dy, tc, a.dy_stride), w, a.d, f);
     }
   }
   if (!a.part) return;
+  // the slots' column sums, in slot order
+  float* out = a.part + (int64_t)blockIdx.x * 2 * a.d;
+  const int width = rl.lanes * kPiece;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int c = (r * blockDim.x + threadIdx.x) * kPiece, n = a.d - c;
-    if (n <= 0) continue;
-    float* p = a.part + (int64_t)blockIdx.x * 3 * a.d + c;
-    store_piece(p, n, sum_out[r]);
-    store_piece(p + a.d, n, sum_in[r]);
-    store_piece(p + 2 * (int64_t)a.d, n, sum_gate[r]);
-  }
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i)
+        if (i >= c[r].skip && (!kSub || c[r].at + i < a.d))
+          lds[rl.slot * width + c[r].at + i - r * width] = k == 0 ? A[r][i] : B[r][i];
+      __syncthreads();
+      for (int j = threadIdx.x; j < width && r * width + j < a.d; j += blockDim.x) {
+        float v = 0.f;
+        for (int g = 0; g < p.slots; ++g) v += lds[g * width + j];
+        out[k * (int64_t)a.d + r * width + j] = v;
+      }
+    }
 }
 
-// column sums of the workgroups' partial sums; blockIdx.y picks the vector
-__global__ __launch_bounds__(256) void k_norm_vectors(const float* part, int groups, int d, float* dv_out,
-                                                      float* dv_in, float* dgate) {
-  float* out = blockIdx.y == 0 ? dv_out : blockIdx.y == 1 ? dv_in : dgate;
-  if (!out) return;
-  __shared__ float lds[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
-  float s = 0.f;
-  if (c < d)
-    for (int g = wave; g < groups; g += 4) s += part[((int64_t)g * 3 + blockIdx.y) * d + c];
-  lds[wave][lane] = s;
+// the [d] gradients: column sums over the workgroups, 32 columns of A (blockIdx.y = 0)
+// or B by 32 rows of threads
+template <typename S>
+__global__ __launch_bounds__(1024) void k_norm_vectors(const float* part, int groups, NormDev a, float* dv_out,
+                                                       float* dv_in, float* dgate) {
+  __shared__ float lds[32][33];
+  const int x = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + x;
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (c < a.d)
+    for (int g = row; g < groups; g += 256)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (g + 32 * i < groups) s[i] += part[((int64_t)(g + 32 * i) * 2 + blockIdx.y) * a.d + c];
+  lds[row][x] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
   __syncthreads();
-  if (wave == 0 && c < d) out[c] = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
+  if (row != 0 || c >= a.d) return;
+  float v = 0.f;
+  for (int r = 0; r < 32; ++r) v += lds[r][x];
+  if (blockIdx.y == 1) {
+    if (dv_in) dv_in[c] = v;
+    return;
+  }
+  if (dgate) dgate[c] = a.v_out ? v * to_f32(static_cast<const S*>(a.v_out)[c]) : v;
+  if (dv_out) dv_out[c] = a.gate_kind == MOE_GATE_CHANNEL ? v * to_f32(static_cast<const S*>(a.gate)[c]) : v;
 }
 
-// workgroups of the gradient: enough for every CU, few enough that their partial sums
-// stay small beside the rows
-static int norm_groups(int T) { return (int)std::min<int64_t>(T, 1024); }
+// `target` threads per workgroup, more where one row needs them
+static NormSplit norm_split(int d, int target) {
+  NormSplit p;
+  const int pieces = (int)ceil_div(d, kPiece);
+  p.pieces = pieces <= 512 ? 1 : 2;
+  const int lanes = (int)ceil_div(pieces, p.pieces);
+  p.lt = 0;
+  while (p.lt < 6 && (1 << p.lt) < lanes) ++p.lt;
+  p.waves = (int)ceil_div(lanes, 64);
+  p.slots = p.waves > 1 ? std::max(1, target / (64 * p.waves)) : target >> p.lt;
+  p.threads = p.waves > 1 ? p.slots * 64 * p.waves : target;
+  return p;
+}
 
-struct NormShape {
-  int threads, pieces;  // pieces of 8 elements per thread: 1 or 2
-};
-static NormShape norm_shape(int d) {
-  const int lanes = (int)ceil_div(d, kPiece);
-  if (lanes <= kNormMaxThreads) return {(int)ceil_div(lanes, 64) * 64, 1};
-  return {kNormMaxThreads, 2};
+// workgroups of the gradient: two per CU, few enough that their column sums stay small
+// beside the rows
+static int norm_groups(int T, int d) {
+  return (int)std::min<int64_t>(ceil_div(T, norm_split(d, 512).slots), 512);
 }
 
 static int check_norm(const char* fn, const moe_block_norm_args* a) {
@@ -333,14 +476,17 @@ extern "C" int moe_block_norm(const moe_block_norm_args* a, void* h, int64_t h_s
   v.n = n;
   v.n_stride = n_stride;
   hipStream_t s = (hipStream_t)stream;
-  const NormShape sh = norm_shape(a->d);
+  const NormSplit p = norm_split(a->d, 256);
+  const dim3 grid((unsigned)ceil_div(a->T, p.slots));
   timing_begin(K_BLOCK_NORM, s);
   with_dtype(a->dtype, [&](auto e) {
     using S = decltype(e);
-    if (sh.pieces == 1)
-      hipLaunchKernelGGL((k_block_norm<S, 1>), dim3((unsigned)a->T), dim3(sh.threads), 0, s, v);
+    if (p.lt < 6)
+      hipLaunchKernelGGL((k_block_norm<S, 1, true>), grid, dim3(p.threads), 0, s, v, p);
+    else if (p.pieces == 1)
+      hipLaunchKernelGGL((k_block_norm<S, 1, false>), grid, dim3(p.threads), 0, s, v, p);
     else
-      hipLaunchKernelGGL((k_block_norm<S, 2>), dim3((unsigned)a->T), dim3(sh.threads), 0, s, v);
+      hipLaunchKernelGGL((k_block_norm<S, 2, false>), grid, dim3(p.threads), 0, s, v, p);
   });
   timing_end(K_BLOCK_NORM, s);
   return check_launch(fn);
@@ -348,7 +494,7 @@ extern "C" int moe_block_norm(const moe_block_norm_args* a, void* h, int64_t h_s
 
 extern "C" int64_t moe_block_norm_backward_workspace_bytes(int T, int d) {
   if (T < 0 || d <= 0) return -1;
-  return (int64_t)norm_groups(T) * 3 * d * 4;
+  return (int64_t)norm_groups(T, d) * 2 * d * 4;
 }
 
 extern "C" int moe_block_norm_backward(const moe_block_norm_args* a, const moe_block_norm_grads* g, void* stream) {
@@ -394,20 +540,34 @@ extern "C" int moe_block_norm_backward(const moe_block_norm_args* a, const moe_b
   v.dgate_stride = g->dgate_stride;
   v.part = vectors ? static_cast<float*>(g->workspace) : nullptr;
   hipStream_t s = (hipStream_t)stream;
-  const NormShape sh = norm_shape(a->d);
-  const int groups = norm_groups(a->T);
+  const NormSplit p = norm_split(a->d, 512);
+  const int groups = norm_groups(a->T, a->d);
   timing_begin(K_BLOCK_NORM_BWD, s);
-  if (a->T > 0)
-    with_dtype(a->dtype, [&](auto e) {
-      using S = decltype(e);
-      if (sh.pieces == 1)
-        hipLaunchKernelGGL((k_block_norm_backward<S, 1>), dim3(groups), dim3(sh.threads), 0, s, v);
+  with_dtype(a->dtype, [&](auto e) {
+    using S = decltype(e);
+    if (a->T > 0) {
+      auto go = [&](auto pieces, auto threads, auto sub) {
+        constexpr int R = decltype(pieces)::value, B = decltype(threads)::value;
+        constexpr bool kSub = decltype(sub)::value;
+        if (a->gate_kind == MOE_GATE_FULL)
+          hipLaunchKernelGGL((k_block_norm_backward<S, R, B, kSub, true>), dim3(groups), dim3(p.threads), 0, s, v, p);
+        else
+          hipLaunchKernelGGL((k_block_norm_backward<S, R, B, kSub, false>), dim3(groups), dim3(p.threads), 0, s, v, p);
+      };
+      using std::integral_constant;
+      if (p.lt < 6)
+        go(integral_constant<int, 1>{}, integral_constant<int, 512>{}, std::true_type{});
+      else if (p.pieces == 1)
+        go(integral_constant<int, 1>{}, integral_constant<int, 512>{}, std::false_type{});
+      else if (p.threads <= 512)
+        go(integral_constant<int, 2>{}, integral_constant<int, 512>{}, std::false_type{});
       else
-        hipLaunchKernelGGL((k_block_norm_backward<S, 2>), dim3(groups), dim3(sh.threads), 0, s, v);
-    });
-  if (vectors)
-    hipLaunchKernelGGL(k_norm_vectors, dim3((unsigned)ceil_div(a->d, 64), 3), dim3(256), 0, s, v.part, groups, a->d,
-                       g->dnorm_out, g->dnorm_in, dgate_vec);
+        go(integral_constant<int, 2>{}, integral_constant<int, 1024>{}, std::false_type{});
+    }
+    if (vectors)
+      hipLaunchKernelGGL(k_norm_vectors<S>, dim3((unsigned)ceil_div(a->d, 32), 2), dim3(1024), 0, s, v.part, groups, v,
+                         g->dnorm_out, g->dnorm_in, dgate_vec);
+  });
   timing_end(K_BLOCK_NORM_BWD, s);
   return check_launch(fn);
 }

@@ -26,14 +26,8 @@ struct PermuteDev {
   float* dweights;        // products only
 };
 
-// Sum over the 1 << lt lanes of a token's group.
-__device__ __forceinline__ float group_sum(float v, int lt) {
-  for (int m = 1; m < (1 << lt); m <<= 1) v += __shfl_xor(v, m);
-  return v;
-}
-
 // One group of 1 << lt lanes per token (lt <= 6), 64 >> lt tokens per wavefront.
-template <typename S, bool kProducts>
+template <typename S, bool kProducts, bool kTiny>
 __global__ __launch_bounds__(256) void k_spread(PermuteDev a, int lt) {
   const int lane = threadIdx.x & ((1 << lt) - 1);
   const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lt;
@@ -44,8 +38,8 @@ __global__ __launch_bounds__(256) void k_spread(PermuteDev a, int lt) {
 #pragma unroll
   for (int j = 0; j < MOE_MAX_TOPK; ++j) dot[j] = 0.f;
   for (int c = lane * kPiece; c < a.d; c += kPiece << lt) {
-    const int n = a.d - c;
-    const Raw<S> raw = load_raw(src + c, n);
+    const Piece n = piece_of(c, a.d);
+    const Raw<S> raw = load_raw<kTiny>(src, n, a.d);
     float v[kPiece];
     unpack<S>(raw, v);
 #pragma unroll
@@ -54,32 +48,32 @@ __global__ __launch_bounds__(256) void k_spread(PermuteDev a, int lt) {
       if (!live || pos < 0 || pos >= a.num_rows) continue;
       if constexpr (kProducts) {
         float r[kPiece];
-        load_piece(static_cast<const S*>(a.sorted_in) + pos * a.sorted_in_stride + c, n, r);
+        load_piece<kTiny>(static_cast<const S*>(a.sorted_in) + pos * a.sorted_in_stride, n, a.d, r);
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) dot[j] = fmaf(v[i], r[i], dot[j]);
       }
-      S* dst = static_cast<S*>(a.out) + pos * a.out_stride + c;
+      S* dst = static_cast<S*>(a.out) + pos * a.out_stride;
       if (a.weights) {
         const float w = a.weights[tc * a.k + j];
         float o[kPiece];
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) o[i] = w * v[i];
-        store_piece(dst, n, o);
+        store_piece<kTiny>(dst, n, a.d, o);
       } else {
-        store_raw(dst, raw, n);
+        store_raw<kTiny>(dst, n, a.d, raw);
       }
     }
   }
   if constexpr (kProducts) {
 #pragma unroll
     for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-      const float s = group_sum(dot[j], lt);
+      const float s = lane_sum(dot[j], lt);
       if (live && lane == 0 && j < a.k) a.dweights[t * a.k + j] = s;
     }
   }
 }
 
-template <typename S, bool kProducts>
+template <typename S, bool kProducts, bool kTiny>
 __global__ __launch_bounds__(256) void k_gather(PermuteDev a, int lt) {
   const int lane = threadIdx.x & ((1 << lt) - 1);
   const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lt;
@@ -89,31 +83,31 @@ __global__ __launch_bounds__(256) void k_gather(PermuteDev a, int lt) {
 #pragma unroll
   for (int j = 0; j < MOE_MAX_TOPK; ++j) dot[j] = 0.f;
   for (int c = lane * kPiece; c < a.d; c += kPiece << lt) {
-    const int n = a.d - c;
+    const Piece n = piece_of(c, a.d);
     float v[kPiece], acc[kPiece];
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) acc[i] = 0.f;
     if constexpr (kProducts)
-      load_piece(static_cast<const S*>(a.token_in) + tc * a.token_in_stride + c, n, v);
+      load_piece<kTiny>(static_cast<const S*>(a.token_in) + tc * a.token_in_stride, n, a.d, v);
 #pragma unroll
     for (int j = 0; j < MOE_MAX_TOPK; ++j) {
       const int64_t pos = j < a.k ? a.pair_pos[tc * a.k + j] : -1;
       if (!live || pos < 0 || pos >= a.num_rows) continue;
       const float w = a.weights ? a.weights[tc * a.k + j] : 1.f;
       float r[kPiece];
-      load_piece(static_cast<const S*>(a.sorted_in) + pos * a.sorted_in_stride + c, n, r);
+      load_piece<kTiny>(static_cast<const S*>(a.sorted_in) + pos * a.sorted_in_stride, n, a.d, r);
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
         acc[i] = fmaf(w, r[i], acc[i]);
         if constexpr (kProducts) dot[j] = fmaf(v[i], r[i], dot[j]);
       }
     }
-    if (live) store_piece(static_cast<S*>(a.out) + t * a.out_stride + c, n, acc);
+    if (live) store_piece<kTiny>(static_cast<S*>(a.out) + t * a.out_stride, n, a.d, acc);
   }
   if constexpr (kProducts) {
 #pragma unroll
     for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-      const float s = group_sum(dot[j], lt);
+      const float s = lane_sum(dot[j], lt);
       if (live && lane == 0 && j < a.k) a.dweights[t * a.k + j] = s;
     }
   }
@@ -133,17 +127,18 @@ static int launch_rows(const char* name, int timing_id, bool spread, int dtype, 
   timing_begin(timing_id, s);
   with_dtype(dtype, [&](auto v) {
     using S = decltype(v);
-    if (spread) {
-      if (products)
-        hipLaunchKernelGGL((k_spread<S, true>), grid, dim3(256), 0, s, a, lt);
+    auto go = [&](auto prod, auto tiny) {
+      constexpr bool kP = decltype(prod)::value, kT = decltype(tiny)::value;
+      if (spread)
+        hipLaunchKernelGGL((k_spread<S, kP, kT>), grid, dim3(256), 0, s, a, lt);
       else
-        hipLaunchKernelGGL((k_spread<S, false>), grid, dim3(256), 0, s, a, lt);
-    } else {
-      if (products)
-        hipLaunchKernelGGL((k_gather<S, true>), grid, dim3(256), 0, s, a, lt);
-      else
-        hipLaunchKernelGGL((k_gather<S, false>), grid, dim3(256), 0, s, a, lt);
-    }
+        hipLaunchKernelGGL((k_gather<S, kP, kT>), grid, dim3(256), 0, s, a, lt);
+    };
+    const bool tiny = a.d < kPiece;
+    if (products)
+      tiny ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+    else
+      tiny ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
   });
   timing_end(timing_id, s);
   return check_launch(name);

@@ -38,50 +38,80 @@ __device__ __forceinline__ void from_f32(bf16_row_t* p, float v) { p->bits = (ui
 __device__ __forceinline__ void from_f32(_Float16* p, float v) { *p = (_Float16)v; }
 __device__ __forceinline__ void from_f32(float* p, float v) { *p = v; }
 
-// elements [0, n) of a piece of which n are in the row; the rest reads as zero
-template <typename S>
-__device__ __forceinline__ Raw<S> load_raw(const S* p, int n) {
+// Where a lane's eight elements of a row of d lie.  The last piece of a row whose length
+// is no multiple of 8 starts at d - 8, so that every load is one of eight elements inside
+// the row and none sits under a branch; its first `skip` elements belong to the piece
+// before and read as zero.  A lane past the end skips all eight.  kTiny: rows of fewer than
+// eight elements too (at = 0), element by element; kernels take it for short rows only.
+struct Piece {
+  int at, skip;
+};
+__device__ __forceinline__ Piece piece_of(int col, int d) {
+  const int at = col + kPiece <= d ? col : d > kPiece ? d - kPiece : 0;
+  return {at, col - at < kPiece ? col - at : kPiece};
+}
+
+template <bool kTiny, typename S>
+__device__ __forceinline__ Raw<S> load_raw(const S* row, const Piece& p, int d) {
   Raw<S> r;
-  if (n >= kPiece) {
+  if (!kTiny || d >= kPiece) {
+    const S* q = row + p.at;
     if constexpr (sizeof(S) == 2) {
-      r.w[0] = *reinterpret_cast<const u32x4_a2_t*>(p);
+      r.w[0] = *reinterpret_cast<const u32x4_a2_t*>(q);
     } else {
-      r.w[0] = *reinterpret_cast<const u32x4_a4_t*>(p);
-      r.w[1] = *reinterpret_cast<const u32x4_a4_t*>(p + 4);
+      r.w[0] = *reinterpret_cast<const u32x4_a4_t*>(q);
+      r.w[1] = *reinterpret_cast<const u32x4_a4_t*>(q + 4);
     }
   } else {
-    if constexpr (sizeof(S) == 2) {
-      uint32_t h[kPiece];
+    uint32_t h[kPiece];
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) h[i] = i < n ? reinterpret_cast<const uint16_t*>(p)[i] : 0u;
+    for (int i = 0; i < kPiece; ++i) {
+      const int e = i < d ? i : 0;
+      if constexpr (sizeof(S) == 2)
+        h[i] = reinterpret_cast<const uint16_t*>(row)[e];
+      else
+        h[i] = reinterpret_cast<const uint32_t*>(row)[e];
+      h[i] = i < d ? h[i] : 0u;
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r.w[0][i] = h[2 * i] | (h[2 * i + 1] << 16);
-    } else {
+    for (int i = 0; i < kPiece; ++i) {
+      if constexpr (sizeof(S) == 2)
+        r.w[0][i >> 1] = (i & 1) ? r.w[0][i >> 1] | (h[i] << 16) : h[i];
+      else
+        r.w[i >> 2][i & 3] = h[i];
+    }
+  }
+  if (p.skip) {
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) r.w[i >> 2][i & 3] = i < n ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
+    for (int i = 0; i < kPiece; ++i) {
+      if constexpr (sizeof(S) == 2)
+        r.w[0][i >> 1] &= i < p.skip ? ((i & 1) ? 0x0000FFFFu : 0xFFFF0000u) : 0xFFFFFFFFu;
+      else
+        r.w[i >> 2][i & 3] = i < p.skip ? 0u : r.w[i >> 2][i & 3];
     }
   }
   return r;
 }
 
-template <typename S>
-__device__ __forceinline__ void store_raw(S* p, const Raw<S>& r, int n) {
-  if (n >= kPiece) {
+template <bool kTiny, typename S>
+__device__ __forceinline__ void store_raw(S* row, const Piece& p, int d, const Raw<S>& r) {
+  if (p.skip == 0 && (!kTiny || d >= kPiece)) {
+    S* q = row + p.at;
     if constexpr (sizeof(S) == 2) {
-      *reinterpret_cast<u32x4_a2_t*>(p) = r.w[0];
+      *reinterpret_cast<u32x4_a2_t*>(q) = r.w[0];
     } else {
-      *reinterpret_cast<u32x4_a4_t*>(p) = r.w[0];
-      *reinterpret_cast<u32x4_a4_t*>(p + 4) = r.w[1];
+      *reinterpret_cast<u32x4_a4_t*>(q) = r.w[0];
+      *reinterpret_cast<u32x4_a4_t*>(q + 4) = r.w[1];
     }
-  } else {
+    return;
+  }
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) {
-      if constexpr (sizeof(S) == 2) {
-        if (i < n) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(r.w[0][i >> 1] >> (16 * (i & 1)));
-      } else {
-        if (i < n) reinterpret_cast<uint32_t*>(p)[i] = r.w[i >> 2][i & 3];
-      }
-    }
+  for (int i = 0; i < kPiece; ++i) {
+    if (i < p.skip || (kTiny && p.at + i >= d)) continue;
+    if constexpr (sizeof(S) == 2)
+      reinterpret_cast<uint16_t*>(row)[p.at + i] = (uint16_t)(r.w[0][i >> 1] >> (16 * (i & 1)));
+    else
+      reinterpret_cast<uint32_t*>(row)[p.at + i] = r.w[i >> 2][i & 3];
   }
 }
 
@@ -118,13 +148,40 @@ __device__ __forceinline__ Raw<S> pack(const float (&v)[kPiece]) {
   return r;
 }
 
-template <typename S>
-__device__ __forceinline__ void load_piece(const S* p, int n, float (&v)[kPiece]) {
-  unpack<S>(load_raw(p, n), v);
+template <bool kTiny, typename S>
+__device__ __forceinline__ void load_piece(const S* row, const Piece& p, int d, float (&v)[kPiece]) {
+  unpack<S>(load_raw<kTiny>(row, p, d), v);
 }
-template <typename S>
-__device__ __forceinline__ void store_piece(S* p, int n, const float (&v)[kPiece]) {
-  store_raw(p, pack<S>(v), n);
+template <bool kTiny, typename S>
+__device__ __forceinline__ void store_piece(S* row, const Piece& p, int d, const float (&v)[kPiece]) {
+  store_raw<kTiny>(row, p, d, pack<S>(v));
+}
+
+template <int kCtrl>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xF, 0xF, true));
+}
+
+// Sum over groups of 1 << lt lanes (lt uniform, 0..6), the same bits in each of its
+// lanes: both sides of every step add the same two values.  One vector instruction for
+// each of the first four steps (lane ^ 1, ^ 2, and mirrors within 8 and 16 lanes), a swap
+// of rows of 16 or halves of 32 and an addition for the last two.
+__device__ __forceinline__ float lane_sum(float v, int lt) {
+  if (lt > 0) v = add_dpp<0xB1>(v);   // quad_perm 1,0,3,2
+  if (lt > 1) v = add_dpp<0x4E>(v);   // quad_perm 2,3,0,1
+  if (lt > 2) v = add_dpp<0x141>(v);  // row_half_mirror
+  if (lt > 3) v = add_dpp<0x140>(v);  // row_mirror
+  if (lt > 4) {
+    const uint32_t b = __float_as_uint(v);
+    const u32x2_t s = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane16_swap(b, b, false, false));
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  if (lt > 5) {
+    const uint32_t b = __float_as_uint(v);
+    const u32x2_t s = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(b, b, false, false));
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  return v;
 }
 
 // Calls f with a value of the row type of `dtype` (checked by the caller).
