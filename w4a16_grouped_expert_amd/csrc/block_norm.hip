@@ -25,7 +25,7 @@ struct NormDev {
   const void *x, *y, *v_out, *v_in, *gate;
   int64_t x_stride, y_stride, gate_stride;
   int gate_kind, T, d;
-  float scale, eps;
+  float scale, eps, inv_d;
   // forward
   void *h, *n;
   int64_t h_stride, n_stride;
@@ -36,13 +36,25 @@ struct NormDev {
   float* part;  // [workgroup][2][d]: column sums for v_out and gate, and for v_in; or null
 };
 
-template <typename S>
+// Row t of a tensor.  A wavefront with one row keeps its address in scalar registers, as
+// the base that 32-bit lane offsets add to: without the asm the compiler adds the lane's
+// offset to the tensor's address first, two vector registers per tensor and piece.
+template <typename S, bool kSub>
 __device__ __forceinline__ const S* row_ptr(const void* p, int64_t t, int64_t stride) {
-  return static_cast<const S*>(p) + t * stride;
+  const S* r = static_cast<const S*>(p) + t * stride;
+  if (!kSub) asm("" : "+s"(r));
+  return r;
 }
-template <typename S>
+template <typename S, bool kSub>
 __device__ __forceinline__ S* row_ptr(void* p, int64_t t, int64_t stride) {
-  return static_cast<S*>(p) + t * stride;
+  S* r = static_cast<S*>(p) + t * stride;
+  if (!kSub) asm("" : "+s"(r));
+  return r;
+}
+
+template <typename S, bool kSub>
+__device__ __forceinline__ float token_gate(const NormDev& a, int64_t t) {
+  return a.gate_kind == MOE_GATE_TOKEN ? load_one(row_ptr<S, kSub>(a.gate, t, a.gate_stride)) : 1.f;
 }
 
 // How the threads of a workgroup share rows: `slots` rows at a time, each by 1 << lt lanes of a wavefront or by `waves` whole wavefronts.
@@ -54,11 +66,11 @@ struct NormSplit {
 // LDS; the caller alternates between two buffers, so that one barrier is enough: a
 // wavefront that writes a buffer again has passed the barrier of the other one, which
 // every wavefront reaches after it has read the first.
-template <int K>
+template <bool kSub, int K>
 __device__ __forceinline__ void row_sums(float (&v)[K], const NormSplit& p, float* buf) {
 #pragma unroll
-  for (int i = 0; i < K; ++i) v[i] = lane_sum(v[i], p.lt);
-  if (p.waves == 1) return;
+  for (int i = 0; i < K; ++i) v[i] = lane_sum(v[i], kSub ? p.lt : 6);
+  if (kSub || p.waves == 1) return;
   const int wave = threadIdx.x >> 6;
   if ((threadIdx.x & 63) == 0)
 #pragma unroll
@@ -100,6 +112,13 @@ __device__ __forceinline__ Raw<S> masked(Raw<S> r, uint32_t mask) {
   return r;
 }
 
+// The same values, unknown to the compiler.
+template <typename S>
+__device__ __forceinline__ void forget(Raw<S>& r) {
+#pragma unroll
+  for (int q = 0; q < (int)(sizeof(r.w) / sizeof(r.w[0])); ++q) asm volatile("" : "+v"(r.w[q]) : : "memory");
+}
+
 template <typename S, int R, bool kSub>
 __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormSplit p) {
   __shared__ float lds[2][kNormMaxThreads / 64 * 8];
@@ -110,23 +129,31 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL, full = a.gate_kind == MOE_GATE_FULL;
   float h[R][kPiece], z[R][kPiece];
   Piece c[R];
-  Raw<S> vo[R], vi[R], vg[R];
+  Raw<S> rx[R], ry_[R], vo[R], vi[R], vg[R];
   float ss[1] = {0.f};
   // every load of the row before its first use
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     c[r] = piece_of((r * rl.lanes + rl.lane) * kPiece, a.d);
     if (!live) c[r].skip = kPiece;
-    const Raw<S> x = load_raw<kSub>(row_ptr<S>(a.x, tc, a.x_stride), c[r], a.d);
-    unpack<S>(x, h[r]);
-    if (a.y) load_piece<kSub>(row_ptr<S>(a.y, tc, a.y_stride), c[r], a.d, z[r]);
+    rx[r] = load_raw<kSub>(row_ptr<S, kSub>(a.x, tc, a.x_stride), c[r], a.d);
+    if (a.y) ry_[r] = load_raw<kSub>(row_ptr<S, kSub>(a.y, tc, a.y_stride), c[r], a.d);
     vo[r] = vg[r] = vi[r] = ones<S>();
     if (a.v_out) vo[r] = load_raw<kSub>(static_cast<const S*>(a.v_out), c[r], a.d);
     if (channel || full)
-      vg[r] = load_raw<kSub>(full ? row_ptr<S>(a.gate, tc, a.gate_stride) : static_cast<const S*>(a.gate), c[r], a.d);
+      vg[r] = load_raw<kSub>(full ? row_ptr<S, kSub>(a.gate, tc, a.gate_stride) : static_cast<const S*>(a.gate), c[r], a.d);
     if (a.v_in) vi[r] = load_raw<kSub>(static_cast<const S*>(a.v_in), c[r], a.d);
   }
-  const float gt = a.gate_kind == MOE_GATE_TOKEN ? to_f32(*row_ptr<S>(a.gate, tc, a.gate_stride)) : 1.f;
+  const float gt = token_gate<S, kSub>(a, tc);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    mask_piece(rx[r], c[r]);
+    unpack<S>(rx[r], h[r]);
+    if (a.y) {
+      mask_piece(ry_[r], c[r]);
+      unpack<S>(ry_[r], z[r]);
+    }
+  }
   float hh[1] = {0.f};
   if (a.y) {
     float ry = 1.f;
@@ -135,8 +162,8 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) ss[0] = fmaf(z[r][i], z[r][i], ss[0]);
-      row_sums(ss, p, lds[0]);
-      ry = rsqrtf(ss[0] / a.d + a.eps);
+      row_sums<kSub>(ss, p, lds[0]);
+      ry = rsqrtf(ss[0] * a.inv_d + a.eps);
     }
     ry *= gt;
 #pragma unroll
@@ -155,39 +182,48 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    if (a.h) store_piece<kSub>(row_ptr<S>(a.h, tc, a.h_stride), c[r], a.d, h[r]);
+    if (a.h) store_piece<kSub>(row_ptr<S, kSub>(a.h, tc, a.h_stride), c[r], a.d, h[r]);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) hh[0] = fmaf(h[r][i], h[r][i], hh[0]);
   }
   if (!a.v_in) return;
-  row_sums(hh, p, lds[1]);
-  const float rh = rsqrtf(hh[0] / a.d + a.eps);
+  row_sums<kSub>(hh, p, lds[1]);
+  const float rh = rsqrtf(hh[0] * a.inv_d + a.eps);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     float v[kPiece];
     unpack<S>(vi[r], v);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) v[i] *= rh * h[r][i];
-    store_piece<kSub>(row_ptr<S>(a.n, tc, a.n_stride), c[r], a.d, v);
+    store_piece<kSub>(row_ptr<S, kSub>(a.n, tc, a.n_stride), c[r], a.d, v);
   }
 }
 
-// The rows of the gradient, in registers: what the next row needs is requested before
-// the arithmetic of the current one.  D = dh + r_h (u - mean(u hn) r_h h) is linear in
-// dh, u and h, and with q = g v_out y (g the channel or full gate) the sum over q D that
-// dy and a token's gate need is the same combination of the sums over q dh, q u and q h:
-// so a row takes two rounds of sums (y^2, then the other
-// five) and not four, each of which would wait for the one before.
+// The gradient.  D = dh + r_h (u - mean(u hn) r_h h) is linear in dh, u and h, and with
+// q = g v_out y (g the channel or full gate) the sum over q D that dy and a token's gate
+// need is the same combination of the sums over q dh, q u and q h: so a row takes two
+// rounds of sums (y^2, then the other five) and not four, each of which would wait for
+// the one before.
+//
+// A row belongs to one wavefront up to 2048 elements (R pieces per lane), so that its
+// sums need no barrier and the wavefronts of a CU drift apart: some load while others
+// compute.  Only the row as loaded and the column sums stay in registers; h, u and q are
+// computed again for the outputs, v_out times the channel gate (W) and v_in (V) come
+// from LDS.
 // Column sums: only A = sum over rows of D yn (g D yn for a token's or full gate) and
 // B = that of dn hn are kept; dnorm_out and a channel gate's gradient are A times the
 // channel gate and v_out.
-// What a call leaves out is read from a tensor that it has and masked to zero (v_out and
-// the channel gate: ones), so that no load sits under a branch; only a full gate, a
-// fifth stream, has a kernel of its own.
-template <typename S, int R, int kThreads, bool kSub, bool kFull>
-__global__ __launch_bounds__(kThreads, kThreads == 512 && R == 1 ? 4 : 1) void k_block_norm_backward(NormDev a,
-                                                                                                      NormSplit p) {
-  __shared__ float lds[kThreads * kPiece];
+// What a call leaves out is read from a tensor that it has and masked to zero, so that no
+// load sits under a branch; only a full gate, a fifth stream, has a kernel of its own.
+//
+// Wavefronts per workgroup, one workgroup per CU: what the registers of a row of `bytes`
+// per element and R pieces allow.
+constexpr int norm_back_waves(int bytes, int R) { return R == 1 ? 16 : R == 2 && bytes == 2 ? 12 : 8; }
+
+template <typename S, int R, bool kSub, bool kFull>
+__global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_norm_backward(NormDev a, NormSplit p) {
+  __shared__ float sums[2][16 * 8];
+  extern __shared__ f32x4_t vec[];  // [W, V][R][half][lanes]: four elements of a lane's piece each
   const RowLane rl = row_lane<kSub>(p);
   const void* dh_in = a.dh ? a.dh : a.dn;
   const void* dn_in = a.dn ? a.dn : a.dh;
@@ -195,166 +231,221 @@ __global__ __launch_bounds__(kThreads, kThreads == 512 && R == 1 ? 4 : 1) void k
   const void* y_in = a.y ? a.y : x_in;
   const int64_t dh_ld = a.dh ? a.dh_stride : a.dn_stride, dn_ld = a.dn ? a.dn_stride : a.dh_stride;
   const int64_t x_ld = a.dn ? a.x_stride : dh_ld, y_ld = a.y ? a.y_stride : x_ld;
-  const uint32_t dh_on = a.dh ? ~0u : 0u, dn_on = a.dn ? ~0u : 0u, y_on = a.y ? ~0u : 0u;
+  const uint32_t dh_on = __builtin_amdgcn_readfirstlane(a.dh ? ~0u : 0u);
+  const uint32_t dn_on = __builtin_amdgcn_readfirstlane(a.dn ? ~0u : 0u);
+  const uint32_t y_on = __builtin_amdgcn_readfirstlane(a.y ? ~0u : 0u);
   float A[R][kPiece], B[R][kPiece];
-  float W[R][kPiece], V[R][kPiece];  // v_out times the channel gate; v_in
   Piece c[R];
+  auto vec_at = [&](int k, int r, int half) -> f32x4_t& { return vec[((k * R + r) * 2 + half) * rl.lanes + rl.lane]; };
+  auto vec_put = [&](int k, int r, const float (&v)[kPiece]) {
+    vec_at(k, r, 0) = f32x4_t{v[0], v[1], v[2], v[3]};
+    vec_at(k, r, 1) = f32x4_t{v[4], v[5], v[6], v[7]};
+  };
+  auto vec_get = [&](int k, int r, float (&v)[kPiece]) {
+    const f32x4_t lo = vec_at(k, r, 0), hi = vec_at(k, r, 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = lo[i];
+      v[4 + i] = hi[i];
+    }
+  };
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     c[r] = piece_of((r * rl.lanes + rl.lane) * kPiece, a.d);
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) {
-      A[r][i] = B[r][i] = 0.f;
-      W[r][i] = V[r][i] = 1.f;
-    }
-    if (a.v_out) load_piece<kSub>(static_cast<const S*>(a.v_out), c[r], a.d, W[r]);
-    if (a.v_in) load_piece<kSub>(static_cast<const S*>(a.v_in), c[r], a.d, V[r]);
-    if (a.gate_kind == MOE_GATE_CHANNEL) {
-      float g[kPiece];
-      load_piece<kSub>(static_cast<const S*>(a.gate), c[r], a.d, g);
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i) W[r][i] *= g[i];
-    }
+    for (int i = 0; i < kPiece; ++i) A[r][i] = B[r][i] = 0.f;
   }
-  Raw<S> rx[R], ry_[R], rh_[R], rn[R], rg[R];
-  auto request = [&](int64_t t) {
-    const int64_t tc = t < a.T ? t : a.T - 1;
+  if (rl.slot == 0) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      Piece q = c[r];
-      if (t >= a.T) q.skip = kPiece;
-      ry_[r] = load_raw<kSub>(row_ptr<S>(y_in, tc, y_ld), q, a.d);
-      rx[r] = load_raw<kSub>(row_ptr<S>(x_in, tc, x_ld), q, a.d);
-      rn[r] = load_raw<kSub>(row_ptr<S>(dn_in, tc, dn_ld), q, a.d);
-      rh_[r] = load_raw<kSub>(row_ptr<S>(dh_in, tc, dh_ld), q, a.d);
-      if (kFull) rg[r] = load_raw<kSub>(row_ptr<S>(a.gate, tc, a.gate_stride), q, a.d);
+      float v[kPiece], w[kPiece];
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) v[i] = w[i] = 1.f;
+      if (a.v_out) load_piece<kSub>(static_cast<const S*>(a.v_out), c[r], a.d, w);
+      if (a.v_in) load_piece<kSub>(static_cast<const S*>(a.v_in), c[r], a.d, v);
+      if (a.gate_kind == MOE_GATE_CHANNEL) {
+        float g[kPiece];
+        load_piece<kSub>(static_cast<const S*>(a.gate), c[r], a.d, g);
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) w[i] *= g[i];
+      }
+      vec_put(0, r, w);
+      vec_put(1, r, v);
     }
-  };
+  }
+  __syncthreads();
   const int64_t step = (int64_t)gridDim.x * p.slots;
   const int64_t rounds = (a.T + step - 1) / step;
   int64_t t = (int64_t)blockIdx.x * p.slots + rl.slot;
-  request(t);
   for (int64_t it = 0; it < rounds; ++it, t += step) {
     const bool live = t < a.T;
     const int64_t tc = live ? t : a.T - 1;
     Raw<S> x[R], y[R], dh[R], dn[R], g[R];
-    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // y y; then h h, u h, q dh, q u, q h
-    float f[kPiece], e[kPiece];
+#pragma unroll
+    for (int r = 0; r < R; ++r) y[r] = load_raw<kSub>(row_ptr<S, kSub>(y_in, tc, y_ld), c[r], a.d);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      x[r] = masked<S>(rx[r], dn_on);
-      y[r] = masked<S>(ry_[r], y_on);
-      dh[r] = masked<S>(rh_[r], dh_on);
-      dn[r] = masked<S>(rn[r], dn_on);
-      if (kFull) g[r] = rg[r];
+      x[r] = load_raw<kSub>(row_ptr<S, kSub>(x_in, tc, x_ld), c[r], a.d);
+      dn[r] = load_raw<kSub>(row_ptr<S, kSub>(dn_in, tc, dn_ld), c[r], a.d);
+      dh[r] = load_raw<kSub>(row_ptr<S, kSub>(dh_in, tc, dh_ld), c[r], a.d);
+      if (kFull) g[r] = load_raw<kSub>(row_ptr<S, kSub>(a.gate, tc, a.gate_stride), c[r], a.d);
+    }
+    const float gt = token_gate<S, kSub>(a, tc);
+    float sy[1] = {0.f};
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      Piece w = c[r];
+      if (!live) w.skip = kPiece;
+      mask_piece(y[r], w);
+      y[r] = masked<S>(y[r], y_on);
+      float f[kPiece];
       unpack<S>(y[r], f);
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) s[0] = fmaf(f[i], f[i], s[0]);
+      for (int i = 0; i < kPiece; ++i) sy[0] = fmaf(f[i], f[i], sy[0]);
     }
-    const float gt = a.gate_kind == MOE_GATE_TOKEN ? to_f32(*row_ptr<S>(a.gate, tc, a.gate_stride)) : 1.f;
-    request(t + step);
     float ry = 1.f;
     if (a.v_out) {
-      float sy[1] = {s[0]};
-      row_sums(sy, p, lds);
-      ry = rsqrtf(sy[0] / a.d + a.eps);
+      row_sums<kSub>(sy, p, sums[0]);
+      ry = rsqrtf(sy[0] * a.inv_d + a.eps);
     }
-    float h[R][kPiece], q[R][kPiece], u[R][kPiece], D[R][kPiece];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      unpack<S>(y[r], q[r]);
+    for (int r = 0; r < R; ++r) forget(y[r]);
+    // the piece's h, u and q
+    auto piece = [&](int r, float (&h)[kPiece], float (&u)[kPiece], float (&q)[kPiece]) {
+      float w[kPiece];
+      unpack<S>(y[r], q);
+      vec_get(0, r, w);
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) q[r][i] *= W[r][i];
+      for (int i = 0; i < kPiece; ++i) q[i] *= w[i];
       if (kFull) {
-        unpack<S>(g[r], e);
+        unpack<S>(g[r], w);
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) q[r][i] *= e[i];
+        for (int i = 0; i < kPiece; ++i) q[i] *= w[i];
       }
-      unpack<S>(x[r], h[r]);
-      unpack<S>(dn[r], u[r]);
-      unpack<S>(dh[r], D[r]);
+      unpack<S>(x[r], h);
+      unpack<S>(dn[r], u);
+      vec_get(1, r, w);
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
-        h[r][i] = fmaf(gt * ry, q[r][i], a.scale * h[r][i]);
-        u[r][i] *= V[r][i];
-        s[1] = fmaf(h[r][i], h[r][i], s[1]);
-        s[2] = fmaf(u[r][i], h[r][i], s[2]);
-        s[3] = fmaf(q[r][i], D[r][i], s[3]);
-        s[4] = fmaf(q[r][i], u[r][i], s[4]);
-        s[5] = fmaf(q[r][i], h[r][i], s[5]);
+        h[i] = fmaf(gt * ry, q[i], a.scale * h[i]);
+        u[i] *= w[i];
       }
+    };
+    float s[5] = {0.f, 0.f, 0.f, 0.f, 0.f};  // h h, u h, q dh, q u, q h
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      Piece w = c[r];
+      if (!live) w.skip = kPiece;
+      mask_piece(x[r], w);
+      mask_piece(dn[r], w);
+      mask_piece(dh[r], w);
+      if (kFull) mask_piece(g[r], w);
+      x[r] = masked<S>(x[r], dn_on);
+      dn[r] = masked<S>(dn[r], dn_on);
+      dh[r] = masked<S>(dh[r], dh_on);
+      float h[kPiece], u[kPiece], q[kPiece], D[kPiece];
+      piece(r, h, u, q);
+      unpack<S>(dh[r], D);
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) {
+        s[0] = fmaf(h[i], h[i], s[0]);
+        s[1] = fmaf(u[i], h[i], s[1]);
+        s[2] = fmaf(q[i], D[i], s[2]);
+        s[3] = fmaf(q[i], u[i], s[3]);
+        s[4] = fmaf(q[i], h[i], s[4]);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one piece at a time: its floats are many registers
     }
     float rh = 0.f, mh = 0.f, qD = 0.f;
     if (a.dn || a.y) {
-      float sum[5] = {s[1], s[2], s[3], s[4], s[5]};
-      row_sums(sum, p, lds + kThreads / 64 * 8);
-      rh = a.dn ? rsqrtf(sum[0] / a.d + a.eps) : 0.f;
-      mh = rh * (sum[1] / a.d);  // mean(u hn)
-      qD = sum[2] + rh * (sum[3] - mh * (rh * sum[4]));
+      row_sums<kSub>(s, p, sums[1]);
+      rh = a.dn ? rsqrtf(s[0] * a.inv_d + a.eps) : 0.f;
+      mh = rh * (s[1] * a.inv_d);  // mean(u hn)
+      qD = s[2] + rh * (s[3] - mh * (rh * s[4]));
     }
     // mean(g v_out D yn).  (Factors 1 / rms go with the sum or the element that they
     // scale, one at a time: their cube leaves float32's range for rows of size 1e13.)
-    const float my = a.v_out ? gt * (ry * (qD / a.d)) : 0.f;
+    const float my = a.v_out ? gt * (ry * (qD * a.inv_d)) : 0.f;
+    // (as far as the compiler can see the row changes here, as y does above: it would keep
+    // the floats of every piece, 3 x 8 R registers, in place of computing them again)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      forget(x[r]);
+      forget(y[r]);
+      forget(dn[r]);
+      forget(dh[r]);
+      if (kFull) forget(g[r]);
+    }
     if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && live && rl.lane == 0) static_cast<float*>(a.dgate)[t] = ry * qD;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       Piece w = c[r];
       if (!live) w.skip = kPiece;
+      float h[kPiece], u[kPiece], D[kPiece], f[kPiece], e[kPiece];
+      piece(r, h, u, f);
       unpack<S>(dn[r], f);
+      unpack<S>(dh[r], D);
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
-        const float hn = rh * h[r][i];
+        const float hn = rh * h[i];
         B[r][i] = fmaf(f[i], hn, B[r][i]);
-        D[r][i] += rh * (u[r][i] - mh * hn);
-        f[i] = a.scale * D[r][i];
+        D[i] += rh * (u[i] - mh * hn);
+        f[i] = a.scale * D[i];
       }
-      if (a.dx) store_piece<kSub>(row_ptr<S>(a.dx, tc, a.dx_stride), w, a.d, f);
-      if (!a.y) continue;
-      unpack<S>(y[r], e);
-      float k[kPiece];
+      if (a.dx) store_piece<kSub>(row_ptr<S, kSub>(a.dx, tc, a.dx_stride), w, a.d, f);
+      if (a.y) {
+        unpack<S>(y[r], e);
+        vec_get(0, r, u);
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) {
-        f[i] = W[r][i] * D[r][i];  // without the full or the token's gate
-        e[i] *= ry;
-        k[i] = gt;
-      }
-      if (kFull) {
-        if (a.dgate) {
-          float o[kPiece];
-#pragma unroll
-          for (int i = 0; i < kPiece; ++i) o[i] = f[i] * e[i];
-          store_piece<kSub>(row_ptr<S>(a.dgate, tc, a.dgate_stride), w, a.d, o);
+        for (int i = 0; i < kPiece; ++i) {
+          f[i] = u[i] * D[i];  // without the full or the token's gate
+          e[i] *= ry;
+          h[i] = gt;
         }
-        unpack<S>(g[r], k);
-      }
+        if (kFull) {
+          if (a.dgate) {
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) {
-        A[r][i] = fmaf(k[i] * D[r][i], e[i], A[r][i]);
-        f[i] = ry * (k[i] * f[i] - my * e[i]);
+            for (int i = 0; i < kPiece; ++i) u[i] = f[i] * e[i];
+            store_piece<kSub>(row_ptr<S, kSub>(a.dgate, tc, a.dgate_stride), w, a.d, u);
+          }
+          unpack<S>(g[r], h);
+        }
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) {
+          A[r][i] = fmaf(h[i] * D[i], e[i], A[r][i]);
+          f[i] = ry * (h[i] * f[i] - my * e[i]);
+        }
+        if (a.dy) store_piece<kSub>(row_ptr<S, kSub>(a.dy, tc, a.dy_stride), w, a.d, f);
       }
-      if (a.dy) store_piece<kSub>(row_ptr<S>(a.dy, tc, a.dy_stride), w, a.d, f);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   if (!a.part) return;
-  // the slots' column sums, in slot order
-  float* out = a.part + (int64_t)blockIdx.x * 2 * a.d;
-  const int width = rl.lanes * kPiece;
+  // the slots' column sums, one slot after the other
+  for (int s = 0; s < p.slots; ++s) {
+    __syncthreads();
+    if (rl.slot != s) continue;
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) {
+      if (s > 0) {
+        float v[kPiece];
+        vec_get(0, r, v);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      __syncthreads();
+        for (int i = 0; i < kPiece; ++i) A[r][i] += v[i];
+        vec_get(1, r, v);
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i)
-        if (i >= c[r].skip && (!kSub || c[r].at + i < a.d))
-          lds[rl.slot * width + c[r].at + i - r * width] = k == 0 ? A[r][i] : B[r][i];
-      __syncthreads();
-      for (int j = threadIdx.x; j < width && r * width + j < a.d; j += blockDim.x) {
-        float v = 0.f;
-        for (int g = 0; g < p.slots; ++g) v += lds[g * width + j];
-        out[k * (int64_t)a.d + r * width + j] = v;
+        for (int i = 0; i < kPiece; ++i) B[r][i] += v[i];
+      }
+      if (s + 1 < p.slots) {
+        vec_put(0, r, A[r]);
+        vec_put(1, r, B[r]);
+      } else {
+        float* out = a.part + (int64_t)blockIdx.x * 2 * a.d;
+        store_piece<kSub>(out, c[r], a.d, A[r]);
+        store_piece<kSub>(out + a.d, c[r], a.d, B[r]);
       }
     }
+  }
 }
 
 // the [d] gradients: column sums over the workgroups, 32 columns of A (blockIdx.y = 0)
@@ -380,11 +471,11 @@ __global__ __launch_bounds__(1024) void k_norm_vectors(const float* part, int gr
     if (dv_in) dv_in[c] = v;
     return;
   }
-  if (dgate) dgate[c] = a.v_out ? v * to_f32(static_cast<const S*>(a.v_out)[c]) : v;
-  if (dv_out) dv_out[c] = a.gate_kind == MOE_GATE_CHANNEL ? v * to_f32(static_cast<const S*>(a.gate)[c]) : v;
+  if (dgate) dgate[c] = a.v_out ? v * load_one(static_cast<const S*>(a.v_out) + c) : v;
+  if (dv_out) dv_out[c] = a.gate_kind == MOE_GATE_CHANNEL ? v * load_one(static_cast<const S*>(a.gate) + c) : v;
 }
 
-// `target` threads per workgroup, more where one row needs them
+// Forward: `target` threads per workgroup, more where one row needs them.
 static NormSplit norm_split(int d, int target) {
   NormSplit p;
   const int pieces = (int)ceil_div(d, kPiece);
@@ -398,11 +489,33 @@ static NormSplit norm_split(int d, int target) {
   return p;
 }
 
-// workgroups of the gradient: two per CU, few enough that their column sums stay small
-// beside the rows
-static int norm_groups(int T, int d) {
-  return (int)std::min<int64_t>(ceil_div(T, norm_split(d, 512).slots), 512);
+// Gradient: a row of up to 2048 elements of two bytes or 1024 floats has one wavefront
+// with one, two or four pieces per lane, longer ones several with the most pieces; fewer
+// rows per workgroup where there are few, so that every CU has some.
+static NormSplit norm_back_split(int T, int d, int dtype) {
+  NormSplit p;
+  const int bytes = (int)dtype_bytes(dtype);
+  const int pieces = (int)ceil_div(d, kPiece);
+  p.pieces = pieces <= 64 ? 1 : pieces <= (bytes == 4 ? 1024 : 128) ? 2 : 4;
+  const int lanes = (int)ceil_div(pieces, p.pieces);
+  p.lt = 0;
+  while (p.lt < 6 && (1 << p.lt) < lanes) ++p.lt;
+  p.waves = (int)ceil_div(lanes, 64);
+  const int most = norm_back_waves(bytes, p.pieces);
+  const int per_wave = 64 >> p.lt;
+  int groups = p.waves > 1 ? most / p.waves : most;  // wavefronts (or groups of them) per workgroup
+  groups = (int)std::max<int64_t>(1, std::min<int64_t>(groups, ceil_div(T, 256 * per_wave)));
+  p.slots = groups * per_wave;
+  p.threads = groups * p.waves * 64;
+  return p;
 }
+static int64_t norm_back_lds(const NormSplit& p) {
+  return (int64_t)2 * p.pieces * kPiece * 4 * (p.waves > 1 ? p.waves * 64 : 1 << p.lt);
+}
+
+// workgroups of the gradient: one per CU (its registers allow one), so that their column
+// sums stay small beside the rows
+static int norm_groups(int T, const NormSplit& p) { return (int)std::min<int64_t>(ceil_div(T, p.slots), 256); }
 
 static int check_norm(const char* fn, const moe_block_norm_args* a) {
   MOE_CHECK_ARG(a != nullptr, MOE_ERR_INVALID_ARG, "%s: args is NULL", fn);
@@ -451,6 +564,7 @@ static NormDev norm_dev(const moe_block_norm_args* a) {
   v.d = a->d;
   v.scale = a->residual_scale;
   v.eps = a->eps;
+  v.inv_d = 1.f / a->d;
   return v;
 }
 
@@ -494,7 +608,7 @@ extern "C" int moe_block_norm(const moe_block_norm_args* a, void* h, int64_t h_s
 
 extern "C" int64_t moe_block_norm_backward_workspace_bytes(int T, int d) {
   if (T < 0 || d <= 0) return -1;
-  return (int64_t)norm_groups(T, d) * 2 * d * 4;
+  return (int64_t)std::min(T, 256) * 2 * d * 4;
 }
 
 extern "C" int moe_block_norm_backward(const moe_block_norm_args* a, const moe_block_norm_grads* g, void* stream) {
@@ -540,29 +654,35 @@ extern "C" int moe_block_norm_backward(const moe_block_norm_args* a, const moe_b
   v.dgate_stride = g->dgate_stride;
   v.part = vectors ? static_cast<float*>(g->workspace) : nullptr;
   hipStream_t s = (hipStream_t)stream;
-  const NormSplit p = norm_split(a->d, 512);
-  const int groups = norm_groups(a->T, a->d);
+  const NormSplit p = norm_back_split(a->T, a->d, a->dtype);
+  const int groups = norm_groups(a->T, p);
   timing_begin(K_BLOCK_NORM_BWD, s);
   with_dtype(a->dtype, [&](auto e) {
     using S = decltype(e);
     if (a->T > 0) {
-      auto go = [&](auto pieces, auto threads, auto sub) {
-        constexpr int R = decltype(pieces)::value, B = decltype(threads)::value;
+      auto launch = [&](auto kernel) {
+        const int64_t lds = norm_back_lds(p);
+        if (lds > 65536)  // (rows of over 8192 elements)
+          (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        hipLaunchKernelGGL(kernel, dim3(groups), dim3(p.threads), (unsigned)lds, s, v, p);
+      };
+      auto go = [&](auto pieces, auto sub) {
+        constexpr int R = decltype(pieces)::value;
         constexpr bool kSub = decltype(sub)::value;
         if (a->gate_kind == MOE_GATE_FULL)
-          hipLaunchKernelGGL((k_block_norm_backward<S, R, B, kSub, true>), dim3(groups), dim3(p.threads), 0, s, v, p);
+          launch(k_block_norm_backward<S, R, kSub, true>);
         else
-          hipLaunchKernelGGL((k_block_norm_backward<S, R, B, kSub, false>), dim3(groups), dim3(p.threads), 0, s, v, p);
+          launch(k_block_norm_backward<S, R, kSub, false>);
       };
       using std::integral_constant;
       if (p.lt < 6)
-        go(integral_constant<int, 1>{}, integral_constant<int, 512>{}, std::true_type{});
+        go(integral_constant<int, 1>{}, std::true_type{});
       else if (p.pieces == 1)
-        go(integral_constant<int, 1>{}, integral_constant<int, 512>{}, std::false_type{});
-      else if (p.threads <= 512)
-        go(integral_constant<int, 2>{}, integral_constant<int, 512>{}, std::false_type{});
+        go(integral_constant<int, 1>{}, std::false_type{});
+      else if (p.pieces == 2)
+        go(integral_constant<int, 2>{}, std::false_type{});
       else
-        go(integral_constant<int, 2>{}, integral_constant<int, 1024>{}, std::false_type{});
+        go(integral_constant<int, 4>{}, std::false_type{});
     }
     if (vectors)
       hipLaunchKernelGGL(k_norm_vectors<S>, dim3((unsigned)ceil_div(a->d, 32), 2), dim3(1024), 0, s, v.part, groups, v,

@@ -39,7 +39,8 @@ __global__ __launch_bounds__(256) void k_spread(PermuteDev a, int lt) {
   for (int j = 0; j < MOE_MAX_TOPK; ++j) dot[j] = 0.f;
   for (int c = lane * kPiece; c < a.d; c += kPiece << lt) {
     const Piece n = piece_of(c, a.d);
-    const Raw<S> raw = load_raw<kTiny>(src, n, a.d);
+    Raw<S> raw = load_raw<kTiny>(src, n, a.d);
+    mask_piece(raw, n);
     float v[kPiece];
     unpack<S>(raw, v);
 #pragma unroll

@@ -31,36 +31,42 @@ struct Raw {
   u32x4_t w[sizeof(S) == 4 ? 2 : 1];
 };
 
-__device__ __forceinline__ float to_f32(bf16_row_t v) { return bf16_bits_to_f32(v.bits); }
-__device__ __forceinline__ float to_f32(_Float16 v) { return (float)v; }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ void from_f32(bf16_row_t* p, float v) { p->bits = (uint16_t)f32_to_bf16_bits(v); }
-__device__ __forceinline__ void from_f32(_Float16* p, float v) { *p = (_Float16)v; }
-__device__ __forceinline__ void from_f32(float* p, float v) { *p = v; }
 
 // Where a lane's eight elements of a row of d lie.  The last piece of a row whose length
 // is no multiple of 8 starts at d - 8, so that every load is one of eight elements inside
 // the row and none sits under a branch; its first `skip` elements belong to the piece
-// before and read as zero.  A lane past the end skips all eight.  kTiny: rows of fewer than
+// before (mask_piece makes them zero).  A lane past the end skips all eight.  kTiny: rows of fewer than
 // eight elements too (at = 0), element by element; kernels take it for short rows only.
 struct Piece {
-  int at, skip;
+  uint32_t at;  // first element
+  int skip;
 };
 __device__ __forceinline__ Piece piece_of(int col, int d) {
   const int at = col + kPiece <= d ? col : d > kPiece ? d - kPiece : 0;
-  return {at, col - at < kPiece ? col - at : kPiece};
+  return {(uint32_t)at, col - at < kPiece ? col - at : kPiece};
+}
+// (Global memory by a scalar base and a 32-bit offset in bytes where the row's address is
+// uniform: no vector registers for addresses.)
+#define MOE_GLOBAL __attribute__((address_space(1)))
+template <typename S>
+__device__ __forceinline__ const MOE_GLOBAL char* piece_ptr(const S* row, const Piece& p) {
+  return (const MOE_GLOBAL char*)row + (uint32_t)(p.at * sizeof(S));
+}
+template <typename S>
+__device__ __forceinline__ MOE_GLOBAL char* piece_ptr(S* row, const Piece& p) {
+  return (MOE_GLOBAL char*)row + (uint32_t)(p.at * sizeof(S));
 }
 
 template <bool kTiny, typename S>
 __device__ __forceinline__ Raw<S> load_raw(const S* row, const Piece& p, int d) {
   Raw<S> r;
   if (!kTiny || d >= kPiece) {
-    const S* q = row + p.at;
+    const MOE_GLOBAL char* q = piece_ptr(row, p);
     if constexpr (sizeof(S) == 2) {
-      r.w[0] = *reinterpret_cast<const u32x4_a2_t*>(q);
+      r.w[0] = *(const MOE_GLOBAL u32x4_a2_t*)q;
     } else {
-      r.w[0] = *reinterpret_cast<const u32x4_a4_t*>(q);
-      r.w[1] = *reinterpret_cast<const u32x4_a4_t*>(q + 4);
+      r.w[0] = *(const MOE_GLOBAL u32x4_a4_t*)q;
+      r.w[1] = *(const MOE_GLOBAL u32x4_a4_t*)(q + 16);
     }
   } else {
     uint32_t h[kPiece];
@@ -81,6 +87,12 @@ __device__ __forceinline__ Raw<S> load_raw(const S* row, const Piece& p, int d) 
         r.w[i >> 2][i & 3] = h[i];
     }
   }
+  return r;
+}
+
+// zero for the elements that are not this piece's (at the first use, not at the load)
+template <typename S>
+__device__ __forceinline__ void mask_piece(Raw<S>& r, const Piece& p) {
   if (p.skip) {
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) {
@@ -90,28 +102,28 @@ __device__ __forceinline__ Raw<S> load_raw(const S* row, const Piece& p, int d) 
         r.w[i >> 2][i & 3] = i < p.skip ? 0u : r.w[i >> 2][i & 3];
     }
   }
-  return r;
 }
 
 template <bool kTiny, typename S>
 __device__ __forceinline__ void store_raw(S* row, const Piece& p, int d, const Raw<S>& r) {
   if (p.skip == 0 && (!kTiny || d >= kPiece)) {
-    S* q = row + p.at;
+    MOE_GLOBAL char* q = piece_ptr(row, p);
     if constexpr (sizeof(S) == 2) {
-      *reinterpret_cast<u32x4_a2_t*>(q) = r.w[0];
+      *(MOE_GLOBAL u32x4_a2_t*)q = r.w[0];
     } else {
-      *reinterpret_cast<u32x4_a4_t*>(q) = r.w[0];
-      *reinterpret_cast<u32x4_a4_t*>(q + 4) = r.w[1];
+      *(MOE_GLOBAL u32x4_a4_t*)q = r.w[0];
+      *(MOE_GLOBAL u32x4_a4_t*)(q + 16) = r.w[1];
     }
     return;
   }
 #pragma unroll
   for (int i = 0; i < kPiece; ++i) {
-    if (i < p.skip || (kTiny && p.at + i >= d)) continue;
+    if (i < p.skip || (kTiny && (int)p.at + i >= d)) continue;
+    MOE_GLOBAL char* q = piece_ptr(row, p) + i * sizeof(S);
     if constexpr (sizeof(S) == 2)
-      reinterpret_cast<uint16_t*>(row)[p.at + i] = (uint16_t)(r.w[0][i >> 1] >> (16 * (i & 1)));
+      *(MOE_GLOBAL uint16_t*)q = (uint16_t)(r.w[0][i >> 1] >> (16 * (i & 1)));
     else
-      reinterpret_cast<uint32_t*>(row)[p.at + i] = r.w[i >> 2][i & 3];
+      *(MOE_GLOBAL uint32_t*)q = r.w[i >> 2][i & 3];
   }
 }
 
@@ -148,9 +160,19 @@ __device__ __forceinline__ Raw<S> pack(const float (&v)[kPiece]) {
   return r;
 }
 
+template <typename S>
+__device__ __forceinline__ float load_one(const S* p) {
+  if constexpr (std::is_same<S, bf16_row_t>::value)
+    return bf16_bits_to_f32(*(const MOE_GLOBAL uint16_t*)p);
+  else
+    return (float)*(const MOE_GLOBAL S*)p;
+}
+
 template <bool kTiny, typename S>
 __device__ __forceinline__ void load_piece(const S* row, const Piece& p, int d, float (&v)[kPiece]) {
-  unpack<S>(load_raw<kTiny>(row, p, d), v);
+  Raw<S> r = load_raw<kTiny>(row, p, d);
+  mask_piece(r, p);
+  unpack<S>(r, v);
 }
 template <bool kTiny, typename S>
 __device__ __forceinline__ void store_piece(S* row, const Piece& p, int d, const float (&v)[kPiece]) {
