@@ -36,22 +36,6 @@ struct NormDev {
   float* part;  // [workgroup][2][d]: column sums for v_out and gate, and for v_in; or null
 };
 
-// Row t of a tensor.  A wavefront with one row keeps its address in scalar registers, as
-// the base that 32-bit lane offsets add to: without the asm the compiler adds the lane's
-// offset to the tensor's address first, two vector registers per tensor and piece.
-template <typename S, bool kSub>
-__device__ __forceinline__ const S* row_ptr(const void* p, int64_t t, int64_t stride) {
-  const S* r = static_cast<const S*>(p) + t * stride;
-  if (!kSub) asm("" : "+s"(r));
-  return r;
-}
-template <typename S, bool kSub>
-__device__ __forceinline__ S* row_ptr(void* p, int64_t t, int64_t stride) {
-  S* r = static_cast<S*>(p) + t * stride;
-  if (!kSub) asm("" : "+s"(r));
-  return r;
-}
-
 template <typename S, bool kSub>
 __device__ __forceinline__ float token_gate(const NormDev& a, int64_t t) {
   return a.gate_kind == MOE_GATE_TOKEN ? load_one(row_ptr<S, kSub>(a.gate, t, a.gate_stride)) : 1.f;
@@ -103,13 +87,6 @@ __device__ __forceinline__ Raw<S> ones() {
 #pragma unroll
   for (int i = 0; i < kPiece; ++i) v[i] = 1.f;
   return pack<S>(v);
-}
-
-template <typename S>
-__device__ __forceinline__ Raw<S> masked(Raw<S> r, uint32_t mask) {
-#pragma unroll
-  for (int q = 0; q < (int)(sizeof(r.w) / sizeof(r.w[0])); ++q) r.w[q] &= mask;
-  return r;
 }
 
 // The same values, unknown to the compiler.

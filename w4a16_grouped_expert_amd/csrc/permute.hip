@@ -5,9 +5,9 @@
 //
 // With R the T*k x T matrix that holds w[p] at (pair_pos[p], p / k), the four calls are
 // rows = R x, out = R^T rows, and the transposes of these in their gradients, which add
-// the scalar products that are the weights' gradients.  So there are two kernels, one
-// that spreads a token's row over its k sorted rows and one that gathers them, each with
-// or without the scalar products.  Both go by token: its row is read (written) once.
+// the scalar products that are the weights' gradients.  So one kernel either spreads a
+// token's row over its k sorted rows or gathers them, with or without the scalar
+// products.  It goes by token, whose row is read (written) once.
 #include "rows.hpp"
 
 namespace moe {
@@ -21,125 +21,199 @@ struct PermuteDev {
   int64_t out_stride;
   int64_t num_rows;
   int T, d, k;
-  const int32_t* pair_pos;
-  const float* weights;   // or null
   float* dweights;        // products only
 };
 
-// One group of 1 << lt lanes per token (lt <= 6), 64 >> lt tokens per wavefront.
-template <typename S, bool kProducts, bool kTiny>
-__global__ __launch_bounds__(256) void k_spread(PermuteDev a, int lt) {
-  const int lane = threadIdx.x & ((1 << lt) - 1);
-  const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lt;
+// How the threads of a workgroup share tokens: a token has 1 << lt lanes of a wavefront
+// (short rows) or `waves` whole ones, and each lane `rounds` pieces of its row.
+struct TokenSplit {
+  int lt, waves, tokens, threads, rounds;
+};
+
+// Rows of more than 256 elements.  A wavefront handles 64 pieces of 8 elements of one
+// token with at most KM pairs: its positions and weights come through scalar loads, the
+// rows' addresses stay in scalar registers, and the loads of KB rows go out before the
+// first use.  Pairs that were dropped read some row that is there (`sorted_in` always has
+// one) and are masked, so that no load sits under a branch.
+template <typename S, bool kSpread, bool kProducts, int KM, int KB>
+__global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __restrict__ pair_pos,
+                                               const float* __restrict__ weights, TokenSplit p) {
+  __shared__ float part_sums[kProducts ? 16 : 1][KM];
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int part = wave % p.waves, lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * p.tokens + wave / p.waves;
   const bool live = t < a.T;
+  if (!live && !kProducts) return;
   const int64_t tc = live ? t : a.T - 1;
-  const S* src = static_cast<const S*>(a.token_in) + tc * a.token_in_stride;
-  float dot[MOE_MAX_TOPK];
+  int64_t pos[KM];
+  float w[KM], dot[KM];
+  uint32_t kept[KM];
 #pragma unroll
-  for (int j = 0; j < MOE_MAX_TOPK; ++j) dot[j] = 0.f;
-  for (int c = lane * kPiece; c < a.d; c += kPiece << lt) {
-    const Piece n = piece_of(c, a.d);
-    Raw<S> raw = load_raw<kTiny>(src, n, a.d);
-    mask_piece(raw, n);
-    float v[kPiece];
-    unpack<S>(raw, v);
+  for (int j = 0; j < KM; ++j) {
+    const int64_t at = tc * a.k + (j < a.k ? j : a.k - 1);
+    pos[j] = pair_pos[at];
+    w[j] = weights ? weights[at] : 1.f;
+    dot[j] = 0.f;
+  }
 #pragma unroll
-    for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-      const int64_t pos = j < a.k ? a.pair_pos[tc * a.k + j] : -1;
-      if (!live || pos < 0 || pos >= a.num_rows) continue;
-      if constexpr (kProducts) {
-        float r[kPiece];
-        load_piece<kTiny>(static_cast<const S*>(a.sorted_in) + pos * a.sorted_in_stride, n, a.d, r);
+  for (int j = 0; j < KM; ++j) {
+    kept[j] = live && j < a.k && pos[j] >= 0 && pos[j] < a.num_rows ? ~0u : 0u;
+    pos[j] = kept[j] ? pos[j] : 0;
+  }
+  for (int it = 0; it < p.rounds; ++it) {
+    Piece c = piece_of((part * 64 + lane + it * p.waves * 64) * kPiece, a.d);
+    if (!live) c.skip = kPiece;
+    Raw<S> mine;
+    if (kSpread || kProducts)
+      mine = load_raw<false>(row_ptr<S, false>(a.token_in, tc, a.token_in_stride), c, a.d);
+    float v[kPiece], r[kPiece], acc[kPiece];
+    if (kSpread || kProducts) unpack<S>(mine, v);
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) dot[j] = fmaf(v[i], r[i], dot[j]);
-      }
-      S* dst = static_cast<S*>(a.out) + pos * a.out_stride;
-      if (a.weights) {
-        const float w = a.weights[tc * a.k + j];
-        float o[kPiece];
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) o[i] = w * v[i];
-        store_piece<kTiny>(dst, n, a.d, o);
-      } else {
-        store_raw<kTiny>(dst, n, a.d, raw);
-      }
+    for (int i = 0; i < kPiece; ++i) {
+      acc[i] = 0.f;
+      if (kProducts) v[i] = i < c.skip ? 0.f : v[i];  // (elements of the piece before: in its sum)
     }
+#pragma unroll
+    for (int j0 = 0; j0 < KM; j0 += KB) {
+      if (j0 >= a.k) continue;
+      Raw<S> row[KB];
+      if (!kSpread || kProducts) {
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+          row[b] = load_raw<false>(row_ptr<S, false>(a.sorted_in, pos[j0 + b], a.sorted_in_stride), c, a.d);
+      }
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        const int j = j0 + b;
+        if (!kSpread || kProducts) {
+          unpack<S>(masked<S>(row[b], kept[j]), r);
+#pragma unroll
+          for (int i = 0; i < kPiece; ++i) {
+            if (!kSpread) acc[i] = fmaf(w[j], r[i], acc[i]);
+            if (kProducts) dot[j] = fmaf(v[i], r[i], dot[j]);
+          }
+        }
+        if (kSpread && kept[j]) {
+          S* dst = row_ptr<S, false>(a.out, pos[j], a.out_stride);
+          if (weights) {
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) acc[i] = w[j] * v[i];
+            store_piece<false>(dst, c, a.d, acc);
+          } else {
+            store_raw<false>(dst, c, a.d, mine);
+          }
+        }
+      }
+      if (KB < KM) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (!kSpread && live) store_piece<false>(row_ptr<S, false>(a.out, tc, a.out_stride), c, a.d, acc);
   }
   if constexpr (kProducts) {
+    // over the lanes, then over the token's wavefronts in order
 #pragma unroll
-    for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-      const float s = lane_sum(dot[j], lt);
-      if (live && lane == 0 && j < a.k) a.dweights[t * a.k + j] = s;
+    for (int j = 0; j < KM; ++j) {
+      dot[j] = lane_sum(dot[j], 6);
+      if (lane == 0) part_sums[wave][j] = dot[j];
     }
+    __syncthreads();
+    if (!live || part != 0 || lane >= a.k) return;
+    float s = 0.f;
+    for (int i = 0; i < p.waves; ++i) s += part_sums[wave + i][lane];
+    a.dweights[t * a.k + lane] = s;
   }
 }
 
-template <typename S, bool kProducts, bool kTiny>
-__global__ __launch_bounds__(256) void k_gather(PermuteDev a, int lt) {
-  const int lane = threadIdx.x & ((1 << lt) - 1);
-  const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> lt;
-  const bool live = t < a.T;
-  const int64_t tc = live ? t : a.T - 1;
-  float dot[MOE_MAX_TOPK];
+// Rows of at most 256 elements: 1 << lt lanes per token, several tokens per wavefront.
+template <typename S, bool kSpread, bool kProducts>
+__global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t* __restrict__ pair_pos,
+                                                    const float* __restrict__ weights, TokenSplit p) {
+  const int lane = threadIdx.x & ((1 << p.lt) - 1);
+  const int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> p.lt;
+  if (t >= a.T) return;  // (a token's lanes return together: the sums below stay within them)
+  const Piece c = piece_of(lane * kPiece, a.d);
+  Raw<S> mine{};
+  if (kSpread || kProducts) mine = load_raw<true>(row_ptr<S, true>(a.token_in, t, a.token_in_stride), c, a.d);
+  mask_piece(mine, c);
+  float v[kPiece], r[kPiece], acc[kPiece];
+  unpack<S>(mine, v);
 #pragma unroll
-  for (int j = 0; j < MOE_MAX_TOPK; ++j) dot[j] = 0.f;
-  for (int c = lane * kPiece; c < a.d; c += kPiece << lt) {
-    const Piece n = piece_of(c, a.d);
-    float v[kPiece], acc[kPiece];
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) acc[i] = 0.f;
-    if constexpr (kProducts)
-      load_piece<kTiny>(static_cast<const S*>(a.token_in) + tc * a.token_in_stride, n, a.d, v);
-#pragma unroll
-    for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-      const int64_t pos = j < a.k ? a.pair_pos[tc * a.k + j] : -1;
-      if (!live || pos < 0 || pos >= a.num_rows) continue;
-      const float w = a.weights ? a.weights[tc * a.k + j] : 1.f;
-      float r[kPiece];
-      load_piece<kTiny>(static_cast<const S*>(a.sorted_in) + pos * a.sorted_in_stride, n, a.d, r);
+  for (int i = 0; i < kPiece; ++i) acc[i] = 0.f;
+  for (int j = 0; j < a.k; ++j) {
+    const int64_t at = t * a.k + j, pos = pair_pos[at];
+    const bool kept = pos >= 0 && pos < a.num_rows;
+    const float w = weights ? weights[at] : 1.f;
+    float dot = 0.f;
+    if (!kSpread || kProducts) {
+      Raw<S> row = load_raw<true>(row_ptr<S, true>(a.sorted_in, kept ? pos : 0, a.sorted_in_stride), c, a.d);
+      unpack<S>(masked<S>(row, kept ? ~0u : 0u), r);
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
-        acc[i] = fmaf(w, r[i], acc[i]);
-        if constexpr (kProducts) dot[j] = fmaf(v[i], r[i], dot[j]);
+        if (!kSpread) acc[i] = fmaf(w, r[i], acc[i]);
+        if (kProducts) dot = fmaf(v[i], r[i], dot);
       }
     }
-    if (live) store_piece<kTiny>(static_cast<S*>(a.out) + t * a.out_stride, n, a.d, acc);
-  }
-  if constexpr (kProducts) {
+    if (kSpread && kept) {
+      S* dst = row_ptr<S, true>(a.out, pos, a.out_stride);
+      if (weights) {
 #pragma unroll
-    for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-      const float s = lane_sum(dot[j], lt);
-      if (live && lane == 0 && j < a.k) a.dweights[t * a.k + j] = s;
+        for (int i = 0; i < kPiece; ++i) r[i] = w * v[i];
+        store_piece<true>(dst, c, a.d, r);
+      } else {
+        store_raw<true>(dst, c, a.d, mine);
+      }
+    }
+    if (kProducts) {
+      dot = lane_sum(dot, p.lt);
+      if (lane == 0) a.dweights[at] = dot;
     }
   }
+  if (!kSpread) store_piece<true>(row_ptr<S, true>(a.out, t, a.out_stride), c, a.d, acc);
 }
 
-// lanes per token (log2): as many as have a piece of the row, at most a wavefront
-static int token_lanes_log2(int d) {
-  int lt = 0;
-  while (lt < 6 && (kPiece << lt) < d) ++lt;
-  return lt;
+static TokenSplit token_split(int d) {
+  TokenSplit p;
+  const int pieces = (int)ceil_div(d, kPiece);
+  p.lt = 0;
+  while (p.lt < 6 && (1 << p.lt) < pieces) ++p.lt;
+  const int64_t full = ceil_div(pieces, 64);
+  p.waves = (int)std::min<int64_t>(full, 16);
+  p.rounds = (int)ceil_div(full, p.waves);
+  p.tokens = p.lt < 6 ? 256 >> p.lt : std::max(1, 4 / p.waves);
+  p.threads = p.lt < 6 ? 256 : p.tokens * p.waves * 64;
+  return p;
 }
 
-static int launch_rows(const char* name, int timing_id, bool spread, int dtype, const PermuteDev& a, hipStream_t s) {
-  const int lt = token_lanes_log2(a.d);
-  const dim3 grid((unsigned)ceil_div((int64_t)a.T << lt, 256));
-  const bool products = a.dweights != nullptr;
+static int launch_rows(const char* name, int timing_id, bool spread, int dtype, PermuteDev a, const int32_t* pair_pos,
+                       const float* weights, hipStream_t s) {
+  const TokenSplit p = token_split(a.d);
+  const dim3 grid((unsigned)ceil_div(a.T, p.tokens));
+  if (a.num_rows == 0) {  // every pair is dropped: what they read is masked, any row will do
+    a.sorted_in = spread ? a.token_in : a.out;
+    a.sorted_in_stride = 0;
+  }
   timing_begin(timing_id, s);
   with_dtype(dtype, [&](auto v) {
     using S = decltype(v);
-    auto go = [&](auto prod, auto tiny) {
-      constexpr bool kP = decltype(prod)::value, kT = decltype(tiny)::value;
-      if (spread)
-        hipLaunchKernelGGL((k_spread<S, kP, kT>), grid, dim3(256), 0, s, a, lt);
+    auto go = [&](auto spread_c, auto products_c) {
+      constexpr bool kSpread = decltype(spread_c)::value, kProducts = decltype(products_c)::value;
+      auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(p.threads), 0, s, a, pair_pos, weights, p); };
+      if (p.lt < 6)
+        launch(k_rows_short<S, kSpread, kProducts>);
+      else if (a.k <= 2)
+        launch(k_rows<S, kSpread, kProducts, 2, 2>);
+      else if (a.k <= 4)
+        launch(k_rows<S, kSpread, kProducts, 4, 4>);
+      else if (a.k <= 8)
+        launch(k_rows<S, kSpread, kProducts, 8, 8>);
       else
-        hipLaunchKernelGGL((k_gather<S, kP, kT>), grid, dim3(256), 0, s, a, lt);
+        launch(k_rows<S, kSpread, kProducts, 16, 8>);
     };
-    const bool tiny = a.d < kPiece;
-    if (products)
-      tiny ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+    const std::true_type yes;
+    const std::false_type no;
+    if (spread)
+      a.dweights ? go(yes, yes) : go(yes, no);
     else
-      tiny ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
+      a.dweights ? go(no, yes) : go(no, no);
   });
   timing_end(timing_id, s);
   return check_launch(name);
@@ -185,8 +259,8 @@ extern "C" int moe_permute(const void* x, int64_t x_stride, int dtype, int T, in
   const RowArg args[4] = {{"x", x, x_stride, false, true}, {"rows", rows, rows_stride, true, num_rows > 0}, {}, {}};
   const int rc = check_rows("moe_permute", dtype, T, d, k, num_rows, pair_pos, weights, nullptr, args);
   if (rc || T == 0) return rc;
-  const PermuteDev a{x, x_stride, nullptr, 0, rows, rows_stride, num_rows, T, d, k, pair_pos, weights, nullptr};
-  return launch_rows("moe_permute", K_PERMUTE, true, dtype, a, (hipStream_t)stream);
+  const PermuteDev a{x, x_stride, nullptr, 0, rows, rows_stride, num_rows, T, d, k, nullptr};
+  return launch_rows("moe_permute", K_PERMUTE, true, dtype, a, pair_pos, weights, (hipStream_t)stream);
 }
 
 extern "C" int moe_unpermute(const void* rows, int64_t rows_stride, int64_t num_rows, int dtype, int T, int d, int k,
@@ -196,8 +270,8 @@ extern "C" int moe_unpermute(const void* rows, int64_t rows_stride, int64_t num_
   const RowArg args[4] = {{"rows", rows, rows_stride, false, num_rows > 0}, {"out", out, out_stride, true, true}, {}, {}};
   const int rc = check_rows("moe_unpermute", dtype, T, d, k, num_rows, pair_pos, weights, nullptr, args);
   if (rc || T == 0) return rc;
-  const PermuteDev a{nullptr, 0, rows, rows_stride, out, out_stride, num_rows, T, d, k, pair_pos, weights, nullptr};
-  return launch_rows("moe_unpermute", K_UNPERMUTE, false, dtype, a, (hipStream_t)stream);
+  const PermuteDev a{nullptr, 0, rows, rows_stride, out, out_stride, num_rows, T, d, k, nullptr};
+  return launch_rows("moe_unpermute", K_UNPERMUTE, false, dtype, a, pair_pos, weights, (hipStream_t)stream);
 }
 
 extern "C" int moe_permute_backward(const void* drows, int64_t drows_stride, int64_t num_rows, const void* x,
@@ -210,8 +284,8 @@ extern "C" int moe_permute_backward(const void* drows, int64_t drows_stride, int
                           {}};
   const int rc = check_rows("moe_permute_backward", dtype, T, d, k, num_rows, pair_pos, weights, dweights, args);
   if (rc || T == 0) return rc;
-  const PermuteDev a{x, x_stride, drows, drows_stride, dx, dx_stride, num_rows, T, d, k, pair_pos, weights, dweights};
-  return launch_rows("moe_permute_backward", K_UNPERMUTE, false, dtype, a, (hipStream_t)stream);
+  const PermuteDev a{x, x_stride, drows, drows_stride, dx, dx_stride, num_rows, T, d, k, dweights};
+  return launch_rows("moe_permute_backward", K_UNPERMUTE, false, dtype, a, pair_pos, weights, (hipStream_t)stream);
 }
 
 extern "C" int moe_unpermute_backward(const void* dout, int64_t dout_stride, const void* rows, int64_t rows_stride,
@@ -225,7 +299,6 @@ extern "C" int moe_unpermute_backward(const void* dout, int64_t dout_stride, con
                           {}};
   const int rc = check_rows("moe_unpermute_backward", dtype, T, d, k, num_rows, pair_pos, weights, dweights, args);
   if (rc || T == 0) return rc;
-  const PermuteDev a{dout,     dout_stride, rows, rows_stride, drows,   drows_stride, num_rows,
-                     T,        d,           k,    pair_pos,    weights, dweights};
-  return launch_rows("moe_unpermute_backward", K_PERMUTE, true, dtype, a, (hipStream_t)stream);
+  const PermuteDev a{dout, dout_stride, rows, rows_stride, drows, drows_stride, num_rows, T, d, k, dweights};
+  return launch_rows("moe_unpermute_backward", K_PERMUTE, true, dtype, a, pair_pos, weights, (hipStream_t)stream);
 }

@@ -179,6 +179,29 @@ __device__ __forceinline__ void store_piece(S* row, const Piece& p, int d, const
   store_raw<kTiny>(row, p, d, pack<S>(v));
 }
 
+// Row t of a tensor.  A wavefront with one row keeps its address in scalar registers, as
+// the base that 32-bit lane offsets add to: without the asm the compiler adds the lane's
+// offset to the tensor's address first, two vector registers per tensor and piece.
+template <typename S, bool kSub>
+__device__ __forceinline__ const S* row_ptr(const void* p, int64_t t, int64_t stride) {
+  const S* r = static_cast<const S*>(p) + t * stride;
+  if (!kSub) asm("" : "+s"(r));
+  return r;
+}
+template <typename S, bool kSub>
+__device__ __forceinline__ S* row_ptr(void* p, int64_t t, int64_t stride) {
+  S* r = static_cast<S*>(p) + t * stride;
+  if (!kSub) asm("" : "+s"(r));
+  return r;
+}
+
+template <typename S>
+__device__ __forceinline__ Raw<S> masked(Raw<S> r, uint32_t mask) {
+#pragma unroll
+  for (int q = 0; q < (int)(sizeof(r.w) / sizeof(r.w[0])); ++q) r.w[q] &= mask;
+  return r;
+}
+
 template <int kCtrl>
 __device__ __forceinline__ float add_dpp(float v) {
   return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xF, 0xF, true));
