@@ -16,9 +16,9 @@
 
 namespace moe {
 
-constexpr int kRbTokens = 16;    // tokens per workgroup of the logits' gradient
-constexpr int kRbCols = 128;     // columns of d per wavefront
-constexpr int kRbTokenBlocks = 4;  // token blocks of 16 per wavefront of dx
+constexpr int kRbTokens = 16;      // tokens per workgroup of the logits' gradient
+constexpr int kRbCols = 128;       // columns of d per wavefront
+constexpr int kRbTokenBlocks = 2;  // token blocks of 16 per wavefront of dx
 
 struct RouteBackDev {
   const uint16_t *x, *w;
@@ -42,55 +42,74 @@ struct RouteBackDev {
 __host__ __device__ inline int rb_row_floats(int Ep) { return Ep < 1024 ? Ep + 1 : Ep; }
 static_assert(kRbTokens * 1024 * 4 <= 65536 && MOE_MAX_EXPERTS <= 1024, "LDS of k_route_dlogits");
 
-// the gradient of the logits of kRbTokens tokens, split and stored both ways
-__global__ __launch_bounds__(256) void k_route_dlogits(RouteBackDev a) {
+// The gradient of the logits of kRbTokens tokens, split and stored both ways: a wavefront
+// per token, its E <= 64 kEL logits (read once) in the lanes' registers.
+template <int kEL>
+__global__ __launch_bounds__(64 * kRbTokens) void k_route_dlogits(RouteBackDev a) {
   extern __shared__ float g[];  // [kRbTokens][ld]
   const int lane = lane_id(), wave = threadIdx.x >> 6;
-  const int64_t t0 = (int64_t)blockIdx.x * kRbTokens;
+  const int64_t t0 = (int64_t)blockIdx.x * kRbTokens, t = t0 + wave;
   const int ld = rb_row_floats(a.Ep);
-  for (int i = wave; i < kRbTokens; i += 4) {
-    const int64_t t = t0 + i;
-    float* row = g + i * ld;
-    if (t >= a.T) {
-      for (int e = lane; e < a.Ep; e += 64) row[e] = 0.f;
-      continue;
+  float* row = g + wave * ld;
+  float v[kEL];
+#pragma unroll
+  for (int i = 0; i < kEL; ++i) v[i] = 0.f;
+  if (t < a.T) {
+    float add[kEL];
+#pragma unroll
+    for (int i = 0; i < kEL; ++i) {
+      const int e = lane + 64 * i;
+      v[i] = !a.renormalize && e < a.E ? a.logits[t * a.E + e] : -INFINITY;
+      add[i] = a.dlogits && e < a.E ? a.dlogits[t * a.E + e] : 0.f;
     }
     int id = -1;
     float w = 0.f, dw = 0.f;
     if (lane < a.k) {
       id = a.ids[t * a.k + lane];
-      if (id < 0 || id >= a.E) id = -1;
-      if (id >= 0) {
-        w = a.weights[t * a.k + lane];
-        dw = a.dweights[t * a.k + lane];
+      w = a.weights[t * a.k + lane];
+      dw = a.dweights[t * a.k + lane];
+      if (id < 0 || id >= a.E) {
+        id = -1;
+        w = dw = 0.f;
       }
     }
-    float s = w * dw;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
+    const float s = lane_sum(w * dw, 6);
     if (a.renormalize) {
-      for (int e = lane; e < a.Ep; e += 64) row[e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kEL; ++i) v[i] = 0.f;
     } else {
-      const float* l = a.logits + t * a.E;
-      float top = -INFINITY, sum = 0.f;
-      for (int e = lane; e < a.E; e += 64) top = fmaxf(top, l[e]);
+      float top = v[0], sum = 0.f;
+#pragma unroll
+      for (int i = 1; i < kEL; ++i) top = fmaxf(top, v[i]);
 #pragma unroll
       for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
-      for (int e = lane; e < a.E; e += 64) sum += expf(l[e] - top);
 #pragma unroll
-      for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
-      for (int e = lane; e < a.Ep; e += 64) row[e] = e < a.E ? -(expf(l[e] - top) / sum) * s : 0.f;
+      for (int i = 0; i < kEL; ++i) {
+        v[i] = expf(v[i] - top);  // 0 past the last expert
+        sum += v[i];
+      }
+      sum = lane_sum(sum, 6);
+#pragma unroll
+      for (int i = 0; i < kEL; ++i) v[i] = -(v[i] / sum) * s;
     }
+    // the selected experts' own values, through LDS to the lanes that hold them
+#pragma unroll
+    for (int i = 0; i < kEL; ++i)
+      if (lane + 64 * i < a.Ep) row[lane + 64 * i] = v[i];
     __builtin_amdgcn_wave_barrier();
     if (id >= 0) row[id] = w * (dw - s);
     __builtin_amdgcn_wave_barrier();
     if (a.dlogits)
-      for (int e = lane; e < a.E; e += 64) row[e] += a.dlogits[t * a.E + e];
+#pragma unroll
+      for (int i = 0; i < kEL; ++i)
+        if (lane + 64 * i < a.E) row[lane + 64 * i] += add[i];
+  } else {
+    for (int e = lane; e < a.Ep; e += 64) row[e] = 0.f;
   }
   __syncthreads();
   // rows: two parts
   const int64_t plane = a.Tp * a.Ep;
-  for (int i = threadIdx.x; i < kRbTokens * a.Ep / 2; i += 256) {
+  for (int i = threadIdx.x; i < kRbTokens * a.Ep / 2; i += 64 * kRbTokens) {
     const int r = i / (a.Ep / 2), e = i % (a.Ep / 2) * 2;
     const float v0 = g[r * ld + e], v1 = g[r * ld + e + 1];
     const uint32_t hi = pack_bf16x2(v0, v1);
@@ -100,7 +119,7 @@ __global__ __launch_bounds__(256) void k_route_dlogits(RouteBackDev a) {
     dst[plane / 2] = lo;
   }
   // columns: three parts, eight tokens at a time
-  for (int i = threadIdx.x; i < a.Ep * (kRbTokens / 8); i += 256) {
+  for (int i = threadIdx.x; i < a.Ep * (kRbTokens / 8); i += 64 * kRbTokens) {
     const int e = i / (kRbTokens / 8), r = i % (kRbTokens / 8) * 8;
     u32x4_t p[3];
 #pragma unroll
@@ -118,58 +137,75 @@ __global__ __launch_bounds__(256) void k_route_dlogits(RouteBackDev a) {
   }
 }
 
-// rows r0 .. r0 + 7 (clamped to the last) of 8 columns -> for each column its eight k
-__device__ __forceinline__ void load_transposed(const uint16_t* m, int64_t r0, int64_t last, int64_t stride,
-                                                bf16x8_t (&col)[8]) {
+// Eight rows, r0 .. r0 + 7 (clamped to the last), of a lane's eight columns ...
+struct Block8 {
   u32x4_t row[8];
+};
+__device__ __forceinline__ Block8 load_block8(const uint16_t* m, int64_t r0, int64_t last, int64_t stride) {
+  Block8 b;
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
     const int64_t q = r0 + r < last ? r0 + r : last;
-    row[r] = *reinterpret_cast<const u32x4_t*>(m + q * stride);
+    b.row[r] = *reinterpret_cast<const u32x4_t*>(m + q * stride);
   }
+  return b;
+}
+// ... and column c of them, as eight k of an MFMA operand
+__device__ __forceinline__ bf16x8_t column(const Block8& b, int c) {
+  u32x4_t v;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    u32x4_t v;
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-      v[p] = __builtin_amdgcn_perm(row[2 * p + 1][c >> 1], row[2 * p][c >> 1], (c & 1) ? 0x07060302u : 0x05040100u);
-    col[c] = as_bf16x8(v);
-  }
+  for (int p = 0; p < 4; ++p)
+    v[p] = __builtin_amdgcn_perm(b.row[2 * p + 1][c >> 1], b.row[2 * p][c >> 1], (c & 1) ? 0x07060302u : 0x05040100u);
+  return as_bf16x8(v);
 }
 
+constexpr int kRbWaves = 8;  // per workgroup of the products
+typedef float rb_sums_t[16][kRbCols + 4];
+
 // dW: a workgroup sums 16 EB experts x 128 columns over its share of the tokens, its
-// four wavefronts each over steps of 32 tokens of their own
+// wavefronts each over steps of 32 tokens of their own; they meet in LDS.
 template <int EB>
-__global__ __launch_bounds__(256) void k_route_dw(RouteBackDev a) {
-  __shared__ float sums[4][16][kRbCols + 4];
+__device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, rb_sums_t* sums) {
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   const int n = lane & 15, kq = lane >> 4;
-  const int c0 = blockIdx.x * kRbCols;
-  const int e0 = blockIdx.y * 16 * EB;
-  const int split = blockIdx.z;
+  const int chunks = (a.d + kRbCols - 1) / kRbCols, tiles = (a.E + 16 * EB - 1) / (16 * EB);
+  const int c0 = block % chunks * kRbCols;
+  const int e0 = block / chunks % tiles * 16 * EB;
+  const int split = block / chunks / tiles;
   const int col = c0 + 8 * n < a.d ? c0 + 8 * n : 0;  // columns past the end: summed and not stored
   const int64_t steps = a.Tp / 32, plane = a.Tp * a.Ep;
+  const int64_t stride = (int64_t)kRbWaves * a.splits;
   f32x4_t acc[EB][8];
 #pragma unroll
   for (int b = 0; b < EB; ++b)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int64_t st = split * 4 + wave; st < steps; st += 4 * a.splits) {
-    bf16x8_t xf[8];
-    load_transposed(a.x + col, st * 32 + 8 * kq, a.T - 1, a.d, xf);
+  int64_t st = split * kRbWaves + wave;
+  Block8 next;
+  if (st < steps) next = load_block8(a.x + col, st * 32 + 8 * kq, a.T - 1, a.d);
+  for (; st < steps; st += stride) {
+    const Block8 x = next;
+    u32x4_t gf[EB][3];
 #pragma unroll
     for (int b = 0; b < EB; ++b)
 #pragma unroll
-      for (int s = 0; s < 3; ++s) {
-        const bf16x8_t gf = as_bf16x8(*reinterpret_cast<const u32x4_t*>(
-            a.g_cols + s * plane + (int64_t)(e0 + 16 * b + n) * a.Tp + st * 32 + 8 * kq));
+      for (int s = 0; s < 3; ++s)
+        gf[b][s] = *reinterpret_cast<const u32x4_t*>(a.g_cols + s * plane + (int64_t)(e0 + 16 * b + n) * a.Tp +
+                                                     st * 32 + 8 * kq);
+    if (st + stride < steps) next = load_block8(a.x + col, (st + stride) * 32 + 8 * kq, a.T - 1, a.d);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[b][i] = mfma16x16x32(gf, xf[i], acc[b][i]);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const bf16x8_t xf = column(x, i);
+#pragma unroll
+      for (int b = 0; b < EB; ++b)
+#pragma unroll
+        for (int s = 0; s < 3; ++s) acc[b][i] = mfma16x16x32(as_bf16x8(gf[b][s]), xf, acc[b][i]);
+    }
   }
   float* out = a.splits > 1 ? a.part + (int64_t)split * a.E * a.d : a.dw;
 #pragma unroll
   for (int b = 0; b < EB; ++b) {
+    if (e0 + 16 * b >= a.E) break;
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -178,56 +214,80 @@ __global__ __launch_bounds__(256) void k_route_dw(RouteBackDev a) {
       *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{acc[b][4][q], acc[b][5][q], acc[b][6][q], acc[b][7][q]};
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * kRbCols / 4; i += 256) {
-      const int r = i / (kRbCols / 4), c = i % (kRbCols / 4) * 4;
-      const int e = e0 + 16 * b + r;
-      if (e >= a.E || c0 + c >= a.d) continue;
+    static_assert(kRbWaves * 64 == 16 * kRbCols / 4, "four columns of a row per thread");
+    const int r = threadIdx.x / (kRbCols / 4), c = threadIdx.x % (kRbCols / 4) * 4;
+    const int e = e0 + 16 * b + r;
+    if (e < a.E && c0 + c < a.d) {
       f32x4_t v = *reinterpret_cast<const f32x4_t*>(&sums[0][r][c]);
 #pragma unroll
-      for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const f32x4_t*>(&sums[w][r][c]);
+      for (int w = 1; w < kRbWaves; ++w) v += *reinterpret_cast<const f32x4_t*>(&sums[w][r][c]);
       *reinterpret_cast<f32x4_t*>(out + (int64_t)e * a.d + c0 + c) = v;
     }
   }
 }
 
-__global__ __launch_bounds__(256) void k_route_dw_sum(const float* part, int splits, int64_t count, float* dw) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= count) return;
-  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4_t*>(part + s * count + i);
-  *reinterpret_cast<f32x4_t*>(dw + i) = v;
-}
-
-// dx: a wavefront computes 64 tokens x 128 columns
-__global__ __launch_bounds__(256) void k_route_dx(RouteBackDev a) {
+// dx: a wavefront computes 16 kRbTokenBlocks tokens x 128 columns, 32 experts a step.
+__device__ __forceinline__ void route_dx(const RouteBackDev& a, int block) {
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   const int n = lane & 15, kq = lane >> 4;
-  const int c0 = blockIdx.y * kRbCols;
-  const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 16 * kRbTokenBlocks;
+  const int chunks = (a.d + kRbCols - 1) / kRbCols;
+  const int c0 = block % chunks * kRbCols;
+  const int64_t t0 = ((int64_t)(block / chunks) * kRbWaves + wave) * 16 * kRbTokenBlocks;
   if (t0 >= a.T) return;
-  const int col = c0 + 8 * n < a.d ? c0 + 8 * n : 0;
+  const bool stored = c0 + 8 * n < a.d;
+  const int col = stored ? c0 + 8 * n : 0;
   const int64_t plane = a.Tp * a.Ep;
+  u32x4_t add[kRbTokenBlocks][4];
+#pragma unroll
+  for (int b = 0; b < kRbTokenBlocks; ++b)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t t = t0 + 16 * b + 4 * kq + q;
+      add[b][q] = u32x4_t{0, 0, 0, 0};
+      if (a.dx_add) add[b][q] = *reinterpret_cast<const u32x4_t*>(a.dx_add + (t < a.T ? t : a.T - 1) * a.d + col);
+    }
   f32x4_t acc[kRbTokenBlocks][8];
 #pragma unroll
   for (int b = 0; b < kRbTokenBlocks; ++b)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int e = 0; e < a.Ep; e += 32) {
-    bf16x8_t wf[8];
-    load_transposed(a.w + col, e + 8 * kq, a.E - 1, a.d, wf);
+  const uint16_t* grow[kRbTokenBlocks];
 #pragma unroll
-    for (int b = 0; b < kRbTokenBlocks; ++b) {
-      const int64_t t = t0 + 16 * b + n < a.Tp ? t0 + 16 * b + n : a.Tp - 1;
-      const uint16_t* p = a.g_rows + t * a.Ep + e + 8 * kq;
+  for (int b = 0; b < kRbTokenBlocks; ++b) {
+    const int64_t t = t0 + 16 * b + n;
+    grow[b] = a.g_rows + (t < a.Tp ? t : a.Tp - 1) * a.Ep + 8 * kq;
+  }
+  const int last = (a.E + 31) / 32 * 32;
+  Block8 next = load_block8(a.w + col, 8 * kq, a.E - 1, a.d);
+  u32x4_t gnext[kRbTokenBlocks][2];
+  auto request = [&](int e) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const bf16x8_t gf = as_bf16x8(*reinterpret_cast<const u32x4_t*>(p + s * plane));
+    for (int b = 0; b < kRbTokenBlocks; ++b)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[b][i] = mfma16x16x32(gf, wf[i], acc[b][i]);
-      }
+      for (int s = 0; s < 2; ++s) gnext[b][s] = *reinterpret_cast<const u32x4_t*>(grow[b] + e + s * plane);
+  };
+  request(0);
+  for (int e = 0; e < last; e += 32) {
+    const Block8 w = next;
+    u32x4_t gf[kRbTokenBlocks][2];
+#pragma unroll
+    for (int b = 0; b < kRbTokenBlocks; ++b)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) gf[b][s] = gnext[b][s];
+    if (e + 32 < last) {
+      next = load_block8(a.w + col, e + 32 + 8 * kq, a.E - 1, a.d);
+      request(e + 32);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bf16x8_t wf = column(w, i);
+#pragma unroll
+      for (int b = 0; b < kRbTokenBlocks; ++b)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) acc[b][i] = mfma16x16x32(as_bf16x8(gf[b][s]), wf, acc[b][i]);
     }
   }
-  if (c0 + 8 * n >= a.d) return;
+  if (!stored) return;
 #pragma unroll
   for (int b = 0; b < kRbTokenBlocks; ++b)
 #pragma unroll
@@ -236,19 +296,33 @@ __global__ __launch_bounds__(256) void k_route_dx(RouteBackDev a) {
       if (t >= a.T) continue;
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = acc[b][i][q];
-      const int64_t at = t * a.d + c0 + 8 * n;
-      if (a.dx_add) {
-        const u32x4_t add = *reinterpret_cast<const u32x4_t*>(a.dx_add + at);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[i] += __uint_as_float((i & 1) ? (add[i >> 1] & 0xFFFF0000u) : (add[i >> 1] << 16));
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t p = add[b][q][i >> 1];
+        v[i] = acc[b][i][q] + __uint_as_float((i & 1) ? (p & 0xFFFF0000u) : (p << 16));
       }
       u32x4_t o;
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      *reinterpret_cast<u32x4_t*>(a.dx + at) = o;
+      *reinterpret_cast<u32x4_t*>(a.dx + t * a.d + c0 + 8 * n) = o;
     }
+}
+
+// Both products in one launch: the first dw_blocks workgroups sum dW, the others dx.
+template <int EB>
+__global__ __launch_bounds__(64 * kRbWaves) void k_route_products(RouteBackDev a, int dw_blocks) {
+  __shared__ rb_sums_t sums[kRbWaves];
+  if ((int)blockIdx.x < dw_blocks)
+    route_dw<EB>(a, blockIdx.x, sums);
+  else
+    route_dx(a, blockIdx.x - dw_blocks);
+}
+
+__global__ __launch_bounds__(256) void k_route_dw_sum(const float* part, int splits, int64_t count, float* dw) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= count) return;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4_t*>(part + s * count + i);
+  *reinterpret_cast<f32x4_t*>(dw + i) = v;
 }
 
 __global__ __launch_bounds__(256) void k_zero(float* p, int64_t count) {
@@ -267,7 +341,7 @@ static RouteBackPlan route_back_plan(int T, int d, int E) {
   p.Ep = E <= 32 ? 32 : (int)ceil_div(E, 64) * 64;
   p.EB = E <= 16 ? 1 : E <= 32 ? 2 : 4;
   const int64_t tiles = ceil_div(d, kRbCols) * ceil_div(E, 16 * p.EB);
-  const int64_t most = std::max<int64_t>(1, ceil_div(p.Tp / 32, 4));
+  const int64_t most = std::max<int64_t>(1, ceil_div(p.Tp / 32, kRbWaves));
   p.splits = (int)std::min<int64_t>(most, std::max<int64_t>(1, ceil_div(256, tiles)));
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
   p.rows_bytes = up(2 * p.Tp * p.Ep * 2);
@@ -343,25 +417,34 @@ extern "C" int moe_route_backward(const moe_route_backward_args* a, void* stream
   v.part = reinterpret_cast<float*>(ws + p.rows_bytes + p.cols_bytes);
   v.splits = p.splits;
   timing_begin(K_ROUTE_BWD, s);
-  hipLaunchKernelGGL(k_route_dlogits, dim3((unsigned)(p.Tp / kRbTokens)), dim3(256),
-                     kRbTokens * rb_row_floats(p.Ep) * sizeof(float), s, v);
-  const unsigned chunks = (unsigned)ceil_div(a->d, kRbCols);
-  if (a->dw_router) {
-    const dim3 grid(chunks, (unsigned)ceil_div(a->E, 16 * p.EB), (unsigned)p.splits);
-    if (p.EB == 1)
-      hipLaunchKernelGGL(k_route_dw<1>, grid, dim3(256), 0, s, v);
-    else if (p.EB == 2)
-      hipLaunchKernelGGL(k_route_dw<2>, grid, dim3(256), 0, s, v);
-    else
-      hipLaunchKernelGGL(k_route_dw<4>, grid, dim3(256), 0, s, v);
-    if (p.splits > 1) {
-      const int64_t count = (int64_t)a->E * a->d;
-      hipLaunchKernelGGL(k_route_dw_sum, dim3((unsigned)ceil_div(count, 1024)), dim3(256), 0, s, v.part, p.splits,
-                         count, a->dw_router);
-    }
+  const int per_lane = (int)ceil_div(p.Ep, 64);
+  auto dlogits = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.Tp / kRbTokens)), dim3(64 * kRbTokens),
+                       kRbTokens * rb_row_floats(p.Ep) * sizeof(float), s, v);
+  };
+  if (per_lane <= 1)
+    dlogits(k_route_dlogits<1>);
+  else if (per_lane <= 4)
+    dlogits(k_route_dlogits<4>);
+  else
+    dlogits(k_route_dlogits<16>);
+  const int64_t chunks = ceil_div(a->d, kRbCols);
+  const int64_t dw_blocks = a->dw_router ? chunks * ceil_div(a->E, 16 * p.EB) * p.splits : 0;
+  const int64_t dx_blocks = a->dx ? chunks * ceil_div(a->T, 16 * kRbTokenBlocks * kRbWaves) : 0;
+  auto products = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(dw_blocks + dx_blocks)), dim3(64 * kRbWaves), 0, s, v, (int)dw_blocks);
+  };
+  if (p.EB == 1)
+    products(k_route_products<1>);
+  else if (p.EB == 2)
+    products(k_route_products<2>);
+  else
+    products(k_route_products<4>);
+  if (a->dw_router && p.splits > 1) {
+    const int64_t count = (int64_t)a->E * a->d;
+    hipLaunchKernelGGL(k_route_dw_sum, dim3((unsigned)ceil_div(count, 1024)), dim3(256), 0, s, v.part, p.splits, count,
+                       a->dw_router);
   }
-  if (a->dx)
-    hipLaunchKernelGGL(k_route_dx, dim3((unsigned)ceil_div(a->T, 64 * kRbTokenBlocks), chunks), dim3(256), 0, s, v);
   timing_end(K_ROUTE_BWD, s);
   return check_launch("moe_route_backward");
 }
