@@ -12,45 +12,43 @@
 // bytes (eight columns), and v_perm pairs the rows, which transposes the 8 x 8 block in
 // registers.  MFMA i of eight then has column 8n + i as its column n, so a lane ends with
 // eight consecutive columns of the result.
+//
+// G itself: with the softmax over the selected experts and no loss on the logits it has k
+// values per token, and each wavefront builds the 32-token tiles it needs in its part of
+// LDS from the pairs; otherwise a first launch writes G in float32 and the tiles are read.
 #include "rows.hpp"
 
 namespace moe {
 
-constexpr int kRbTokens = 16;      // tokens per workgroup of the logits' gradient
-constexpr int kRbCols = 128;       // columns of d per wavefront
-constexpr int kRbTokenBlocks = 2;  // token blocks of 16 per wavefront of dx
+constexpr int kRbCols = 128;   // columns of d per wavefront
+constexpr int kRbWaves = 8;    // wavefronts per workgroup of the products
+constexpr int kRbTile = 64;    // experts of a tile of G
+constexpr int kRbTileLd = 68;  // floats per token of a tile: rows stay 16-byte aligned
+constexpr int kRbTokenBlocks = 2;  // token blocks of 16 per wavefront of dx: one tile
+static_assert(MOE_MAX_TOPK <= 16, "a lane holds every other pair of its token, at most eight");
 
 struct RouteBackDev {
   const uint16_t *x, *w;
   int T, d, E, k, renormalize;
   int64_t Tp;  // T rounded up to 32
-  int Ep;      // E rounded up to 32 (E <= 32) or 64
+  int Ep;      // E rounded up to 64
   const float* logits;
   const int32_t* ids;
   const float *weights, *dweights, *dlogits;
   const uint16_t* dx_add;
   uint16_t* dx;
   float* dw;
-  uint16_t* g_rows;  // [2][Tp][Ep]: G in two bf16 parts
-  uint16_t* g_cols;  // [3][Ep][Tp]: G^T in three
-  float* part;       // [splits][E][d] or null
+  float* g;     // [Tp][Ep] G, or null: built from the pairs
+  float* part;  // [splits][E][d] or null
   int splits;
 };
 
-// floats per token in LDS: odd, so that a column's tokens lie in different banks, but
-// at most 64 KiB for all tokens
-__host__ __device__ inline int rb_row_floats(int Ep) { return Ep < 1024 ? Ep + 1 : Ep; }
-static_assert(kRbTokens * 1024 * 4 <= 65536 && MOE_MAX_EXPERTS <= 1024, "LDS of k_route_dlogits");
-
-// The gradient of the logits of kRbTokens tokens, split and stored both ways: a wavefront
-// per token, its E <= 64 kEL logits (read once) in the lanes' registers.
+// G of four tokens, a wavefront each, its E <= 64 kEL logits (read once) in the lanes'
+// registers.
 template <int kEL>
-__global__ __launch_bounds__(64 * kRbTokens) void k_route_dlogits(RouteBackDev a) {
-  extern __shared__ float g[];  // [kRbTokens][ld]
-  const int lane = lane_id(), wave = threadIdx.x >> 6;
-  const int64_t t0 = (int64_t)blockIdx.x * kRbTokens, t = t0 + wave;
-  const int ld = rb_row_floats(a.Ep);
-  float* row = g + wave * ld;
+__global__ __launch_bounds__(256) void k_route_dlogits(RouteBackDev a) {
+  const int lane = lane_id();
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   float v[kEL];
 #pragma unroll
   for (int i = 0; i < kEL; ++i) v[i] = 0.f;
@@ -92,48 +90,121 @@ __global__ __launch_bounds__(64 * kRbTokens) void k_route_dlogits(RouteBackDev a
 #pragma unroll
       for (int i = 0; i < kEL; ++i) v[i] = -(v[i] / sum) * s;
     }
-    // the selected experts' own values, through LDS to the lanes that hold them
+    // the selected experts' own values, to the lanes that hold them
+    const float own = w * (dw - s);
+    for (int j = 0; j < a.k; ++j) {
+      const int e = __builtin_amdgcn_readlane(id, j);
+      const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(own), j));
 #pragma unroll
-    for (int i = 0; i < kEL; ++i)
-      if (lane + 64 * i < a.Ep) row[lane + 64 * i] = v[i];
-    __builtin_amdgcn_wave_barrier();
-    if (id >= 0) row[id] = w * (dw - s);
-    __builtin_amdgcn_wave_barrier();
-    if (a.dlogits)
-#pragma unroll
-      for (int i = 0; i < kEL; ++i)
-        if (lane + 64 * i < a.E) row[lane + 64 * i] += add[i];
-  } else {
-    for (int e = lane; e < a.Ep; e += 64) row[e] = 0.f;
-  }
-  __syncthreads();
-  // rows: two parts
-  const int64_t plane = a.Tp * a.Ep;
-  for (int i = threadIdx.x; i < kRbTokens * a.Ep / 2; i += 64 * kRbTokens) {
-    const int r = i / (a.Ep / 2), e = i % (a.Ep / 2) * 2;
-    const float v0 = g[r * ld + e], v1 = g[r * ld + e + 1];
-    const uint32_t hi = pack_bf16x2(v0, v1);
-    const uint32_t lo = pack_bf16x2(v0 - __uint_as_float(hi << 16), v1 - __uint_as_float(hi & 0xFFFF0000u));
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.g_rows + (t0 + r) * a.Ep + e);
-    dst[0] = hi;
-    dst[plane / 2] = lo;
-  }
-  // columns: three parts, eight tokens at a time
-  for (int i = threadIdx.x; i < a.Ep * (kRbTokens / 8); i += 64 * kRbTokens) {
-    const int e = i / (kRbTokens / 8), r = i % (kRbTokens / 8) * 8;
-    u32x4_t p[3];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float v0 = g[(r + 2 * q) * ld + e], v1 = g[(r + 2 * q + 1) * ld + e];
-#pragma unroll
-      for (int s = 0; s < 3; ++s) {
-        p[s][q] = pack_bf16x2(v0, v1);
-        v0 -= __uint_as_float(p[s][q] << 16);
-        v1 -= __uint_as_float(p[s][q] & 0xFFFF0000u);
-      }
+      for (int i = 0; i < kEL; ++i) v[i] = e == lane + 64 * i ? o : v[i];
     }
 #pragma unroll
-    for (int s = 0; s < 3; ++s) *reinterpret_cast<u32x4_t*>(a.g_cols + s * plane + e * a.Tp + t0 + r) = p[s];
+    for (int i = 0; i < kEL; ++i) v[i] += add[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kEL; ++i)
+    if (lane + 64 * i < a.Ep) a.g[t * a.Ep + lane + 64 * i] = v[i];
+}
+
+// What a wavefront needs to build tiles of 32 tokens: two lanes per token, each with
+// every other of its pairs.  The tokens' pairs lie one after the other: they are loaded
+// in that order (whole cache lines) and dealt out through the wavefront's tile.
+// (LDS operations of one wavefront take effect in order.)
+struct TilePairs {
+  int id[8];
+  float g[8];
+};
+struct PairLoads {
+  int id[8];
+  float w[8], g[8];
+};
+__device__ __forceinline__ PairLoads request_pairs(const RouteBackDev& a, int64_t t0) {
+  PairLoads r;
+  const int64_t base = t0 * a.k, last = (int64_t)a.T * a.k - 1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (2 * i >= a.k) break;  // (32 k pairs)
+    int64_t at = base + 64 * i + lane_id();
+    at = at < last ? at : last;
+    r.id[i] = a.ids[at];
+    r.w[i] = a.weights[at];
+    r.g[i] = a.dweights[at];
+  }
+  return r;
+}
+__device__ __forceinline__ TilePairs deal_pairs(const RouteBackDev& a, const PairLoads& r, int64_t t0, float* tile) {
+  const int lane = lane_id();
+  float* stage_w = tile + 32 * MOE_MAX_TOPK;
+  float* stage_g = stage_w + 32 * MOE_MAX_TOPK;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (2 * i >= a.k) break;
+    reinterpret_cast<int*>(tile)[64 * i + lane] = r.id[i];
+    stage_w[64 * i + lane] = r.w[i];
+    stage_g[64 * i + lane] = r.g[i];
+  }
+  __builtin_amdgcn_wave_barrier();
+  TilePairs p;
+  const bool live = t0 + (lane >> 1) < a.T;
+  float w[8], s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    p.id[i] = -1;
+    w[i] = p.g[i] = 0.f;
+    if (2 * i >= a.k) continue;
+    const int j = (lane & 1) + 2 * i, at = (lane >> 1) * a.k + (j < a.k ? j : 0);
+    const int id = reinterpret_cast<const int*>(tile)[at];
+    const bool there = live && j < a.k && id >= 0 && id < a.E;
+    p.id[i] = there ? id : -1;
+    w[i] = there ? stage_w[at] : 0.f;
+    p.g[i] = there ? stage_g[at] : 0.f;
+    s = fmaf(w[i], p.g[i], s);
+  }
+  s = lane_sum(s, 1);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p.g[i] = w[i] * (p.g[i] - s);
+  __builtin_amdgcn_wave_barrier();
+  return p;
+}
+static_assert(3 * 32 * MOE_MAX_TOPK <= 32 * kRbTileLd, "the pairs' staging lies in the tile");
+
+// G of 32 tokens and experts e0 .. e0 + 63 into the wavefront's tile.
+__device__ __forceinline__ void fill_tile(const RouteBackDev& a, float* tile, const TilePairs& p, int64_t t0, int e0) {
+  const int lane = lane_id();
+  f32x4_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int r = lane >> 4, c = (lane & 15) * 4;
+  if (a.g) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const f32x4_t*>(a.g + (t0 + 4 * i + r) * a.Ep + e0 + c);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) *reinterpret_cast<f32x4_t*>(tile + (4 * i + r) * kRbTileLd + c) = v[i];
+  __builtin_amdgcn_wave_barrier();
+  if (!a.g) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = p.id[i] - e0;
+      if (p.id[i] >= 0 && e >= 0 && e < kRbTile) tile[(lane >> 1) * kRbTileLd + e] = p.g[i];
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// eight float32 values as kParts bf16 operands whose sum they are
+template <int kParts>
+__device__ __forceinline__ void split_parts(float (&v)[8], bf16x8_t (&part)[kParts]) {
+#pragma unroll
+  for (int s = 0; s < kParts; ++s) {
+    u32x4_t q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      q[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      v[2 * i] -= __uint_as_float(q[i] << 16);
+      v[2 * i + 1] -= __uint_as_float(q[i] & 0xFFFF0000u);
+    }
+    part[s] = as_bf16x8(q);
   }
 }
 
@@ -159,13 +230,16 @@ __device__ __forceinline__ bf16x8_t column(const Block8& b, int c) {
   return as_bf16x8(v);
 }
 
-constexpr int kRbWaves = 8;  // per workgroup of the products
-typedef float rb_sums_t[16][kRbCols + 4];
+// LDS of a workgroup: the wavefronts' tiles, then (dW) their sums
+union alignas(16) RouteBackLds {
+  float tile[kRbWaves][32 * kRbTileLd];
+  float sums[kRbWaves][16][kRbCols + 4];
+};
 
 // dW: a workgroup sums 16 EB experts x 128 columns over its share of the tokens, its
 // wavefronts each over steps of 32 tokens of their own; they meet in LDS.
 template <int EB>
-__device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, rb_sums_t* sums) {
+__device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, RouteBackLds& lds) {
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   const int n = lane & 15, kq = lane >> 4;
   const int chunks = (a.d + kRbCols - 1) / kRbCols, tiles = (a.E + 16 * EB - 1) / (16 * EB);
@@ -173,33 +247,35 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, rb_su
   const int e0 = block / chunks % tiles * 16 * EB;
   const int split = block / chunks / tiles;
   const int col = c0 + 8 * n < a.d ? c0 + 8 * n : 0;  // columns past the end: summed and not stored
-  const int64_t steps = a.Tp / 32, plane = a.Tp * a.Ep;
-  const int64_t stride = (int64_t)kRbWaves * a.splits;
+  const int64_t steps = a.Tp / 32;
+  float* tile = lds.tile[wave];
   f32x4_t acc[EB][8];
 #pragma unroll
   for (int b = 0; b < EB; ++b)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  int64_t st = split * kRbWaves + wave;
-  Block8 next;
-  if (st < steps) next = load_block8(a.x + col, st * 32 + 8 * kq, a.T - 1, a.d);
-  for (; st < steps; st += stride) {
-    const Block8 x = next;
-    u32x4_t gf[EB][3];
+  for (int64_t st = split * kRbWaves + wave; st < steps; st += (int64_t)kRbWaves * a.splits) {
+    PairLoads r;
+    if (!a.g) r = request_pairs(a, st * 32);
+    const Block8 x = load_block8(a.x + col, st * 32 + 8 * kq, a.T - 1, a.d);
+    TilePairs p;
+    if (!a.g) p = deal_pairs(a, r, st * 32, tile);
+    fill_tile(a, tile, p, st * 32, e0);
+    bf16x8_t xf[8];
 #pragma unroll
-    for (int b = 0; b < EB; ++b)
+    for (int i = 0; i < 8; ++i) xf[i] = column(x, i);
 #pragma unroll
-      for (int s = 0; s < 3; ++s)
-        gf[b][s] = *reinterpret_cast<const u32x4_t*>(a.g_cols + s * plane + (int64_t)(e0 + 16 * b + n) * a.Tp +
-                                                     st * 32 + 8 * kq);
-    if (st + stride < steps) next = load_block8(a.x + col, (st + stride) * 32 + 8 * kq, a.T - 1, a.d);
+    for (int b = 0; b < EB; ++b) {
+      if (e0 + 16 * b >= a.E) break;
+      float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bf16x8_t xf = column(x, i);
+      for (int i = 0; i < 8; ++i) v[i] = tile[(8 * kq + i) * kRbTileLd + 16 * b + n];
+      bf16x8_t gf[3];
+      split_parts<3>(v, gf);
 #pragma unroll
-      for (int b = 0; b < EB; ++b)
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int s = 0; s < 3; ++s) acc[b][i] = mfma16x16x32(as_bf16x8(gf[b][s]), xf, acc[b][i]);
+        for (int s = 0; s < 3; ++s) acc[b][i] = mfma16x16x32(gf[s], xf[i], acc[b][i]);
     }
   }
   float* out = a.splits > 1 ? a.part + (int64_t)split * a.E * a.d : a.dw;
@@ -209,7 +285,7 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, rb_su
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      float* p = &sums[wave][4 * kq + q][8 * n];
+      float* p = &lds.sums[wave][4 * kq + q][8 * n];
       *reinterpret_cast<f32x4_t*>(p) = f32x4_t{acc[b][0][q], acc[b][1][q], acc[b][2][q], acc[b][3][q]};
       *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{acc[b][4][q], acc[b][5][q], acc[b][6][q], acc[b][7][q]};
     }
@@ -218,16 +294,16 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, rb_su
     const int r = threadIdx.x / (kRbCols / 4), c = threadIdx.x % (kRbCols / 4) * 4;
     const int e = e0 + 16 * b + r;
     if (e < a.E && c0 + c < a.d) {
-      f32x4_t v = *reinterpret_cast<const f32x4_t*>(&sums[0][r][c]);
+      f32x4_t v = *reinterpret_cast<const f32x4_t*>(&lds.sums[0][r][c]);
 #pragma unroll
-      for (int w = 1; w < kRbWaves; ++w) v += *reinterpret_cast<const f32x4_t*>(&sums[w][r][c]);
+      for (int w = 1; w < kRbWaves; ++w) v += *reinterpret_cast<const f32x4_t*>(&lds.sums[w][r][c]);
       *reinterpret_cast<f32x4_t*>(out + (int64_t)e * a.d + c0 + c) = v;
     }
   }
 }
 
-// dx: a wavefront computes 16 kRbTokenBlocks tokens x 128 columns, 32 experts a step.
-__device__ __forceinline__ void route_dx(const RouteBackDev& a, int block) {
+// dx: a wavefront computes 32 tokens x 128 columns, 32 experts a step.
+__device__ __forceinline__ void route_dx(const RouteBackDev& a, int block, RouteBackLds& lds) {
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   const int n = lane & 15, kq = lane >> 4;
   const int chunks = (a.d + kRbCols - 1) / kRbCols;
@@ -236,7 +312,10 @@ __device__ __forceinline__ void route_dx(const RouteBackDev& a, int block) {
   if (t0 >= a.T) return;
   const bool stored = c0 + 8 * n < a.d;
   const int col = stored ? c0 + 8 * n : 0;
-  const int64_t plane = a.Tp * a.Ep;
+  float* tile = lds.tile[wave];
+  PairLoads r;
+  if (!a.g) r = request_pairs(a, t0);
+  Block8 next = load_block8(a.w + col, 8 * kq, a.E - 1, a.d);
   u32x4_t add[kRbTokenBlocks][4];
 #pragma unroll
   for (int b = 0; b < kRbTokenBlocks; ++b)
@@ -251,32 +330,19 @@ __device__ __forceinline__ void route_dx(const RouteBackDev& a, int block) {
   for (int b = 0; b < kRbTokenBlocks; ++b)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const uint16_t* grow[kRbTokenBlocks];
-#pragma unroll
-  for (int b = 0; b < kRbTokenBlocks; ++b) {
-    const int64_t t = t0 + 16 * b + n;
-    grow[b] = a.g_rows + (t < a.Tp ? t : a.Tp - 1) * a.Ep + 8 * kq;
-  }
-  const int last = (a.E + 31) / 32 * 32;
-  Block8 next = load_block8(a.w + col, 8 * kq, a.E - 1, a.d);
-  u32x4_t gnext[kRbTokenBlocks][2];
-  auto request = [&](int e) {
-#pragma unroll
-    for (int b = 0; b < kRbTokenBlocks; ++b)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) gnext[b][s] = *reinterpret_cast<const u32x4_t*>(grow[b] + e + s * plane);
-  };
-  request(0);
-  for (int e = 0; e < last; e += 32) {
+  TilePairs p;
+  if (!a.g) p = deal_pairs(a, r, t0, tile);
+  for (int e = 0; e < a.E; e += 32) {
+    if (e % kRbTile == 0) fill_tile(a, tile, p, t0, e);
     const Block8 w = next;
-    u32x4_t gf[kRbTokenBlocks][2];
+    if (e + 32 < a.E) next = load_block8(a.w + col, e + 32 + 8 * kq, a.E - 1, a.d);
+    bf16x8_t gf[kRbTokenBlocks][2];
 #pragma unroll
-    for (int b = 0; b < kRbTokenBlocks; ++b)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) gf[b][s] = gnext[b][s];
-    if (e + 32 < last) {
-      next = load_block8(a.w + col, e + 32 + 8 * kq, a.E - 1, a.d);
-      request(e + 32);
+    for (int b = 0; b < kRbTokenBlocks; ++b) {
+      const float* row = tile + (16 * b + n) * kRbTileLd + e % kRbTile + 8 * kq;
+      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(row), hi = *reinterpret_cast<const f32x4_t*>(row + 4);
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      split_parts<2>(v, gf[b]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -284,7 +350,7 @@ __device__ __forceinline__ void route_dx(const RouteBackDev& a, int block) {
 #pragma unroll
       for (int b = 0; b < kRbTokenBlocks; ++b)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) acc[b][i] = mfma16x16x32(as_bf16x8(gf[b][s]), wf, acc[b][i]);
+        for (int s = 0; s < 2; ++s) acc[b][i] = mfma16x16x32(gf[b][s], wf, acc[b][i]);
     }
   }
   if (!stored) return;
@@ -297,8 +363,8 @@ __device__ __forceinline__ void route_dx(const RouteBackDev& a, int block) {
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t p = add[b][q][i >> 1];
-        v[i] = acc[b][i][q] + __uint_as_float((i & 1) ? (p & 0xFFFF0000u) : (p << 16));
+        const uint32_t p2 = add[b][q][i >> 1];
+        v[i] = acc[b][i][q] + __uint_as_float((i & 1) ? (p2 & 0xFFFF0000u) : (p2 << 16));
       }
       u32x4_t o;
 #pragma unroll
@@ -310,11 +376,11 @@ __device__ __forceinline__ void route_dx(const RouteBackDev& a, int block) {
 // Both products in one launch: the first dw_blocks workgroups sum dW, the others dx.
 template <int EB>
 __global__ __launch_bounds__(64 * kRbWaves) void k_route_products(RouteBackDev a, int dw_blocks) {
-  __shared__ rb_sums_t sums[kRbWaves];
+  __shared__ RouteBackLds lds;
   if ((int)blockIdx.x < dw_blocks)
-    route_dw<EB>(a, blockIdx.x, sums);
+    route_dw<EB>(a, blockIdx.x, lds);
   else
-    route_dx(a, blockIdx.x - dw_blocks);
+    route_dx(a, blockIdx.x - dw_blocks, lds);
 }
 
 __global__ __launch_bounds__(256) void k_route_dw_sum(const float* part, int splits, int64_t count, float* dw) {
@@ -331,23 +397,22 @@ __global__ __launch_bounds__(256) void k_zero(float* p, int64_t count) {
 }
 
 struct RouteBackPlan {
-  int64_t Tp, rows_bytes, cols_bytes, part_bytes, total;
+  int64_t Tp, g_bytes, part_bytes, total;
   int Ep, EB, splits;
 };
 
 static RouteBackPlan route_back_plan(int T, int d, int E) {
   RouteBackPlan p;
   p.Tp = ceil_div(T, 32) * 32;
-  p.Ep = E <= 32 ? 32 : (int)ceil_div(E, 64) * 64;
+  p.Ep = (int)ceil_div(E, kRbTile) * kRbTile;
   p.EB = E <= 16 ? 1 : E <= 32 ? 2 : 4;
   const int64_t tiles = ceil_div(d, kRbCols) * ceil_div(E, 16 * p.EB);
   const int64_t most = std::max<int64_t>(1, ceil_div(p.Tp / 32, kRbWaves));
   p.splits = (int)std::min<int64_t>(most, std::max<int64_t>(1, ceil_div(256, tiles)));
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
-  p.rows_bytes = up(2 * p.Tp * p.Ep * 2);
-  p.cols_bytes = up(3 * p.Tp * p.Ep * 2);
+  p.g_bytes = up(p.Tp * p.Ep * 4);
   p.part_bytes = p.splits > 1 ? up((int64_t)p.splits * E * d * 4) : 0;
-  p.total = p.rows_bytes + p.cols_bytes + p.part_bytes;
+  p.total = p.g_bytes + p.part_bytes;
   return p;
 }
 
@@ -412,22 +477,19 @@ extern "C" int moe_route_backward(const moe_route_backward_args* a, void* stream
   v.dx = a->dx;
   v.dw = a->dw_router;
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
-  v.g_rows = reinterpret_cast<uint16_t*>(ws);
-  v.g_cols = reinterpret_cast<uint16_t*>(ws + p.rows_bytes);
-  v.part = reinterpret_cast<float*>(ws + p.rows_bytes + p.cols_bytes);
+  v.g = a->renormalize && !a->dlogits ? nullptr : reinterpret_cast<float*>(ws);
+  v.part = reinterpret_cast<float*>(ws + p.g_bytes);
   v.splits = p.splits;
   timing_begin(K_ROUTE_BWD, s);
-  const int per_lane = (int)ceil_div(p.Ep, 64);
-  auto dlogits = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.Tp / kRbTokens)), dim3(64 * kRbTokens),
-                       kRbTokens * rb_row_floats(p.Ep) * sizeof(float), s, v);
-  };
-  if (per_lane <= 1)
-    dlogits(k_route_dlogits<1>);
-  else if (per_lane <= 4)
-    dlogits(k_route_dlogits<4>);
-  else
-    dlogits(k_route_dlogits<16>);
+  if (v.g) {
+    const dim3 grid((unsigned)(p.Tp / 4));
+    if (p.Ep <= 64)
+      hipLaunchKernelGGL(k_route_dlogits<1>, grid, dim3(256), 0, s, v);
+    else if (p.Ep <= 256)
+      hipLaunchKernelGGL(k_route_dlogits<4>, grid, dim3(256), 0, s, v);
+    else
+      hipLaunchKernelGGL(k_route_dlogits<16>, grid, dim3(256), 0, s, v);
+  }
   const int64_t chunks = ceil_div(a->d, kRbCols);
   const int64_t dw_blocks = a->dw_router ? chunks * ceil_div(a->E, 16 * p.EB) * p.splits : 0;
   const int64_t dx_blocks = a->dx ? chunks * ceil_div(a->T, 16 * kRbTokenBlocks * kRbWaves) : 0;
