@@ -24,7 +24,6 @@ constexpr int kRbCols = 128;   // columns of d per wavefront
 constexpr int kRbWaves = 8;    // wavefronts per workgroup of the products
 constexpr int kRbTile = 64;    // experts of a tile of G
 constexpr int kRbTileLd = 68;  // floats per token of a tile: rows stay 16-byte aligned
-constexpr int kRbTokenBlocks = 2;  // token blocks of 16 per wavefront of dx: one tile
 static_assert(MOE_MAX_TOPK <= 16, "a lane holds every other pair of its token, at most eight");
 
 struct RouteBackDev {
@@ -208,21 +207,28 @@ __device__ __forceinline__ void split_parts(float (&v)[8], bf16x8_t (&part)[kPar
   }
 }
 
-// Eight rows, r0 .. r0 + 7 (clamped to the last), of a lane's eight columns ...
-struct Block8 {
-  u32x4_t row[8];
+// Eight elements of row r at column `col`, by a uniform base and a 32-bit offset
+// (rows of up to 2^20 elements, at most 1024 of them).
+__device__ __forceinline__ u32x4_t load_words(const uint16_t* base, uint32_t r, uint32_t d, uint32_t col) {
+  return *(const MOE_GLOBAL u32x4_t*)((const MOE_GLOBAL char*)base + 2 * (r * d + col));
+}
+
+// Rows r0 .. r0 + 7 (clamped to the last) of a lane's eight columns ...
+struct Block {
+  uint32_t row[8][4];
 };
-__device__ __forceinline__ Block8 load_block8(const uint16_t* m, int64_t r0, int64_t last, int64_t stride) {
-  Block8 b;
+__device__ __forceinline__ Block load_block(const uint16_t* base, int r0, int last, int d, int col) {
+  Block b;
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
-    const int64_t q = r0 + r < last ? r0 + r : last;
-    b.row[r] = *reinterpret_cast<const u32x4_t*>(m + q * stride);
+    const u32x4_t v = load_words(base, r0 + r < last ? r0 + r : last, d, col);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b.row[r][i] = v[i];
   }
   return b;
 }
 // ... and column c of them, as eight k of an MFMA operand
-__device__ __forceinline__ bf16x8_t column(const Block8& b, int c) {
+__device__ __forceinline__ bf16x8_t column(const Block& b, int c) {
   u32x4_t v;
 #pragma unroll
   for (int p = 0; p < 4; ++p)
@@ -236,31 +242,117 @@ union alignas(16) RouteBackLds {
   float sums[kRbWaves][16][kRbCols + 4];
 };
 
-// dW: a workgroup sums 16 EB experts x 128 columns over its share of the tokens, its
-// wavefronts each over steps of 32 tokens of their own; they meet in LDS.
+// dx of a tile's 32 tokens in 128 columns: what is requested first ...
+struct DxLoads {
+  Block w;             // the first 32 experts
+  uint32_t add[2][4][4];  // dx_add of the lane's results
+};
+__device__ __forceinline__ DxLoads request_dx(const RouteBackDev& a, int64_t t0, int col) {
+  const int kq = lane_id() >> 4;
+  DxLoads r;
+  r.w = load_block(a.w, 8 * kq, a.E - 1, a.d, col);
+  const uint16_t* base = a.dx_add + t0 * a.d;
+  const int last = (int)(a.T - 1 - t0 < 31 ? a.T - 1 - t0 : 31);
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int t = 16 * b + 4 * kq + q;
+      u32x4_t v = {};
+      if (a.dx_add) v = load_words(base, t < last ? t : last, a.d, col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.add[b][q][i] = v[i];
+    }
+  return r;
+}
+// ... and the product, 32 experts a step.
+__device__ __forceinline__ void run_dx(const RouteBackDev& a, float* tile, const TilePairs& p, const DxLoads& r,
+                                       int64_t t0, int col, bool stored) {
+  const int lane = lane_id();
+  const int n = lane & 15, kq = lane >> 4;
+  f32x4_t acc[2][8];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  Block next = r.w;
+  for (int e = 0; e < a.E; e += 32) {
+    if (e % kRbTile == 0) fill_tile(a, tile, p, t0, e);
+    const Block w = next;
+    if (e + 32 < a.E) next = load_block(a.w, e + 32 + 8 * kq, a.E - 1, a.d, col);
+    bf16x8_t gf[2][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const float* row = tile + (16 * b + n) * kRbTileLd + e % kRbTile + 8 * kq;
+      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(row), hi = *reinterpret_cast<const f32x4_t*>(row + 4);
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      split_parts<2>(v, gf[b]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bf16x8_t wf = column(w, i);
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) acc[b][i] = mfma16x16x32(gf[b][s], wf, acc[b][i]);
+    }
+  }
+  if (!stored) return;
+  MOE_GLOBAL char* base = (MOE_GLOBAL char*)(a.dx + t0 * a.d);
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int t = 16 * b + 4 * kq + q;
+      if (t0 + t >= a.T) continue;
+      u32x4_t o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t add = r.add[b][q][i];
+        o[i] = pack_bf16x2(acc[b][2 * i][q] + __uint_as_float(add << 16),
+                           acc[b][2 * i + 1][q] + __uint_as_float(add & 0xFFFF0000u));
+      }
+      *(MOE_GLOBAL u32x4_t*)(base + 2 * ((uint32_t)t * (uint32_t)a.d + (uint32_t)col)) = o;
+    }
+}
+
+// dW: a workgroup sums 32 EB experts x 128 columns over its share of the tokens.  Its
+// wavefronts take half of the experts each, for steps of 32 tokens of their own (four
+// steps at a time); the four meet in LDS.
 template <int EB>
 __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, RouteBackLds& lds) {
-  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int n = lane & 15, kq = lane >> 4;
-  const int chunks = (a.d + kRbCols - 1) / kRbCols, tiles = (a.E + 16 * EB - 1) / (16 * EB);
+  const int half = wave & 1, group = wave >> 1;
+  const int chunks = (a.d + kRbCols - 1) / kRbCols, tiles = (a.E + 32 * EB - 1) / (32 * EB);
   const int c0 = block % chunks * kRbCols;
-  const int e0 = block / chunks % tiles * 16 * EB;
+  const int tile_e0 = block / chunks % tiles * 32 * EB, e0 = tile_e0 + half * 16 * EB;
   const int split = block / chunks / tiles;
   const int col = c0 + 8 * n < a.d ? c0 + 8 * n : 0;  // columns past the end: summed and not stored
-  const int64_t steps = a.Tp / 32;
+  const int64_t steps = a.Tp / 32, stride = (int64_t)(kRbWaves / 2) * a.splits;
   float* tile = lds.tile[wave];
   f32x4_t acc[EB][8];
 #pragma unroll
   for (int b = 0; b < EB; ++b)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int64_t st = split * kRbWaves + wave; st < steps; st += (int64_t)kRbWaves * a.splits) {
+  int64_t st = split * (kRbWaves / 2) + group;
+  auto load_x = [&](int64_t st) {
+    const int64_t left = a.T - 1 - st * 32;
+    return load_block(a.x + st * 32 * a.d, 8 * kq, (int)(left < 31 ? left : 31), a.d, col);
+  };
+  Block next;
+  if (st < steps) next = load_x(st);
+  for (; st < steps; st += stride) {
+    const int64_t t0 = st * 32;
     PairLoads r;
-    if (!a.g) r = request_pairs(a, st * 32);
-    const Block8 x = load_block8(a.x + col, st * 32 + 8 * kq, a.T - 1, a.d);
+    if (!a.g) r = request_pairs(a, t0);
+    const Block x = next;
     TilePairs p;
-    if (!a.g) p = deal_pairs(a, r, st * 32, tile);
-    fill_tile(a, tile, p, st * 32, e0);
+    if (!a.g) p = deal_pairs(a, r, t0, tile);
+    const int e_base = tile_e0 / kRbTile * kRbTile;  // the tile's first expert
+    fill_tile(a, tile, p, t0, e_base);
+    if (st + stride < steps) next = load_x(st + stride);
     bf16x8_t xf[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) xf[i] = column(x, i);
@@ -269,7 +361,7 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, Route
       if (e0 + 16 * b >= a.E) break;
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = tile[(8 * kq + i) * kRbTileLd + 16 * b + n];
+      for (int i = 0; i < 8; ++i) v[i] = tile[(8 * kq + i) * kRbTileLd + e0 - e_base + 16 * b + n];
       bf16x8_t gf[3];
       split_parts<3>(v, gf);
 #pragma unroll
@@ -281,7 +373,6 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, Route
   float* out = a.splits > 1 ? a.part + (int64_t)split * a.E * a.d : a.dw;
 #pragma unroll
   for (int b = 0; b < EB; ++b) {
-    if (e0 + 16 * b >= a.E) break;
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -290,90 +381,42 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, Route
       *reinterpret_cast<f32x4_t*>(p + 4) = f32x4_t{acc[b][4][q], acc[b][5][q], acc[b][6][q], acc[b][7][q]};
     }
     __syncthreads();
-    static_assert(kRbWaves * 64 == 16 * kRbCols / 4, "four columns of a row per thread");
-    const int r = threadIdx.x / (kRbCols / 4), c = threadIdx.x % (kRbCols / 4) * 4;
-    const int e = e0 + 16 * b + r;
-    if (e < a.E && c0 + c < a.d) {
-      f32x4_t v = *reinterpret_cast<const f32x4_t*>(&lds.sums[0][r][c]);
+    // both halves' 16 rows, four columns of two of them per thread
 #pragma unroll
-      for (int w = 1; w < kRbWaves; ++w) v += *reinterpret_cast<const f32x4_t*>(&lds.sums[w][r][c]);
-      *reinterpret_cast<f32x4_t*>(out + (int64_t)e * a.d + c0 + c) = v;
+    for (int h = 0; h < 2; ++h) {
+      static_assert(kRbWaves * 64 == 16 * kRbCols / 4, "four columns of a row per thread");
+      const int r = threadIdx.x / (kRbCols / 4), c = threadIdx.x % (kRbCols / 4) * 4;
+      const int e = tile_e0 + h * 16 * EB + 16 * b + r;
+      if (e < a.E && c0 + c < a.d) {
+        f32x4_t v = *reinterpret_cast<const f32x4_t*>(&lds.sums[h][r][c]);
+#pragma unroll
+        for (int w = 1; w < kRbWaves / 2; ++w) v += *reinterpret_cast<const f32x4_t*>(&lds.sums[2 * w + h][r][c]);
+        *reinterpret_cast<f32x4_t*>(out + (int64_t)e * a.d + c0 + c) = v;
+      }
     }
   }
 }
 
-// dx: a wavefront computes 32 tokens x 128 columns, 32 experts a step.
+// dx alone: a wavefront computes 32 tokens x 128 columns.
 __device__ __forceinline__ void route_dx(const RouteBackDev& a, int block, RouteBackLds& lds) {
-  const int lane = lane_id(), wave = threadIdx.x >> 6;
-  const int n = lane & 15, kq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int chunks = (a.d + kRbCols - 1) / kRbCols;
-  const int c0 = block % chunks * kRbCols;
-  const int64_t t0 = ((int64_t)(block / chunks) * kRbWaves + wave) * 16 * kRbTokenBlocks;
+  const int at = block % chunks * kRbCols + 8 * (lane_id() & 15);
+  const int64_t t0 = ((int64_t)(block / chunks) * kRbWaves + wave) * 32;
   if (t0 >= a.T) return;
-  const bool stored = c0 + 8 * n < a.d;
-  const int col = stored ? c0 + 8 * n : 0;
+  const int col = at < a.d ? at : 0;
   float* tile = lds.tile[wave];
   PairLoads r;
   if (!a.g) r = request_pairs(a, t0);
-  Block8 next = load_block8(a.w + col, 8 * kq, a.E - 1, a.d);
-  u32x4_t add[kRbTokenBlocks][4];
-#pragma unroll
-  for (int b = 0; b < kRbTokenBlocks; ++b)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t t = t0 + 16 * b + 4 * kq + q;
-      add[b][q] = u32x4_t{0, 0, 0, 0};
-      if (a.dx_add) add[b][q] = *reinterpret_cast<const u32x4_t*>(a.dx_add + (t < a.T ? t : a.T - 1) * a.d + col);
-    }
-  f32x4_t acc[kRbTokenBlocks][8];
-#pragma unroll
-  for (int b = 0; b < kRbTokenBlocks; ++b)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const DxLoads dx = request_dx(a, t0, col);
   TilePairs p;
   if (!a.g) p = deal_pairs(a, r, t0, tile);
-  for (int e = 0; e < a.E; e += 32) {
-    if (e % kRbTile == 0) fill_tile(a, tile, p, t0, e);
-    const Block8 w = next;
-    if (e + 32 < a.E) next = load_block8(a.w + col, e + 32 + 8 * kq, a.E - 1, a.d);
-    bf16x8_t gf[kRbTokenBlocks][2];
-#pragma unroll
-    for (int b = 0; b < kRbTokenBlocks; ++b) {
-      const float* row = tile + (16 * b + n) * kRbTileLd + e % kRbTile + 8 * kq;
-      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(row), hi = *reinterpret_cast<const f32x4_t*>(row + 4);
-      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      split_parts<2>(v, gf[b]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bf16x8_t wf = column(w, i);
-#pragma unroll
-      for (int b = 0; b < kRbTokenBlocks; ++b)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) acc[b][i] = mfma16x16x32(gf[b][s], wf, acc[b][i]);
-    }
-  }
-  if (!stored) return;
-#pragma unroll
-  for (int b = 0; b < kRbTokenBlocks; ++b)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t t = t0 + 16 * b + 4 * kq + q;
-      if (t >= a.T) continue;
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t p2 = add[b][q][i >> 1];
-        v[i] = acc[b][i][q] + __uint_as_float((i & 1) ? (p2 & 0xFFFF0000u) : (p2 << 16));
-      }
-      u32x4_t o;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      *reinterpret_cast<u32x4_t*>(a.dx + t * a.d + c0 + 8 * n) = o;
-    }
+  run_dx(a, tile, p, dx, t0, col, at < a.d);
 }
 
 // Both products in one launch: the first dw_blocks workgroups sum dW, the others dx.
+// (One workgroup that computes both from the same tiles ran slower, 36 against 23 us at
+// T = 4096, d = 2048, E = 64: the registers of the two add up and spill.)
 template <int EB>
 __global__ __launch_bounds__(64 * kRbWaves) void k_route_products(RouteBackDev a, int dw_blocks) {
   __shared__ RouteBackLds lds;
@@ -405,9 +448,9 @@ static RouteBackPlan route_back_plan(int T, int d, int E) {
   RouteBackPlan p;
   p.Tp = ceil_div(T, 32) * 32;
   p.Ep = (int)ceil_div(E, kRbTile) * kRbTile;
-  p.EB = E <= 16 ? 1 : E <= 32 ? 2 : 4;
-  const int64_t tiles = ceil_div(d, kRbCols) * ceil_div(E, 16 * p.EB);
-  const int64_t most = std::max<int64_t>(1, ceil_div(p.Tp / 32, kRbWaves));
+  p.EB = E <= 32 ? 1 : 2;
+  const int64_t tiles = ceil_div(d, kRbCols) * ceil_div(E, 32 * p.EB);
+  const int64_t most = std::max<int64_t>(1, ceil_div(p.Tp / 32, kRbWaves / 2));
   p.splits = (int)std::min<int64_t>(most, std::max<int64_t>(1, ceil_div(256, tiles)));
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
   p.g_bytes = up(p.Tp * p.Ep * 4);
@@ -491,17 +534,15 @@ extern "C" int moe_route_backward(const moe_route_backward_args* a, void* stream
       hipLaunchKernelGGL(k_route_dlogits<16>, grid, dim3(256), 0, s, v);
   }
   const int64_t chunks = ceil_div(a->d, kRbCols);
-  const int64_t dw_blocks = a->dw_router ? chunks * ceil_div(a->E, 16 * p.EB) * p.splits : 0;
-  const int64_t dx_blocks = a->dx ? chunks * ceil_div(a->T, 16 * kRbTokenBlocks * kRbWaves) : 0;
+  const int64_t dw_blocks = a->dw_router ? chunks * ceil_div(a->E, 32 * p.EB) * p.splits : 0;
+  const int64_t dx_blocks = a->dx ? chunks * ceil_div(a->T, 32 * kRbWaves) : 0;
   auto products = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)(dw_blocks + dx_blocks)), dim3(64 * kRbWaves), 0, s, v, (int)dw_blocks);
   };
   if (p.EB == 1)
     products(k_route_products<1>);
-  else if (p.EB == 2)
-    products(k_route_products<2>);
   else
-    products(k_route_products<4>);
+    products(k_route_products<2>);
   if (a->dw_router && p.splits > 1) {
     const int64_t count = (int64_t)a->E * a->d;
     hipLaunchKernelGGL(k_route_dw_sum, dim3((unsigned)ceil_div(count, 1024)), dim3(256), 0, s, v.part, p.splits, count,
