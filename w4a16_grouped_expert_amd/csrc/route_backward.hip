@@ -167,21 +167,32 @@ __device__ __forceinline__ TilePairs deal_pairs(const RouteBackDev& a, const Pai
 }
 static_assert(3 * 32 * MOE_MAX_TOPK <= 32 * kRbTileLd, "the pairs' staging lies in the tile");
 
-// G of 32 tokens and experts e0 .. e0 + 63 into the wavefront's tile.
-__device__ __forceinline__ void fill_tile(const RouteBackDev& a, float* tile, const TilePairs& p, int64_t t0, int e0) {
-  const int lane = lane_id();
+// G of 32 tokens and experts e0 .. e0 + 63: requested (kRows: a first launch has written
+// it) and put into the wavefront's tile.
+struct TileLoads {
   f32x4_t v[8];
+};
+template <bool kRows>
+__device__ __forceinline__ TileLoads request_tile(const RouteBackDev& a, int64_t t0, int e0) {
+  TileLoads r;
+  if (kRows) {
+    const MOE_GLOBAL char* base = (const MOE_GLOBAL char*)(a.g + t0 * a.Ep + e0);
+    const uint32_t at = (lane_id() >> 4) * a.Ep + (lane_id() & 15) * 4;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int r = lane >> 4, c = (lane & 15) * 4;
-  if (a.g) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const f32x4_t*>(a.g + (t0 + 4 * i + r) * a.Ep + e0 + c);
+    for (int i = 0; i < 8; ++i) r.v[i] = *(const MOE_GLOBAL f32x4_t*)(base + 4 * (at + 4 * i * (uint32_t)a.Ep));
   }
+  return r;
+}
+template <bool kRows>
+__device__ __forceinline__ void put_tile(const RouteBackDev& a, float* tile, const TilePairs& p, const TileLoads& r,
+                                         int e0) {
+  const int lane = lane_id();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) *reinterpret_cast<f32x4_t*>(tile + (4 * i + r) * kRbTileLd + c) = v[i];
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<f32x4_t*>(tile + (4 * i + (lane >> 4)) * kRbTileLd + (lane & 15) * 4) =
+        kRows ? r.v[i] : f32x4_t{0.f, 0.f, 0.f, 0.f};
   __builtin_amdgcn_wave_barrier();
-  if (!a.g) {
+  if (!kRows) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = p.id[i] - e0;
@@ -245,11 +256,14 @@ union alignas(16) RouteBackLds {
 // dx of a tile's 32 tokens in 128 columns: what is requested first ...
 struct DxLoads {
   Block w;             // the first 32 experts
+  TileLoads g;         // the first 64
   uint32_t add[2][4][4];  // dx_add of the lane's results
 };
+template <bool kRows>
 __device__ __forceinline__ DxLoads request_dx(const RouteBackDev& a, int64_t t0, int col) {
   const int kq = lane_id() >> 4;
   DxLoads r;
+  r.g = request_tile<kRows>(a, t0, 0);
   r.w = load_block(a.w, 8 * kq, a.E - 1, a.d, col);
   const uint16_t* base = a.dx_add + t0 * a.d;
   const int last = (int)(a.T - 1 - t0 < 31 ? a.T - 1 - t0 : 31);
@@ -266,6 +280,7 @@ __device__ __forceinline__ DxLoads request_dx(const RouteBackDev& a, int64_t t0,
   return r;
 }
 // ... and the product, 32 experts a step.
+template <bool kRows>
 __device__ __forceinline__ void run_dx(const RouteBackDev& a, float* tile, const TilePairs& p, const DxLoads& r,
                                        int64_t t0, int col, bool stored) {
   const int lane = lane_id();
@@ -276,8 +291,12 @@ __device__ __forceinline__ void run_dx(const RouteBackDev& a, float* tile, const
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   Block next = r.w;
+  TileLoads tile_next = r.g;
   for (int e = 0; e < a.E; e += 32) {
-    if (e % kRbTile == 0) fill_tile(a, tile, p, t0, e);
+    if (e % kRbTile == 0) {
+      put_tile<kRows>(a, tile, p, tile_next, e);
+      if (e + kRbTile < a.E) tile_next = request_tile<kRows>(a, t0, e + kRbTile);
+    }
     const Block w = next;
     if (e + 32 < a.E) next = load_block(a.w, e + 32 + 8 * kq, a.E - 1, a.d, col);
     bf16x8_t gf[2][2];
@@ -319,7 +338,7 @@ __device__ __forceinline__ void run_dx(const RouteBackDev& a, float* tile, const
 // dW: a workgroup sums 32 EB experts x 128 columns over its share of the tokens.  Its
 // wavefronts take half of the experts each, for steps of 32 tokens of their own (four
 // steps at a time); the four meet in LDS.
-template <int EB>
+template <int EB, bool kRows>
 __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, RouteBackLds& lds) {
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int n = lane & 15, kq = lane >> 4;
@@ -342,17 +361,24 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, Route
     return load_block(a.x + st * 32 * a.d, 8 * kq, (int)(left < 31 ? left : 31), a.d, col);
   };
   Block next;
-  if (st < steps) next = load_x(st);
+  const int e_base = tile_e0 / kRbTile * kRbTile;  // the tile's first expert
+  TileLoads tile_next;
+  if (st < steps) {
+    tile_next = request_tile<kRows>(a, st * 32, e_base);
+    next = load_x(st);
+  }
   for (; st < steps; st += stride) {
     const int64_t t0 = st * 32;
     PairLoads r;
-    if (!a.g) r = request_pairs(a, t0);
+    if (!kRows) r = request_pairs(a, t0);
     const Block x = next;
     TilePairs p;
-    if (!a.g) p = deal_pairs(a, r, t0, tile);
-    const int e_base = tile_e0 / kRbTile * kRbTile;  // the tile's first expert
-    fill_tile(a, tile, p, t0, e_base);
-    if (st + stride < steps) next = load_x(st + stride);
+    if (!kRows) p = deal_pairs(a, r, t0, tile);
+    put_tile<kRows>(a, tile, p, tile_next, e_base);
+    if (st + stride < steps) {
+      tile_next = request_tile<kRows>(a, (st + stride) * 32, e_base);
+      next = load_x(st + stride);
+    }
     bf16x8_t xf[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) xf[i] = column(x, i);
@@ -398,6 +424,7 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, Route
 }
 
 // dx alone: a wavefront computes 32 tokens x 128 columns.
+template <bool kRows>
 __device__ __forceinline__ void route_dx(const RouteBackDev& a, int block, RouteBackLds& lds) {
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int chunks = (a.d + kRbCols - 1) / kRbCols;
@@ -407,23 +434,23 @@ __device__ __forceinline__ void route_dx(const RouteBackDev& a, int block, Route
   const int col = at < a.d ? at : 0;
   float* tile = lds.tile[wave];
   PairLoads r;
-  if (!a.g) r = request_pairs(a, t0);
-  const DxLoads dx = request_dx(a, t0, col);
+  if (!kRows) r = request_pairs(a, t0);
+  const DxLoads dx = request_dx<kRows>(a, t0, col);
   TilePairs p;
-  if (!a.g) p = deal_pairs(a, r, t0, tile);
-  run_dx(a, tile, p, dx, t0, col, at < a.d);
+  if (!kRows) p = deal_pairs(a, r, t0, tile);
+  run_dx<kRows>(a, tile, p, dx, t0, col, at < a.d);
 }
 
 // Both products in one launch: the first dw_blocks workgroups sum dW, the others dx.
 // (One workgroup that computes both from the same tiles ran slower, 36 against 23 us at
 // T = 4096, d = 2048, E = 64: the registers of the two add up and spill.)
-template <int EB>
+template <int EB, bool kRows>
 __global__ __launch_bounds__(64 * kRbWaves) void k_route_products(RouteBackDev a, int dw_blocks) {
   __shared__ RouteBackLds lds;
   if ((int)blockIdx.x < dw_blocks)
-    route_dw<EB>(a, blockIdx.x, lds);
+    route_dw<EB, kRows>(a, blockIdx.x, lds);
   else
-    route_dx(a, blockIdx.x - dw_blocks, lds);
+    route_dx<kRows>(a, blockIdx.x - dw_blocks, lds);
 }
 
 __global__ __launch_bounds__(256) void k_route_dw_sum(const float* part, int splits, int64_t count, float* dw) {
@@ -540,9 +567,9 @@ extern "C" int moe_route_backward(const moe_route_backward_args* a, void* stream
     hipLaunchKernelGGL(kernel, dim3((unsigned)(dw_blocks + dx_blocks)), dim3(64 * kRbWaves), 0, s, v, (int)dw_blocks);
   };
   if (p.EB == 1)
-    products(k_route_products<1>);
+    v.g ? products(k_route_products<1, true>) : products(k_route_products<1, false>);
   else
-    products(k_route_products<2>);
+    v.g ? products(k_route_products<2, true>) : products(k_route_products<2, false>);
   if (a->dw_router && p.splits > 1) {
     const int64_t count = (int64_t)a->E * a->d;
     hipLaunchKernelGGL(k_route_dw_sum, dim3((unsigned)ceil_div(count, 1024)), dim3(256), 0, s, v.part, p.splits, count,
