@@ -22,8 +22,8 @@ namespace moe {
 
 constexpr int kRbCols = 128;   // columns of d per wavefront
 constexpr int kRbWaves = 8;    // wavefronts per workgroup of the products
-constexpr int kRbTile = 64;    // experts of a tile of G
-constexpr int kRbTileLd = 68;  // floats per token of a tile: rows stay 16-byte aligned
+constexpr int kRbTile = 64;    // experts of a tile of G for dx (32 for dW)
+constexpr int tile_ld(int kE) { return kE + 4; }  // floats per token of a tile: rows stay 16-byte aligned
 static_assert(MOE_MAX_TOPK <= 16, "a lane holds every other pair of its token, at most eight");
 
 struct RouteBackDev {
@@ -165,38 +165,41 @@ __device__ __forceinline__ TilePairs deal_pairs(const RouteBackDev& a, const Pai
   __builtin_amdgcn_wave_barrier();
   return p;
 }
-static_assert(3 * 32 * MOE_MAX_TOPK <= 32 * kRbTileLd, "the pairs' staging lies in the tile");
+static_assert(3 * 32 * MOE_MAX_TOPK <= 32 * tile_ld(kRbTile), "the pairs' staging lies in the tile");
 
-// G of 32 tokens and experts e0 .. e0 + 63: requested (kRows: a first launch has written
-// it) and put into the wavefront's tile.
+// G of 32 tokens and experts e0 .. e0 + kE - 1 (32 or 64): requested (kRows: a first launch
+// has written it) and put into the wavefront's tile.
+template <int kE>
 struct TileLoads {
-  f32x4_t v[8];
+  f32x4_t v[kE / 8];
 };
-template <bool kRows>
-__device__ __forceinline__ TileLoads request_tile(const RouteBackDev& a, int64_t t0, int e0) {
-  TileLoads r;
+template <bool kRows, int kE>
+__device__ __forceinline__ TileLoads<kE> request_tile(const RouteBackDev& a, int64_t t0, int e0) {
+  TileLoads<kE> r;
+  constexpr int kLanes = kE / 4, kStep = 64 / kLanes;  // lanes per token, tokens per load
   if (kRows) {
     const MOE_GLOBAL char* base = (const MOE_GLOBAL char*)(a.g + t0 * a.Ep + e0);
-    const uint32_t at = (lane_id() >> 4) * a.Ep + (lane_id() & 15) * 4;
+    const uint32_t at = (lane_id() / kLanes) * a.Ep + lane_id() % kLanes * 4;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = *(const MOE_GLOBAL f32x4_t*)(base + 4 * (at + 4 * i * (uint32_t)a.Ep));
+    for (int i = 0; i < kE / 8; ++i)
+      r.v[i] = *(const MOE_GLOBAL f32x4_t*)(base + 4 * (at + kStep * i * (uint32_t)a.Ep));
   }
   return r;
 }
-template <bool kRows>
-__device__ __forceinline__ void put_tile(const RouteBackDev& a, float* tile, const TilePairs& p, const TileLoads& r,
-                                         int e0) {
+template <bool kRows, int kE>
+__device__ __forceinline__ void put_tile(float* tile, const TilePairs& p, const TileLoads<kE>& r, int e0) {
   const int lane = lane_id();
+  constexpr int kLanes = kE / 4, kStep = 64 / kLanes, kLd = tile_ld(kE);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<f32x4_t*>(tile + (4 * i + (lane >> 4)) * kRbTileLd + (lane & 15) * 4) =
+  for (int i = 0; i < kE / 8; ++i)
+    *reinterpret_cast<f32x4_t*>(tile + (kStep * i + lane / kLanes) * kLd + lane % kLanes * 4) =
         kRows ? r.v[i] : f32x4_t{0.f, 0.f, 0.f, 0.f};
   __builtin_amdgcn_wave_barrier();
   if (!kRows) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = p.id[i] - e0;
-      if (p.id[i] >= 0 && e >= 0 && e < kRbTile) tile[(lane >> 1) * kRbTileLd + e] = p.g[i];
+      if (p.id[i] >= 0 && e >= 0 && e < kE) tile[(lane >> 1) * kLd + e] = p.g[i];
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -249,21 +252,21 @@ __device__ __forceinline__ bf16x8_t column(const Block& b, int c) {
 
 // LDS of a workgroup: the wavefronts' tiles, then (dW) their sums
 union alignas(16) RouteBackLds {
-  float tile[kRbWaves][32 * kRbTileLd];
+  float tile[kRbWaves][32 * tile_ld(kRbTile)];
   float sums[kRbWaves][16][kRbCols + 4];
 };
 
 // dx of a tile's 32 tokens in 128 columns: what is requested first ...
 struct DxLoads {
   Block w;             // the first 32 experts
-  TileLoads g;         // the first 64
+  TileLoads<kRbTile> g;  // the first 64
   uint32_t add[2][4][4];  // dx_add of the lane's results
 };
 template <bool kRows>
 __device__ __forceinline__ DxLoads request_dx(const RouteBackDev& a, int64_t t0, int col) {
   const int kq = lane_id() >> 4;
   DxLoads r;
-  r.g = request_tile<kRows>(a, t0, 0);
+  r.g = request_tile<kRows, kRbTile>(a, t0, 0);
   r.w = load_block(a.w, 8 * kq, a.E - 1, a.d, col);
   const uint16_t* base = a.dx_add + t0 * a.d;
   const int last = (int)(a.T - 1 - t0 < 31 ? a.T - 1 - t0 : 31);
@@ -291,18 +294,18 @@ __device__ __forceinline__ void run_dx(const RouteBackDev& a, float* tile, const
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   Block next = r.w;
-  TileLoads tile_next = r.g;
+  TileLoads<kRbTile> tile_next = r.g;
   for (int e = 0; e < a.E; e += 32) {
     if (e % kRbTile == 0) {
-      put_tile<kRows>(a, tile, p, tile_next, e);
-      if (e + kRbTile < a.E) tile_next = request_tile<kRows>(a, t0, e + kRbTile);
+      put_tile<kRows, kRbTile>(tile, p, tile_next, e);
+      if (e + kRbTile < a.E) tile_next = request_tile<kRows, kRbTile>(a, t0, e + kRbTile);
     }
     const Block w = next;
     if (e + 32 < a.E) next = load_block(a.w, e + 32 + 8 * kq, a.E - 1, a.d, col);
     bf16x8_t gf[2][2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const float* row = tile + (16 * b + n) * kRbTileLd + e % kRbTile + 8 * kq;
+      const float* row = tile + (16 * b + n) * tile_ld(kRbTile) + e % kRbTile + 8 * kq;
       const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(row), hi = *reinterpret_cast<const f32x4_t*>(row + 4);
       float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       split_parts<2>(v, gf[b]);
@@ -361,10 +364,9 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, Route
     return load_block(a.x + st * 32 * a.d, 8 * kq, (int)(left < 31 ? left : 31), a.d, col);
   };
   Block next;
-  const int e_base = tile_e0 / kRbTile * kRbTile;  // the tile's first expert
-  TileLoads tile_next;
+  TileLoads<32> tile_next;
   if (st < steps) {
-    tile_next = request_tile<kRows>(a, st * 32, e_base);
+    tile_next = request_tile<kRows, 32>(a, st * 32, e0);
     next = load_x(st);
   }
   for (; st < steps; st += stride) {
@@ -374,9 +376,9 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, Route
     const Block x = next;
     TilePairs p;
     if (!kRows) p = deal_pairs(a, r, t0, tile);
-    put_tile<kRows>(a, tile, p, tile_next, e_base);
+    put_tile<kRows, 32>(tile, p, tile_next, e0);
     if (st + stride < steps) {
-      tile_next = request_tile<kRows>(a, (st + stride) * 32, e_base);
+      tile_next = request_tile<kRows, 32>(a, (st + stride) * 32, e0);
       next = load_x(st + stride);
     }
     bf16x8_t xf[8];
@@ -387,7 +389,7 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, Route
       if (e0 + 16 * b >= a.E) break;
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = tile[(8 * kq + i) * kRbTileLd + e0 - e_base + 16 * b + n];
+      for (int i = 0; i < 8; ++i) v[i] = tile[(8 * kq + i) * tile_ld(32) + 16 * b + n];
       bf16x8_t gf[3];
       split_parts<3>(v, gf);
 #pragma unroll
