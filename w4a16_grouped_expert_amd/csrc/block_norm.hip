@@ -46,6 +46,18 @@ struct NormSplit {
   int lt, waves, slots, threads, pieces;
 };
 
+// The same value, unknown to the compiler and settled here: nothing that depends on it is
+// kept from before, moved out of a loop, or put off until later.
+template <typename V>
+__device__ __forceinline__ void forget(V& v) {
+  asm volatile("" : "+v"(v));
+}
+template <typename S>
+__device__ __forceinline__ void forget(Raw<S>& r) {
+#pragma unroll
+  for (int q = 0; q < (int)(sizeof(r.w) / sizeof(r.w[0])); ++q) asm volatile("" : "+v"(r.w[q]) : : "memory");
+}
+
 // sums over the threads of a row, in each of them.  Rows of several wavefronts meet in
 // LDS; the caller alternates between two buffers, so that one barrier is enough: a
 // wavefront that writes a buffer again has passed the barrier of the other one, which
@@ -55,8 +67,10 @@ __device__ __forceinline__ void row_sums(float (&v)[K], const NormSplit& p, floa
 #pragma unroll
   for (int i = 0; i < K; ++i) v[i] = lane_sum(v[i], kSub ? p.lt : 6);
   if (kSub || p.waves == 1) return;
-  const int wave = threadIdx.x >> 6;
-  if ((threadIdx.x & 63) == 0)
+  int tid = threadIdx.x;
+  forget(tid);  // (addresses made from it outside the caller's loop would stay in registers)
+  const int wave = tid >> 6;
+  if ((tid & 63) == 0)
 #pragma unroll
     for (int i = 0; i < K; ++i) buf[wave * 8 + i] = v[i];
   __syncthreads();
@@ -89,13 +103,6 @@ __device__ __forceinline__ Raw<S> ones() {
   return pack<S>(v);
 }
 
-// The same values, unknown to the compiler.
-template <typename S>
-__device__ __forceinline__ void forget(Raw<S>& r) {
-#pragma unroll
-  for (int q = 0; q < (int)(sizeof(r.w) / sizeof(r.w[0])); ++q) asm volatile("" : "+v"(r.w[q]) : : "memory");
-}
-
 template <typename S, int R, bool kSub>
 __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormSplit p) {
   __shared__ float lds[2][kNormMaxThreads / 64 * 8];
@@ -112,7 +119,6 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     c[r] = piece_of((r * rl.lanes + rl.lane) * kPiece, a.d);
-    if (!live) c[r].skip = kPiece;
     rx[r] = load_raw<kSub>(row_ptr<S, kSub>(a.x, tc, a.x_stride), c[r], a.d);
     if (a.y) ry_[r] = load_raw<kSub>(row_ptr<S, kSub>(a.y, tc, a.y_stride), c[r], a.d);
     vo[r] = vg[r] = vi[r] = ones<S>();
@@ -159,7 +165,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    if (a.h) store_piece<kSub>(row_ptr<S, kSub>(a.h, tc, a.h_stride), c[r], a.d, h[r]);
+    if (a.h && live) store_piece<kSub>(row_ptr<S, kSub>(a.h, tc, a.h_stride), c[r], a.d, h[r]);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) hh[0] = fmaf(h[r][i], h[r][i], hh[0]);
   }
@@ -172,7 +178,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
     unpack<S>(vi[r], v);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) v[i] *= rh * h[r][i];
-    store_piece<kSub>(row_ptr<S, kSub>(a.n, tc, a.n_stride), c[r], a.d, v);
+    if (live) store_piece<kSub>(row_ptr<S, kSub>(a.n, tc, a.n_stride), c[r], a.d, v);
   }
 }
 
@@ -185,8 +191,9 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
 // A row belongs to one wavefront up to 2048 elements (R pieces per lane), so that its
 // sums need no barrier and the wavefronts of a CU drift apart: some load while others
 // compute.  Only the row as loaded and the column sums stay in registers; h, u and q are
-// computed again for the outputs, v_out times the channel gate (W) and v_in (V) come
-// from LDS.
+// computed again for the outputs, one piece after the other, v_out times the channel gate
+// (W) and v_in (V) come from LDS.  The forget() calls hold the compiler to that: left
+// alone it keeps every piece's floats, 3 x 8 R registers, and spills.
 // Column sums: only A = sum over rows of D yn (g D yn for a token's or full gate) and
 // B = that of dn hn are kept; dnorm_out and a channel gate's gradient are A times the
 // channel gate and v_out.
@@ -195,12 +202,13 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
 //
 // Wavefronts per workgroup, one workgroup per CU: what the registers of a row of `bytes`
 // per element and R pieces allow.
-constexpr int norm_back_waves(int bytes, int R) { return R == 1 ? 16 : R == 2 && bytes == 2 ? 12 : 8; }
+constexpr int norm_back_waves(int bytes, int R) { return R == 1 ? 16 : R == 2 ? 12 : 8; }
 
 template <typename S, int R, bool kSub, bool kFull>
 __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_norm_backward(NormDev a, NormSplit p) {
   __shared__ float sums[2][16 * 8];
-  extern __shared__ f32x4_t vec[];  // [W, V][R][half][lanes]: four elements of a lane's piece each
+  // [wavefront of the row][W, V][R][half][lane]: four elements of a lane's piece each
+  extern __shared__ f32x4_t vec[];
   const RowLane rl = row_lane<kSub>(p);
   const void* dh_in = a.dh ? a.dh : a.dn;
   const void* dn_in = a.dn ? a.dn : a.dh;
@@ -213,7 +221,8 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
   const uint32_t y_on = __builtin_amdgcn_readfirstlane(a.y ? ~0u : 0u);
   float A[R][kPiece], B[R][kPiece];
   Piece c[R];
-  auto vec_at = [&](int k, int r, int half) -> f32x4_t& { return vec[((k * R + r) * 2 + half) * rl.lanes + rl.lane]; };
+  f32x4_t* const vec_mine = vec + (rl.lane >> 6) * (4 * R * 64) + (rl.lane & 63);
+  auto vec_at = [&](int k, int r, int half) -> f32x4_t& { return vec_mine[((k * R + r) * 2 + half) * 64]; };
   auto vec_put = [&](int k, int r, const float (&v)[kPiece]) {
     vec_at(k, r, 0) = f32x4_t{v[0], v[1], v[2], v[3]};
     vec_at(k, r, 1) = f32x4_t{v[4], v[5], v[6], v[7]};
@@ -272,7 +281,7 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       Piece w = c[r];
-      if (!live) w.skip = kPiece;
+      forget(w.skip);  // (or its masks would stay in registers through the loop)
       mask_piece(y[r], w);
       y[r] = masked<S>(y[r], y_on);
       float f[kPiece];
@@ -285,8 +294,6 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
       row_sums<kSub>(sy, p, sums[0]);
       ry = rsqrtf(sy[0] * a.inv_d + a.eps);
     }
-#pragma unroll
-    for (int r = 0; r < R; ++r) forget(y[r]);
     // the piece's h, u and q
     auto piece = [&](int r, float (&h)[kPiece], float (&u)[kPiece], float (&q)[kPiece]) {
       float w[kPiece];
@@ -311,12 +318,13 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
     float s[5] = {0.f, 0.f, 0.f, 0.f, 0.f};  // h h, u h, q dh, q u, q h
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      forget(y[r]);
+      forget(x[r]);
+      forget(dn[r]);
+      forget(dh[r]);
       Piece w = c[r];
-      if (!live) w.skip = kPiece;
-      mask_piece(x[r], w);
-      mask_piece(dn[r], w);
-      mask_piece(dh[r], w);
-      if (kFull) mask_piece(g[r], w);
+      forget(w.skip);
+      mask_piece(x[r], w);  // (with y it is enough: h and q are zero where both are)
       x[r] = masked<S>(x[r], dn_on);
       dn[r] = masked<S>(dn[r], dn_on);
       dh[r] = masked<S>(dh[r], dh_on);
@@ -331,7 +339,8 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
         s[3] = fmaf(q[i], u[i], s[3]);
         s[4] = fmaf(q[i], h[i], s[4]);
       }
-      __builtin_amdgcn_sched_barrier(0);  // one piece at a time: its floats are many registers
+#pragma unroll
+      for (int i = 0; i < 5; ++i) forget(s[i]);
     }
     float rh = 0.f, mh = 0.f, qD = 0.f;
     if (a.dn || a.y) {
@@ -343,21 +352,15 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
     // mean(g v_out D yn).  (Factors 1 / rms go with the sum or the element that they
     // scale, one at a time: their cube leaves float32's range for rows of size 1e13.)
     const float my = a.v_out ? gt * (ry * (qD * a.inv_d)) : 0.f;
-    // (as far as the compiler can see the row changes here, as y does above: it would keep
-    // the floats of every piece, 3 x 8 R registers, in place of computing them again)
+    if (!live) continue;  // (a row past the last took part in the barriers, on the last row's values)
+    if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && rl.lane == 0) static_cast<float*>(a.dgate)[t] = ry * qD;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      forget(x[r]);
       forget(y[r]);
+      forget(x[r]);
       forget(dn[r]);
       forget(dh[r]);
       if (kFull) forget(g[r]);
-    }
-    if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && live && rl.lane == 0) static_cast<float*>(a.dgate)[t] = ry * qD;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      Piece w = c[r];
-      if (!live) w.skip = kPiece;
       float h[kPiece], u[kPiece], D[kPiece], f[kPiece], e[kPiece];
       piece(r, h, u, f);
       unpack<S>(dn[r], f);
@@ -368,8 +371,9 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
         B[r][i] = fmaf(f[i], hn, B[r][i]);
         D[i] += rh * (u[i] - mh * hn);
         f[i] = a.scale * D[i];
+        forget(B[r][i]);  // (put off, the addition would keep its operands to the end of the row)
       }
-      if (a.dx) store_piece<kSub>(row_ptr<S, kSub>(a.dx, tc, a.dx_stride), w, a.d, f);
+      if (a.dx) store_piece<kSub>(row_ptr<S, kSub>(a.dx, tc, a.dx_stride), c[r], a.d, f);
       if (a.y) {
         unpack<S>(y[r], e);
         vec_get(0, r, u);
@@ -383,7 +387,7 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
           if (a.dgate) {
 #pragma unroll
             for (int i = 0; i < kPiece; ++i) u[i] = f[i] * e[i];
-            store_piece<kSub>(row_ptr<S, kSub>(a.dgate, tc, a.dgate_stride), w, a.d, u);
+            store_piece<kSub>(row_ptr<S, kSub>(a.dgate, tc, a.dgate_stride), c[r], a.d, u);
           }
           unpack<S>(g[r], h);
         }
@@ -391,10 +395,10 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
         for (int i = 0; i < kPiece; ++i) {
           A[r][i] = fmaf(h[i] * D[i], e[i], A[r][i]);
           f[i] = ry * (h[i] * f[i] - my * e[i]);
+          forget(A[r][i]);
         }
-        if (a.dy) store_piece<kSub>(row_ptr<S, kSub>(a.dy, tc, a.dy_stride), w, a.d, f);
+        if (a.dy) store_piece<kSub>(row_ptr<S, kSub>(a.dy, tc, a.dy_stride), c[r], a.d, f);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
   }
   if (!a.part) return;
@@ -487,7 +491,7 @@ static NormSplit norm_back_split(int T, int d, int dtype) {
   return p;
 }
 static int64_t norm_back_lds(const NormSplit& p) {
-  return (int64_t)2 * p.pieces * kPiece * 4 * (p.waves > 1 ? p.waves * 64 : 1 << p.lt);
+  return (int64_t)2 * p.pieces * kPiece * 4 * 64 * p.waves;
 }
 
 // workgroups of the gradient: one per CU (its registers allow one), so that their column
