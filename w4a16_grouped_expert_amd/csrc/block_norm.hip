@@ -44,6 +44,7 @@ __device__ __forceinline__ float token_gate(const NormDev& a, int64_t t) {
 // How the threads of a workgroup share rows: `slots` rows at a time, each by 1 << lt lanes of a wavefront or by `waves` whole wavefronts.
 struct NormSplit {
   int lt, waves, slots, threads, pieces;
+  bool ahead;  // gradient: the next row is requested before the current one's arithmetic
 };
 
 // The same value, unknown to the compiler and settled here: nothing that depends on it is
@@ -202,10 +203,10 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
 //
 // Wavefronts per workgroup, one workgroup per CU: what the registers of a row of `bytes`
 // per element and R pieces allow.
-constexpr int norm_back_waves(int bytes, int R) { return R == 1 ? 16 : R == 2 ? 12 : 8; }
+constexpr int norm_back_waves(int R, bool ahead) { return R == 1 ? 16 : R == 2 ? 12 : ahead ? 4 : 8; }
 
-template <typename S, int R, bool kSub, bool kFull>
-__global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_norm_backward(NormDev a, NormSplit p) {
+template <typename S, int R, bool kSub, bool kFull, bool kAhead>
+__global__ __launch_bounds__(64 * norm_back_waves(R, kAhead)) void k_block_norm_backward(NormDev a, NormSplit p) {
   __shared__ float sums[2][16 * 8];
   // [wavefront of the row][W, V][R][half][lane]: four elements of a lane's piece each
   extern __shared__ f32x4_t vec[];
@@ -242,18 +243,26 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
     for (int i = 0; i < kPiece; ++i) A[r][i] = B[r][i] = 0.f;
   }
   if (rl.slot == 0) {
+    // (every load before the first use: what is missing is read from x and replaced)
+    const S* any = static_cast<const S*>(a.x);
+    const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
+    Raw<S> vo[R], vi[R], vg[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float v[kPiece], w[kPiece];
+      vo[r] = load_raw<kSub>(a.v_out ? static_cast<const S*>(a.v_out) : any, c[r], a.d);
+      vi[r] = load_raw<kSub>(a.v_in ? static_cast<const S*>(a.v_in) : any, c[r], a.d);
+      vg[r] = load_raw<kSub>(channel ? static_cast<const S*>(a.gate) : any, c[r], a.d);
+    }
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) v[i] = w[i] = 1.f;
-      if (a.v_out) load_piece<kSub>(static_cast<const S*>(a.v_out), c[r], a.d, w);
-      if (a.v_in) load_piece<kSub>(static_cast<const S*>(a.v_in), c[r], a.d, v);
-      if (a.gate_kind == MOE_GATE_CHANNEL) {
-        float g[kPiece];
-        load_piece<kSub>(static_cast<const S*>(a.gate), c[r], a.d, g);
+    for (int r = 0; r < R; ++r) {
+      float v[kPiece], w[kPiece], g[kPiece];
+      unpack<S>(vo[r], w);
+      unpack<S>(vi[r], v);
+      unpack<S>(vg[r], g);
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) w[i] *= g[i];
+      for (int i = 0; i < kPiece; ++i) {
+        w[i] = (a.v_out ? w[i] : 1.f) * (channel ? g[i] : 1.f);
+        v[i] = a.v_in ? v[i] : 1.f;
       }
       vec_put(0, r, w);
       vec_put(1, r, v);
@@ -263,19 +272,42 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
   const int64_t step = (int64_t)gridDim.x * p.slots;
   const int64_t rounds = (a.T + step - 1) / step;
   int64_t t = (int64_t)blockIdx.x * p.slots + rl.slot;
+  struct Row {
+    Raw<S> x[R], y[R], dh[R], dn[R], g[R];
+  };
+  Row next;
+  auto request = [&](int64_t t) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) next.y[r] = load_raw<kSub>(row_ptr<S, kSub>(y_in, t, y_ld), c[r], a.d);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      next.x[r] = load_raw<kSub>(row_ptr<S, kSub>(x_in, t, x_ld), c[r], a.d);
+      next.dn[r] = load_raw<kSub>(row_ptr<S, kSub>(dn_in, t, dn_ld), c[r], a.d);
+      next.dh[r] = load_raw<kSub>(row_ptr<S, kSub>(dh_in, t, dh_ld), c[r], a.d);
+      if (kFull) next.g[r] = load_raw<kSub>(row_ptr<S, kSub>(a.gate, t, a.gate_stride), c[r], a.d);
+    }
+  };
+  if (kAhead) request(t < a.T ? t : a.T - 1);
   for (int64_t it = 0; it < rounds; ++it, t += step) {
     const bool live = t < a.T;
     const int64_t tc = live ? t : a.T - 1;
+    if (!kAhead) request(tc);
     Raw<S> x[R], y[R], dh[R], dn[R], g[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) y[r] = load_raw<kSub>(row_ptr<S, kSub>(y_in, tc, y_ld), c[r], a.d);
-#pragma unroll
     for (int r = 0; r < R; ++r) {
-      x[r] = load_raw<kSub>(row_ptr<S, kSub>(x_in, tc, x_ld), c[r], a.d);
-      dn[r] = load_raw<kSub>(row_ptr<S, kSub>(dn_in, tc, dn_ld), c[r], a.d);
-      dh[r] = load_raw<kSub>(row_ptr<S, kSub>(dh_in, tc, dh_ld), c[r], a.d);
-      if (kFull) g[r] = load_raw<kSub>(row_ptr<S, kSub>(a.gate, tc, a.gate_stride), c[r], a.d);
+      x[r] = next.x[r];
+      y[r] = next.y[r];
+      dn[r] = next.dn[r];
+      dh[r] = next.dh[r];
+      if (kFull) g[r] = next.g[r];
+      if (kAhead) {
+        forget(x[r]);
+        forget(y[r]);
+        forget(dn[r]);
+        forget(dh[r]);
+      }
     }
+    if (kAhead && t + step < a.T) request(t + step);
     const float gt = token_gate<S, kSub>(a, tc);
     float sy[1] = {0.f};
 #pragma unroll
@@ -294,8 +326,8 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
       row_sums<kSub>(sy, p, sums[0]);
       ry = rsqrtf(sy[0] * a.inv_d + a.eps);
     }
-    // the piece's h, u and q
-    auto piece = [&](int r, float (&h)[kPiece], float (&u)[kPiece], float (&q)[kPiece]) {
+    // the piece's u, q and h, scaled: sx x + sq q
+    auto piece = [&](int r, float sx, float sq, float (&h)[kPiece], float (&u)[kPiece], float (&q)[kPiece]) {
       float w[kPiece];
       unpack<S>(y[r], q);
       vec_get(0, r, w);
@@ -311,7 +343,7 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
       vec_get(1, r, w);
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
-        h[i] = fmaf(gt * ry, q[i], a.scale * h[i]);
+        h[i] = fmaf(sq, q[i], sx * h[i]);
         u[i] *= w[i];
       }
     };
@@ -329,7 +361,7 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
       dn[r] = masked<S>(dn[r], dn_on);
       dh[r] = masked<S>(dh[r], dh_on);
       float h[kPiece], u[kPiece], q[kPiece], D[kPiece];
-      piece(r, h, u, q);
+      piece(r, a.scale, gt * ry, h, u, q);
       unpack<S>(dh[r], D);
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
@@ -362,14 +394,13 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
       forget(dh[r]);
       if (kFull) forget(g[r]);
       float h[kPiece], u[kPiece], D[kPiece], f[kPiece], e[kPiece];
-      piece(r, h, u, f);
+      piece(r, rh * a.scale, rh * (gt * ry), h, u, f);  // hn in place of h
       unpack<S>(dn[r], f);
       unpack<S>(dh[r], D);
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
-        const float hn = rh * h[i];
-        B[r][i] = fmaf(f[i], hn, B[r][i]);
-        D[i] += rh * (u[i] - mh * hn);
+        B[r][i] = fmaf(f[i], h[i], B[r][i]);
+        D[i] = fmaf(-rh * mh, h[i], fmaf(rh, u[i], D[i]));
         f[i] = a.scale * D[i];
         forget(B[r][i]);  // (put off, the addition would keep its operands to the end of the row)
       }
@@ -377,24 +408,27 @@ __global__ __launch_bounds__(64 * norm_back_waves(sizeof(S), R)) void k_block_no
       if (a.y) {
         unpack<S>(y[r], e);
         vec_get(0, r, u);
-#pragma unroll
-        for (int i = 0; i < kPiece; ++i) {
-          f[i] = u[i] * D[i];  // without the full or the token's gate
-          e[i] *= ry;
-          h[i] = gt;
-        }
         if (kFull) {
-          if (a.dgate) {
+          float k[kPiece];
+          unpack<S>(g[r], k);
 #pragma unroll
-            for (int i = 0; i < kPiece; ++i) u[i] = f[i] * e[i];
-            store_piece<kSub>(row_ptr<S, kSub>(a.dgate, tc, a.dgate_stride), c[r], a.d, u);
+          for (int i = 0; i < kPiece; ++i) {
+            e[i] *= ry;
+            f[i] = D[i] * (u[i] * e[i]);
+            D[i] *= k[i];
           }
-          unpack<S>(g[r], h);
+          if (a.dgate) store_piece<kSub>(row_ptr<S, kSub>(a.dgate, tc, a.dgate_stride), c[r], a.d, f);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kPiece; ++i) {
+            e[i] *= ry;
+            D[i] *= gt;
+          }
         }
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) {
-          A[r][i] = fmaf(h[i] * D[i], e[i], A[r][i]);
-          f[i] = ry * (h[i] * f[i] - my * e[i]);
+          A[r][i] = fmaf(D[i], e[i], A[r][i]);
+          f[i] = fmaf(-ry * my, e[i], ry * (u[i] * D[i]));
           forget(A[r][i]);
         }
         if (a.dy) store_piece<kSub>(row_ptr<S, kSub>(a.dy, tc, a.dy_stride), c[r], a.d, f);
@@ -482,7 +516,8 @@ static NormSplit norm_back_split(int T, int d, int dtype) {
   p.lt = 0;
   while (p.lt < 6 && (1 << p.lt) < lanes) ++p.lt;
   p.waves = (int)ceil_div(lanes, 64);
-  const int most = norm_back_waves(bytes, p.pieces);
+  p.ahead = bytes == 2 && p.pieces == 4 && p.waves == 1;
+  const int most = norm_back_waves(p.pieces, p.ahead);
   const int per_wave = 64 >> p.lt;
   int groups = p.waves > 1 ? most / p.waves : most;  // wavefronts (or groups of them) per workgroup
   groups = (int)std::max<int64_t>(1, std::min<int64_t>(groups, ceil_div(T, 256 * per_wave)));
@@ -647,23 +682,31 @@ extern "C" int moe_block_norm_backward(const moe_block_norm_args* a, const moe_b
           (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         hipLaunchKernelGGL(kernel, dim3(groups), dim3(p.threads), (unsigned)lds, s, v, p);
       };
-      auto go = [&](auto pieces, auto sub) {
+      auto go = [&](auto pieces, auto sub, auto ahead) {
         constexpr int R = decltype(pieces)::value;
-        constexpr bool kSub = decltype(sub)::value;
+        constexpr bool kSub = decltype(sub)::value, kAhead = decltype(ahead)::value;
         if (a->gate_kind == MOE_GATE_FULL)
-          launch(k_block_norm_backward<S, R, kSub, true>);
+          launch(k_block_norm_backward<S, R, kSub, true, kAhead>);
         else
-          launch(k_block_norm_backward<S, R, kSub, false>);
+          launch(k_block_norm_backward<S, R, kSub, false, kAhead>);
       };
       using std::integral_constant;
+      const std::true_type yes;
+      const std::false_type no;
       if (p.lt < 6)
-        go(integral_constant<int, 1>{}, std::true_type{});
+        go(integral_constant<int, 1>{}, yes, no);
       else if (p.pieces == 1)
-        go(integral_constant<int, 1>{}, std::false_type{});
+        go(integral_constant<int, 1>{}, no, no);
       else if (p.pieces == 2)
-        go(integral_constant<int, 2>{}, std::false_type{});
-      else
-        go(integral_constant<int, 4>{}, std::false_type{});
+        go(integral_constant<int, 2>{}, no, no);
+      else if constexpr (sizeof(S) == 2) {
+        if (p.ahead)
+          go(integral_constant<int, 4>{}, no, yes);
+        else
+          go(integral_constant<int, 4>{}, no, no);
+      } else {
+        go(integral_constant<int, 4>{}, no, no);
+      }
     }
     if (vectors)
       hipLaunchKernelGGL(k_norm_vectors<S>, dim3((unsigned)ceil_div(a->d, 32), 2), dim3(1024), 0, s, v.part, groups, v,
