@@ -104,6 +104,14 @@ __device__ __forceinline__ Raw<S> ones() {
   return pack<S>(v);
 }
 
+// a piece's own elements, zero for those of the piece before
+template <typename S>
+__device__ __forceinline__ void unpack_own(Raw<S> r, Piece p, float (&v)[kPiece]) {
+  forget(p.skip);  // (or its masks would stay in registers through the caller's loop)
+  mask_piece(r, p);
+  unpack<S>(r, v);
+}
+
 template <typename S, int R, bool kSub>
 __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormSplit p) {
   __shared__ float lds[2][kNormMaxThreads / 64 * 8];
@@ -131,12 +139,8 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
   const float gt = token_gate<S, kSub>(a, tc);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    mask_piece(rx[r], c[r]);
     unpack<S>(rx[r], h[r]);
-    if (a.y) {
-      mask_piece(ry_[r], c[r]);
-      unpack<S>(ry_[r], z[r]);
-    }
+    if (a.y) unpack<S>(ry_[r], z[r]);
   }
   float hh[1] = {0.f};
   if (a.y) {
@@ -145,7 +149,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) ss[0] = fmaf(z[r][i], z[r][i], ss[0]);
+        for (int i = 0; i < kPiece; ++i) ss[0] = i < c[r].skip ? ss[0] : fmaf(z[r][i], z[r][i], ss[0]);
       row_sums<kSub>(ss, p, lds[0]);
       ry = rsqrtf(ss[0] * a.inv_d + a.eps);
     }
@@ -164,11 +168,14 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) h[r][i] *= a.scale;
   }
+  // h may lie where x or y does, and pieces of two wavefronts may overlap: no store before
+  // the row's last load
+  if (!kSub && p.waves > 1 && !a.v_out) __syncthreads();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if (a.h && live) store_piece<kSub>(row_ptr<S, kSub>(a.h, tc, a.h_stride), c[r], a.d, h[r]);
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) hh[0] = fmaf(h[r][i], h[r][i], hh[0]);
+    for (int i = 0; i < kPiece; ++i) hh[0] = i < c[r].skip ? hh[0] : fmaf(h[r][i], h[r][i], hh[0]);
   }
   if (!a.v_in) return;
   row_sums<kSub>(hh, p, lds[1]);
@@ -312,12 +319,9 @@ __global__ __launch_bounds__(64 * norm_back_waves(R, kAhead)) void k_block_norm_
     float sy[1] = {0.f};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      Piece w = c[r];
-      forget(w.skip);  // (or its masks would stay in registers through the loop)
-      mask_piece(y[r], w);
       y[r] = masked<S>(y[r], y_on);
       float f[kPiece];
-      unpack<S>(y[r], f);
+      unpack_own(y[r], c[r], f);
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) sy[0] = fmaf(f[i], f[i], sy[0]);
     }
@@ -326,10 +330,11 @@ __global__ __launch_bounds__(64 * norm_back_waves(R, kAhead)) void k_block_norm_
       row_sums<kSub>(sy, p, sums[0]);
       ry = rsqrtf(sy[0] * a.inv_d + a.eps);
     }
-    // the piece's u, q and h, scaled: sx x + sq q
-    auto piece = [&](int r, float sx, float sq, float (&h)[kPiece], float (&u)[kPiece], float (&q)[kPiece]) {
+    // the piece's u, q and h, scaled: sx x + sq q; own: q and h zero (and with them every
+    // term of the sums) where the element is another piece's
+    auto piece = [&](int r, float sx, float sq, bool own, float (&h)[kPiece], float (&u)[kPiece], float (&q)[kPiece]) {
       float w[kPiece];
-      unpack<S>(y[r], q);
+      own ? unpack_own(y[r], c[r], q) : unpack<S>(y[r], q);
       vec_get(0, r, w);
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) q[i] *= w[i];
@@ -338,7 +343,7 @@ __global__ __launch_bounds__(64 * norm_back_waves(R, kAhead)) void k_block_norm_
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) q[i] *= w[i];
       }
-      unpack<S>(x[r], h);
+      own ? unpack_own(x[r], c[r], h) : unpack<S>(x[r], h);
       unpack<S>(dn[r], u);
       vec_get(1, r, w);
 #pragma unroll
@@ -354,14 +359,11 @@ __global__ __launch_bounds__(64 * norm_back_waves(R, kAhead)) void k_block_norm_
       forget(x[r]);
       forget(dn[r]);
       forget(dh[r]);
-      Piece w = c[r];
-      forget(w.skip);
-      mask_piece(x[r], w);  // (with y it is enough: h and q are zero where both are)
       x[r] = masked<S>(x[r], dn_on);
       dn[r] = masked<S>(dn[r], dn_on);
       dh[r] = masked<S>(dh[r], dh_on);
       float h[kPiece], u[kPiece], q[kPiece], D[kPiece];
-      piece(r, a.scale, gt * ry, h, u, q);
+      piece(r, a.scale, gt * ry, true, h, u, q);
       unpack<S>(dh[r], D);
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
@@ -374,13 +376,10 @@ __global__ __launch_bounds__(64 * norm_back_waves(R, kAhead)) void k_block_norm_
 #pragma unroll
       for (int i = 0; i < 5; ++i) forget(s[i]);
     }
-    float rh = 0.f, mh = 0.f, qD = 0.f;
-    if (a.dn || a.y) {
-      row_sums<kSub>(s, p, sums[1]);
-      rh = a.dn ? rsqrtf(s[0] * a.inv_d + a.eps) : 0.f;
-      mh = rh * (s[1] * a.inv_d);  // mean(u hn)
-      qD = s[2] + rh * (s[3] - mh * (rh * s[4]));
-    }
+    row_sums<kSub>(s, p, sums[1]);  // (its barrier also ends the row's loads before a store in their place)
+    const float rh = a.dn ? rsqrtf(s[0] * a.inv_d + a.eps) : 0.f;
+    const float mh = rh * (s[1] * a.inv_d);  // mean(u hn)
+    const float qD = s[2] + rh * (s[3] - mh * (rh * s[4]));
     // mean(g v_out D yn).  (Factors 1 / rms go with the sum or the element that they
     // scale, one at a time: their cube leaves float32's range for rows of size 1e13.)
     const float my = a.v_out ? gt * (ry * (qD * a.inv_d)) : 0.f;
@@ -394,7 +393,7 @@ __global__ __launch_bounds__(64 * norm_back_waves(R, kAhead)) void k_block_norm_
       forget(dh[r]);
       if (kFull) forget(g[r]);
       float h[kPiece], u[kPiece], D[kPiece], f[kPiece], e[kPiece];
-      piece(r, rh * a.scale, rh * (gt * ry), h, u, f);  // hn in place of h
+      piece(r, rh * a.scale, rh * (gt * ry), false, h, u, f);  // hn in place of h
       unpack<S>(dn[r], f);
       unpack<S>(dh[r], D);
 #pragma unroll
@@ -504,14 +503,17 @@ static NormSplit norm_split(int d, int target) {
   return p;
 }
 
-// Gradient: a row of up to 2048 elements of two bytes or 1024 floats has one wavefront
-// with one, two or four pieces per lane, longer ones several with the most pieces; fewer
-// rows per workgroup where there are few, so that every CU has some.
+// Gradient: a row of up to 2048 elements of two bytes or 1536 floats has one wavefront
+// with one to four pieces per lane, a longer one several; fewer rows per workgroup where
+// there are few, so that every CU has some.
 static NormSplit norm_back_split(int T, int d, int dtype) {
   NormSplit p;
   const int bytes = (int)dtype_bytes(dtype);
   const int pieces = (int)ceil_div(d, kPiece);
-  p.pieces = pieces <= 64 ? 1 : pieces <= (bytes == 4 ? 1024 : 128) ? 2 : 4;
+  if (bytes == 4)
+    p.pieces = pieces <= 64 ? 1 : pieces <= 128 ? 2 : pieces <= 192 ? 3 : pieces <= 1024 ? 2 : 4;
+  else
+    p.pieces = pieces <= 64 ? 1 : pieces <= 128 ? 2 : pieces <= 192 ? 3 : 4;
   const int lanes = (int)ceil_div(pieces, p.pieces);
   p.lt = 0;
   while (p.lt < 6 && (1 << p.lt) < lanes) ++p.lt;
@@ -699,6 +701,8 @@ extern "C" int moe_block_norm_backward(const moe_block_norm_args* a, const moe_b
         go(integral_constant<int, 1>{}, no, no);
       else if (p.pieces == 2)
         go(integral_constant<int, 2>{}, no, no);
+      else if (p.pieces == 3)
+        go(integral_constant<int, 3>{}, no, no);
       else if constexpr (sizeof(S) == 2) {
         if (p.ahead)
           go(integral_constant<int, 4>{}, no, yes);

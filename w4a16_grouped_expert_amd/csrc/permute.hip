@@ -61,17 +61,16 @@ __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __re
     pos[j] = kept[j] ? pos[j] : 0;
   }
   for (int it = 0; it < p.rounds; ++it) {
-    Piece c = piece_of((part * 64 + lane + it * p.waves * 64) * kPiece, a.d);
-    if (!live) c.skip = kPiece;
+    const Piece c = piece_of((part * 64 + lane + it * p.waves * 64) * kPiece, a.d);
     Raw<S> mine;
     if (kSpread || kProducts)
       mine = load_raw<false>(row_ptr<S, false>(a.token_in, tc, a.token_in_stride), c, a.d);
-    float v[kPiece], r[kPiece], acc[kPiece];
+    float v[kPiece], own[kPiece], r[kPiece], acc[kPiece];
     if (kSpread || kProducts) unpack<S>(mine, v);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) {
       acc[i] = 0.f;
-      if (kProducts) v[i] = i < c.skip ? 0.f : v[i];  // (elements of the piece before: in its sum)
+      if (kProducts) own[i] = i < c.skip ? 0.f : v[i];  // (elements of the piece before: in its sum)
     }
 #pragma unroll
     for (int j0 = 0; j0 < KM; j0 += KB) {
@@ -90,7 +89,7 @@ __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __re
 #pragma unroll
           for (int i = 0; i < kPiece; ++i) {
             if (!kSpread) acc[i] = fmaf(w[j], r[i], acc[i]);
-            if (kProducts) dot[j] = fmaf(v[i], r[i], dot[j]);
+            if (kProducts) dot[j] = fmaf(own[i], r[i], dot[j]);
           }
         }
         if (kSpread && kept[j]) {
@@ -133,11 +132,13 @@ __global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t*
   const Piece c = piece_of(lane * kPiece, a.d);
   Raw<S> mine{};
   if (kSpread || kProducts) mine = load_raw<true>(row_ptr<S, true>(a.token_in, t, a.token_in_stride), c, a.d);
-  mask_piece(mine, c);
-  float v[kPiece], r[kPiece], acc[kPiece];
+  float v[kPiece], own[kPiece], r[kPiece], acc[kPiece];
   unpack<S>(mine, v);
 #pragma unroll
-  for (int i = 0; i < kPiece; ++i) acc[i] = 0.f;
+  for (int i = 0; i < kPiece; ++i) {
+    acc[i] = 0.f;
+    own[i] = i < c.skip ? 0.f : v[i];
+  }
   for (int j = 0; j < a.k; ++j) {
     const int64_t at = t * a.k + j, pos = pair_pos[at];
     const bool kept = pos >= 0 && pos < a.num_rows;
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t*
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
         if (!kSpread) acc[i] = fmaf(w, r[i], acc[i]);
-        if (kProducts) dot = fmaf(v[i], r[i], dot);
+        if (kProducts) dot = fmaf(own[i], r[i], dot);
       }
     }
     if (kSpread && kept) {

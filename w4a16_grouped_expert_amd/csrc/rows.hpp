@@ -33,10 +33,12 @@ struct Raw {
 
 
 // Where a lane's eight elements of a row of d lie.  The last piece of a row whose length
-// is no multiple of 8 starts at d - 8, so that every load is one of eight elements inside
-// the row and none sits under a branch; its first `skip` elements belong to the piece
-// before (mask_piece makes them zero).  A lane past the end skips all eight.  kTiny: rows of fewer than
-// eight elements too (at = 0), element by element; kernels take it for short rows only.
+// is no multiple of 8 starts at d - 8, and so do those of lanes past the end: every load
+// and store is one of eight elements inside the row, and none sits under a branch.  The
+// first `skip` elements of such a piece belong to pieces before it.  They are left out of
+// sums (mask_piece); outputs are computed and stored twice, the same bits both times.
+// kTiny: rows of fewer than eight elements too (at = 0, element by element, skip = 0 for
+// the first lane); kernels take it for short rows only.
 struct Piece {
   uint32_t at;  // first element
   int skip;
@@ -46,15 +48,22 @@ __device__ __forceinline__ Piece piece_of(int col, int d) {
   return {(uint32_t)at, col - at < kPiece ? col - at : kPiece};
 }
 // (Global memory by a scalar base and a 32-bit offset in bytes where the row's address is
-// uniform: no vector registers for addresses.)
+// uniform: no vector registers for addresses.  The asm keeps the offset's extension to 64
+// bits beside the access, where the compiler can see that it needs none.)
 #define MOE_GLOBAL __attribute__((address_space(1)))
 template <typename S>
+__device__ __forceinline__ uint32_t piece_offset(const Piece& p) {
+  uint32_t o = p.at * (uint32_t)sizeof(S);
+  asm volatile("" : "+v"(o));
+  return o;
+}
+template <typename S>
 __device__ __forceinline__ const MOE_GLOBAL char* piece_ptr(const S* row, const Piece& p) {
-  return (const MOE_GLOBAL char*)row + (uint32_t)(p.at * sizeof(S));
+  return (const MOE_GLOBAL char*)row + piece_offset<S>(p);
 }
 template <typename S>
 __device__ __forceinline__ MOE_GLOBAL char* piece_ptr(S* row, const Piece& p) {
-  return (MOE_GLOBAL char*)row + (uint32_t)(p.at * sizeof(S));
+  return (MOE_GLOBAL char*)row + piece_offset<S>(p);
 }
 
 template <bool kTiny, typename S>
@@ -106,7 +115,7 @@ __device__ __forceinline__ void mask_piece(Raw<S>& r, const Piece& p) {
 
 template <bool kTiny, typename S>
 __device__ __forceinline__ void store_raw(S* row, const Piece& p, int d, const Raw<S>& r) {
-  if (p.skip == 0 && (!kTiny || d >= kPiece)) {
+  if (!kTiny || d >= kPiece) {
     MOE_GLOBAL char* q = piece_ptr(row, p);
     if constexpr (sizeof(S) == 2) {
       *(MOE_GLOBAL u32x4_a2_t*)q = r.w[0];
@@ -118,8 +127,8 @@ __device__ __forceinline__ void store_raw(S* row, const Piece& p, int d, const R
   }
 #pragma unroll
   for (int i = 0; i < kPiece; ++i) {
-    if (i < p.skip || (kTiny && (int)p.at + i >= d)) continue;
-    MOE_GLOBAL char* q = piece_ptr(row, p) + i * sizeof(S);
+    if (p.skip || i >= d) continue;
+    MOE_GLOBAL char* q = (MOE_GLOBAL char*)row + i * sizeof(S);
     if constexpr (sizeof(S) == 2)
       *(MOE_GLOBAL uint16_t*)q = (uint16_t)(r.w[0][i >> 1] >> (16 * (i & 1)));
     else
@@ -169,30 +178,28 @@ __device__ __forceinline__ float load_one(const S* p) {
 }
 
 template <bool kTiny, typename S>
-__device__ __forceinline__ void load_piece(const S* row, const Piece& p, int d, float (&v)[kPiece]) {
-  Raw<S> r = load_raw<kTiny>(row, p, d);
-  mask_piece(r, p);
-  unpack<S>(r, v);
-}
-template <bool kTiny, typename S>
 __device__ __forceinline__ void store_piece(S* row, const Piece& p, int d, const float (&v)[kPiece]) {
   store_raw<kTiny>(row, p, d, pack<S>(v));
 }
 
-// Row t of a tensor.  A wavefront with one row keeps its address in scalar registers, as
-// the base that 32-bit lane offsets add to: without the asm the compiler adds the lane's
-// offset to the tensor's address first, two vector registers per tensor and piece.
+// Row t of a tensor.  A wavefront with one row (not kSub) keeps its address in scalar
+// registers, as the base that 32-bit lane offsets add to; left alone the compiler adds the
+// lane's offset to the tensor's address first, two vector registers per tensor and piece.
+template <typename P>
+__device__ __forceinline__ P uniform_ptr(P p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<P>(((uint64_t)hi << 32) | lo);
+}
 template <typename S, bool kSub>
 __device__ __forceinline__ const S* row_ptr(const void* p, int64_t t, int64_t stride) {
   const S* r = static_cast<const S*>(p) + t * stride;
-  if (!kSub) asm("" : "+s"(r));
-  return r;
+  return kSub ? r : uniform_ptr(r);
 }
 template <typename S, bool kSub>
 __device__ __forceinline__ S* row_ptr(void* p, int64_t t, int64_t stride) {
   S* r = static_cast<S*>(p) + t * stride;
-  if (!kSub) asm("" : "+s"(r));
-  return r;
+  return kSub ? r : uniform_ptr(r);
 }
 
 template <typename S>
