@@ -44,7 +44,6 @@ __device__ __forceinline__ float token_gate(const NormDev& a, int64_t t) {
 // How the threads of a workgroup share rows: `slots` rows at a time, each by 1 << lt lanes of a wavefront or by `waves` whole wavefronts.
 struct NormSplit {
   int lt, waves, slots, threads, pieces;
-  bool ahead;  // gradient: the next row is requested before the current one's arithmetic
 };
 
 // The same value, unknown to the compiler and settled here: nothing that depends on it is
@@ -210,10 +209,10 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
 //
 // Wavefronts per workgroup, one workgroup per CU: what the registers of a row of `bytes`
 // per element and R pieces allow.
-constexpr int norm_back_waves(int R, bool ahead) { return R == 1 ? 16 : R == 2 ? 12 : ahead ? 4 : 8; }
+constexpr int norm_back_waves(int R) { return R == 1 ? 16 : R == 2 ? 12 : 8; }
 
-template <typename S, int R, bool kSub, bool kFull, bool kAhead>
-__global__ __launch_bounds__(64 * norm_back_waves(R, kAhead)) void k_block_norm_backward(NormDev a, NormSplit p) {
+template <typename S, int R, bool kSub, bool kFull>
+__global__ __launch_bounds__(64 * norm_back_waves(R)) void k_block_norm_backward(NormDev a, NormSplit p) {
   __shared__ float sums[2][16 * 8];
   // [wavefront of the row][W, V][R][half][lane]: four elements of a lane's piece each
   extern __shared__ f32x4_t vec[];
@@ -279,42 +278,34 @@ __global__ __launch_bounds__(64 * norm_back_waves(R, kAhead)) void k_block_norm_
   const int64_t step = (int64_t)gridDim.x * p.slots;
   const int64_t rounds = (a.T + step - 1) / step;
   int64_t t = (int64_t)blockIdx.x * p.slots + rl.slot;
-  struct Row {
-    Raw<S> x[R], y[R], dh[R], dn[R], g[R];
-  };
-  Row next;
+  // y and x of the next row are requested before the arithmetic of the current one, dn and
+  // dh at its start: what the registers allow at two wavefronts per SIMD
+  Raw<S> next_x[R], next_y[R];
   auto request = [&](int64_t t) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) next.y[r] = load_raw<kSub>(row_ptr<S, kSub>(y_in, t, y_ld), c[r], a.d);
+    for (int r = 0; r < R; ++r) next_y[r] = load_raw<kSub>(row_ptr<S, kSub>(y_in, t, y_ld), c[r], a.d);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      next.x[r] = load_raw<kSub>(row_ptr<S, kSub>(x_in, t, x_ld), c[r], a.d);
-      next.dn[r] = load_raw<kSub>(row_ptr<S, kSub>(dn_in, t, dn_ld), c[r], a.d);
-      next.dh[r] = load_raw<kSub>(row_ptr<S, kSub>(dh_in, t, dh_ld), c[r], a.d);
-      if (kFull) next.g[r] = load_raw<kSub>(row_ptr<S, kSub>(a.gate, t, a.gate_stride), c[r], a.d);
-    }
+    for (int r = 0; r < R; ++r) next_x[r] = load_raw<kSub>(row_ptr<S, kSub>(x_in, t, x_ld), c[r], a.d);
   };
-  if (kAhead) request(t < a.T ? t : a.T - 1);
+  request(t < a.T ? t : a.T - 1);
   for (int64_t it = 0; it < rounds; ++it, t += step) {
     const bool live = t < a.T;
     const int64_t tc = live ? t : a.T - 1;
-    if (!kAhead) request(tc);
     Raw<S> x[R], y[R], dh[R], dn[R], g[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      x[r] = next.x[r];
-      y[r] = next.y[r];
-      dn[r] = next.dn[r];
-      dh[r] = next.dh[r];
-      if (kFull) g[r] = next.g[r];
-      if (kAhead) {
-        forget(x[r]);
-        forget(y[r]);
-        forget(dn[r]);
-        forget(dh[r]);
-      }
+      dn[r] = load_raw<kSub>(row_ptr<S, kSub>(dn_in, tc, dn_ld), c[r], a.d);
+      dh[r] = load_raw<kSub>(row_ptr<S, kSub>(dh_in, tc, dh_ld), c[r], a.d);
+      if (kFull) g[r] = load_raw<kSub>(row_ptr<S, kSub>(a.gate, tc, a.gate_stride), c[r], a.d);
     }
-    if (kAhead && t + step < a.T) request(t + step);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      x[r] = next_x[r];
+      y[r] = next_y[r];
+      forget(x[r]);
+      forget(y[r]);
+    }
+    if (t + step < a.T) request(t + step);
     const float gt = token_gate<S, kSub>(a, tc);
     float sy[1] = {0.f};
 #pragma unroll
@@ -435,28 +426,49 @@ __global__ __launch_bounds__(64 * norm_back_waves(R, kAhead)) void k_block_norm_
     }
   }
   if (!a.part) return;
-  // the slots' column sums, one slot after the other
-  for (int s = 0; s < p.slots; ++s) {
+  // The slots' column sums, pairwise: the upper half of the slots hands its sums to the
+  // lower one, until one slot has them.
+  const int pitch = (p.slots / 2) * rl.lanes;  // threads that hand over in the first round
+  auto hand_at = [&](int k, int slot) -> f32x4_t& { return vec[k * pitch + slot * rl.lanes + rl.lane]; };
+  for (int n = p.slots; n > 1;) {
+    const int half = (n + 1) / 2;
     __syncthreads();
-    if (rl.slot != s) continue;
+    if (rl.slot >= half && rl.slot < n) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (s > 0) {
-        float v[kPiece];
-        vec_get(0, r, v);
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) A[r][i] += v[i];
-        vec_get(1, r, v);
+        for (int k = 0; k < 2; ++k) {
+          hand_at(4 * r + k, rl.slot - half) =
+              f32x4_t{A[r][4 * k], A[r][4 * k + 1], A[r][4 * k + 2], A[r][4 * k + 3]};
+          hand_at(4 * r + 2 + k, rl.slot - half) =
+              f32x4_t{B[r][4 * k], B[r][4 * k + 1], B[r][4 * k + 2], B[r][4 * k + 3]};
+        }
+    }
+    __syncthreads();
+    if (rl.slot < n - half) {
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) B[r][i] += v[i];
-      }
-      if (s + 1 < p.slots) {
-        vec_put(0, r, A[r]);
-        vec_put(1, r, B[r]);
-      } else {
-        float* out = a.part + (int64_t)blockIdx.x * 2 * a.d;
-        store_piece<kSub>(out, c[r], a.d, A[r]);
-        store_piece<kSub>(out + a.d, c[r], a.d, B[r]);
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const f32x4_t u = hand_at(4 * r + k, rl.slot), v = hand_at(4 * r + 2 + k, rl.slot);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            A[r][4 * k + i] += u[i];
+            B[r][4 * k + i] += v[i];
+          }
+        }
+    }
+    n = half;
+  }
+  if (rl.slot != 0) return;
+  float* out = a.part + (int64_t)blockIdx.x * 2 * a.d;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) {  // (plain stores: the next launch reads them)
+      if (i >= c[r].skip && (!kSub || (int)c[r].at + i < a.d)) {
+        out[c[r].at + i] = A[r][i];
+        out[a.d + c[r].at + i] = B[r][i];
       }
     }
   }
@@ -518,8 +530,7 @@ static NormSplit norm_back_split(int T, int d, int dtype) {
   p.lt = 0;
   while (p.lt < 6 && (1 << p.lt) < lanes) ++p.lt;
   p.waves = (int)ceil_div(lanes, 64);
-  p.ahead = bytes == 2 && p.pieces == 4 && p.waves == 1;
-  const int most = norm_back_waves(p.pieces, p.ahead);
+  const int most = norm_back_waves(p.pieces);
   const int per_wave = 64 >> p.lt;
   int groups = p.waves > 1 ? most / p.waves : most;  // wavefronts (or groups of them) per workgroup
   groups = (int)std::max<int64_t>(1, std::min<int64_t>(groups, ceil_div(T, 256 * per_wave)));
@@ -528,7 +539,10 @@ static NormSplit norm_back_split(int T, int d, int dtype) {
   return p;
 }
 static int64_t norm_back_lds(const NormSplit& p) {
-  return (int64_t)2 * p.pieces * kPiece * 4 * 64 * p.waves;
+  const int lanes = p.waves > 1 ? p.waves * 64 : 1 << p.lt;
+  const int64_t vectors = (int64_t)2 * p.pieces * kPiece * 4 * 64 * p.waves;
+  const int64_t handed = (int64_t)2 * p.pieces * kPiece * 4 * (p.slots / 2) * lanes;
+  return std::max(vectors, handed);
 }
 
 // workgroups of the gradient: one per CU (its registers allow one), so that their column
@@ -684,33 +698,25 @@ extern "C" int moe_block_norm_backward(const moe_block_norm_args* a, const moe_b
           (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         hipLaunchKernelGGL(kernel, dim3(groups), dim3(p.threads), (unsigned)lds, s, v, p);
       };
-      auto go = [&](auto pieces, auto sub, auto ahead) {
+      auto go = [&](auto pieces, auto sub) {
         constexpr int R = decltype(pieces)::value;
-        constexpr bool kSub = decltype(sub)::value, kAhead = decltype(ahead)::value;
+        constexpr bool kSub = decltype(sub)::value;
         if (a->gate_kind == MOE_GATE_FULL)
-          launch(k_block_norm_backward<S, R, kSub, true, kAhead>);
+          launch(k_block_norm_backward<S, R, kSub, true>);
         else
-          launch(k_block_norm_backward<S, R, kSub, false, kAhead>);
+          launch(k_block_norm_backward<S, R, kSub, false>);
       };
       using std::integral_constant;
-      const std::true_type yes;
-      const std::false_type no;
       if (p.lt < 6)
-        go(integral_constant<int, 1>{}, yes, no);
+        go(integral_constant<int, 1>{}, std::true_type{});
       else if (p.pieces == 1)
-        go(integral_constant<int, 1>{}, no, no);
+        go(integral_constant<int, 1>{}, std::false_type{});
       else if (p.pieces == 2)
-        go(integral_constant<int, 2>{}, no, no);
+        go(integral_constant<int, 2>{}, std::false_type{});
       else if (p.pieces == 3)
-        go(integral_constant<int, 3>{}, no, no);
-      else if constexpr (sizeof(S) == 2) {
-        if (p.ahead)
-          go(integral_constant<int, 4>{}, no, yes);
-        else
-          go(integral_constant<int, 4>{}, no, no);
-      } else {
-        go(integral_constant<int, 4>{}, no, no);
-      }
+        go(integral_constant<int, 3>{}, std::false_type{});
+      else
+        go(integral_constant<int, 4>{}, std::false_type{});
     }
     if (vectors)
       hipLaunchKernelGGL(k_norm_vectors<S>, dim3((unsigned)ceil_div(a->d, 32), 2), dim3(1024), 0, s, v.part, groups, v,

@@ -113,15 +113,18 @@ __device__ __forceinline__ void mask_piece(Raw<S>& r, const Piece& p) {
   }
 }
 
+// Rows are stored past the L2 (non-temporal): what a launch leaves dirty there is written
+// back at its end, when nothing else runs (permute at T = 4096, d = 2048, k = 8: 30.5 to
+// 26.3 us, block norm gradient 43.8 to 40.3; small calls unchanged).
 template <bool kTiny, typename S>
 __device__ __forceinline__ void store_raw(S* row, const Piece& p, int d, const Raw<S>& r) {
   if (!kTiny || d >= kPiece) {
     MOE_GLOBAL char* q = piece_ptr(row, p);
     if constexpr (sizeof(S) == 2) {
-      *(MOE_GLOBAL u32x4_a2_t*)q = r.w[0];
+        __builtin_nontemporal_store(r.w[0], (MOE_GLOBAL u32x4_a2_t*)q);
     } else {
-      *(MOE_GLOBAL u32x4_a4_t*)q = r.w[0];
-      *(MOE_GLOBAL u32x4_a4_t*)(q + 16) = r.w[1];
+      __builtin_nontemporal_store(r.w[0], (MOE_GLOBAL u32x4_a4_t*)q);
+      __builtin_nontemporal_store(r.w[1], (MOE_GLOBAL u32x4_a4_t*)(q + 16));
     }
     return;
   }
