@@ -35,7 +35,10 @@ struct TokenSplit {
 // rows' addresses stay in scalar registers, and the loads of KB rows go out before the
 // first use.  Pairs that were dropped read some row that is there (`sorted_in` always has
 // one) and are masked, so that no load sits under a branch.
-template <typename S, bool kSpread, bool kProducts, int KM, int KB>
+// kStream: the sorted rows, each read once, by non-temporal loads.  That is for rows on
+// 16-byte boundaries (unpermute at T = 4096, d = 2048, k = 8: 29.0 to 26.8 us): off them
+// two lanes share a cache line, which is then fetched twice (odd gradient 4.8 to 5.5 us).
+template <typename S, bool kSpread, bool kProducts, int KM, int KB, bool kStream>
 __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __restrict__ pair_pos,
                                                const float* __restrict__ weights, TokenSplit p) {
   __shared__ float part_sums[kProducts ? 16 : 1][KM];
@@ -79,7 +82,7 @@ __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __re
       if (!kSpread || kProducts) {
 #pragma unroll
         for (int b = 0; b < KB; ++b)
-          row[b] = load_raw<false>(row_ptr<S, false>(a.sorted_in, pos[j0 + b], a.sorted_in_stride), c, a.d);
+          row[b] = load_raw<false, kStream>(row_ptr<S, false>(a.sorted_in, pos[j0 + b], a.sorted_in_stride), c, a.d);
       }
 #pragma unroll
       for (int b = 0; b < KB; ++b) {
@@ -195,26 +198,32 @@ static int launch_rows(const char* name, int timing_id, bool spread, int dtype, 
   timing_begin(timing_id, s);
   with_dtype(dtype, [&](auto v) {
     using S = decltype(v);
-    auto go = [&](auto spread_c, auto products_c) {
+    auto go = [&](auto spread_c, auto products_c, auto stream_c) {
       constexpr bool kSpread = decltype(spread_c)::value, kProducts = decltype(products_c)::value;
+      constexpr bool kStream = decltype(stream_c)::value;
       auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(p.threads), 0, s, a, pair_pos, weights, p); };
       if (p.lt < 6)
         launch(k_rows_short<S, kSpread, kProducts>);
       else if (a.k <= 2)
-        launch(k_rows<S, kSpread, kProducts, 2, 2>);
+        launch(k_rows<S, kSpread, kProducts, 2, 2, kStream>);
       else if (a.k <= 4)
-        launch(k_rows<S, kSpread, kProducts, 4, 4>);
+        launch(k_rows<S, kSpread, kProducts, 4, 4, kStream>);
       else if (a.k <= 8)
-        launch(k_rows<S, kSpread, kProducts, 8, 8>);
+        launch(k_rows<S, kSpread, kProducts, 8, 8, kStream>);
       else
-        launch(k_rows<S, kSpread, kProducts, 16, 8>);
+        launch(k_rows<S, kSpread, kProducts, 16, 8, kStream>);
     };
     const std::true_type yes;
     const std::false_type no;
-    if (spread)
-      a.dweights ? go(yes, yes) : go(yes, no);
+    const bool stream = ((uintptr_t)a.sorted_in | (uintptr_t)(a.sorted_in_stride * (int64_t)sizeof(S))) % 16 == 0;
+    if (spread && !a.dweights)
+      go(yes, no, no);
+    else if (spread)
+      stream ? go(yes, yes, yes) : go(yes, yes, no);
+    else if (a.dweights)
+      stream ? go(no, yes, yes) : go(no, yes, no);
     else
-      a.dweights ? go(no, yes) : go(no, no);
+      stream ? go(no, no, yes) : go(no, no, no);
   });
   timing_end(timing_id, s);
   return check_launch(name);

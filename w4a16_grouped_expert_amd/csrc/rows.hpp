@@ -66,13 +66,19 @@ __device__ __forceinline__ MOE_GLOBAL char* piece_ptr(S* row, const Piece& p) {
   return (MOE_GLOBAL char*)row + piece_offset<S>(p);
 }
 
-template <bool kTiny, typename S>
+// kStream: non-temporal.
+template <bool kTiny, bool kStream = false, typename S>
 __device__ __forceinline__ Raw<S> load_raw(const S* row, const Piece& p, int d) {
   Raw<S> r;
   if (!kTiny || d >= kPiece) {
     const MOE_GLOBAL char* q = piece_ptr(row, p);
-    if constexpr (sizeof(S) == 2) {
+    if constexpr (sizeof(S) == 2 && kStream) {
+      r.w[0] = __builtin_nontemporal_load((const MOE_GLOBAL u32x4_a2_t*)q);
+    } else if constexpr (sizeof(S) == 2) {
       r.w[0] = *(const MOE_GLOBAL u32x4_a2_t*)q;
+    } else if constexpr (kStream) {
+      r.w[0] = __builtin_nontemporal_load((const MOE_GLOBAL u32x4_a4_t*)q);
+      r.w[1] = __builtin_nontemporal_load((const MOE_GLOBAL u32x4_a4_t*)(q + 16));
     } else {
       r.w[0] = *(const MOE_GLOBAL u32x4_a4_t*)q;
       r.w[1] = *(const MOE_GLOBAL u32x4_a4_t*)(q + 16);
