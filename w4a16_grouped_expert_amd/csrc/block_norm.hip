@@ -464,13 +464,8 @@ __global__ __launch_bounds__(64 * norm_back_waves(R)) void k_block_norm_backward
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.d;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) {  // (plain stores: the next launch reads them)
-      if (i >= c[r].skip && (!kSub || (int)c[r].at + i < a.d)) {
-        out[c[r].at + i] = A[r][i];
-        out[a.d + c[r].at + i] = B[r][i];
-      }
-    }
+    store_piece<kSub, false>(out, c[r], a.d, A[r]);
+    store_piece<kSub, false>(out + a.d, c[r], a.d, B[r]);
   }
 }
 

@@ -334,7 +334,8 @@ __device__ __forceinline__ void run_dx(const RouteBackDev& a, float* tile, const
         o[i] = pack_bf16x2(acc[b][2 * i][q] + __uint_as_float(add << 16),
                            acc[b][2 * i + 1][q] + __uint_as_float(add & 0xFFFF0000u));
       }
-      *(MOE_GLOBAL u32x4_t*)(base + 2 * ((uint32_t)t * (uint32_t)a.d + (uint32_t)col)) = o;
+      __builtin_nontemporal_store(
+          o, (MOE_GLOBAL u32x4_t*)(base + 2 * ((uint32_t)t * (uint32_t)a.d + (uint32_t)col)));
     }
 }
 

@@ -121,16 +121,22 @@ __device__ __forceinline__ void mask_piece(Raw<S>& r, const Piece& p) {
 
 // Rows are stored past the L2 (non-temporal): what a launch leaves dirty there is written
 // back at its end, when nothing else runs (permute at T = 4096, d = 2048, k = 8: 30.5 to
-// 26.3 us, block norm gradient 43.8 to 40.3; small calls unchanged).
-template <bool kTiny, typename S>
+// 26.3 us, block norm gradient 43.8 to 40.3; small calls unchanged).  kStream = false: plain
+// stores, for what the next launch reads.
+template <bool kTiny, bool kStream = true, typename S>
 __device__ __forceinline__ void store_raw(S* row, const Piece& p, int d, const Raw<S>& r) {
   if (!kTiny || d >= kPiece) {
     MOE_GLOBAL char* q = piece_ptr(row, p);
-    if constexpr (sizeof(S) == 2) {
-        __builtin_nontemporal_store(r.w[0], (MOE_GLOBAL u32x4_a2_t*)q);
-    } else {
+    if constexpr (sizeof(S) == 2 && kStream) {
+      __builtin_nontemporal_store(r.w[0], (MOE_GLOBAL u32x4_a2_t*)q);
+    } else if constexpr (sizeof(S) == 2) {
+      *(MOE_GLOBAL u32x4_a2_t*)q = r.w[0];
+    } else if constexpr (kStream) {
       __builtin_nontemporal_store(r.w[0], (MOE_GLOBAL u32x4_a4_t*)q);
       __builtin_nontemporal_store(r.w[1], (MOE_GLOBAL u32x4_a4_t*)(q + 16));
+    } else {
+      *(MOE_GLOBAL u32x4_a4_t*)q = r.w[0];
+      *(MOE_GLOBAL u32x4_a4_t*)(q + 16) = r.w[1];
     }
     return;
   }
@@ -186,9 +192,9 @@ __device__ __forceinline__ float load_one(const S* p) {
     return (float)*(const MOE_GLOBAL S*)p;
 }
 
-template <bool kTiny, typename S>
+template <bool kTiny, bool kStream = true, typename S>
 __device__ __forceinline__ void store_piece(S* row, const Piece& p, int d, const float (&v)[kPiece]) {
-  store_raw<kTiny>(row, p, d, pack<S>(v));
+  store_raw<kTiny, kStream>(row, p, d, pack<S>(v));
 }
 
 // Row t of a tensor.  A wavefront with one row (not kSub) keeps its address in scalar
