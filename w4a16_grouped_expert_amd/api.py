@@ -433,41 +433,41 @@ DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # moe_dtype in
 
 
 def _launch(fn, device, stream, *args):
-    """fn(*args, stream handle) with `device` current; the stream defaults to that device's
-    current one (whose handle alone is asked for: a Stream object costs 1.6 us a call)."""
+    """fn(*args, stream handle) with GPU `device` (an index) current; the stream defaults to
+    that GPU's current one (whose handle alone is asked for: a Stream object costs 1.6 us)."""
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
-    elif stream.device != device:
-        raise ValueError(f"stream on {stream.device} for tensors on {device}")
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    elif stream.device.index != device:
+        raise ValueError(f"stream on {stream.device} for tensors on GPU {device}")
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
+    if torch.cuda.current_device() == device:
         return fn(*args, handle)
     with torch.cuda.device(device):
         return fn(*args, handle)
 
 
 def _like(t, name, dtype, shape, device):
-    """A contiguous tensor of this type and shape on `device`: its address."""
-    if t.dtype != dtype:
+    """A contiguous tensor of this type and shape on GPU `device`: its address."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on GPU {device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
     return t.data_ptr()
 
 
 def _rows(t, name, dtype, T, d, device, output=False):
     """A [T, d] tensor with contiguous rows at any stride: its address and row stride."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != d:
+    if t.shape != (T, d):
         raise ValueError(f"{name} must have shape ({T}, {d}), got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on GPU {device}, got {t.device}")
     stride, inner = t.stride()
     if inner != 1 and d > 1:
         raise ValueError(f"{name} must have contiguous rows")
@@ -479,25 +479,29 @@ def _rows(t, name, dtype, T, d, device, output=False):
 
 
 def _row_type(t, name):
+    """Type, GPU index, and the two sizes of a row tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in DTYPES:
-        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    if not t.is_cuda:
+    dtype = t.dtype
+    if dtype not in DTYPES:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {dtype}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(shape)}")
+    device = t.get_device()
+    if device < 0:
         raise ValueError(f"{name} must be a GPU tensor")
-    return t.dtype, t.device
+    return dtype, device, *shape
 
 
 def _pairs(pair_pos, weights, dweights, T, k, device):
     """Addresses of pair_pos (at least T*k positions), weights and dweights ([T, k])."""
-    if pair_pos.dtype != torch.int32:
+    if pair_pos.dtype is not torch.int32:
         raise TypeError(f"pair_pos must be torch.int32, got {pair_pos.dtype}")
-    if not pair_pos.is_contiguous() or pair_pos.numel() < T * k:
+    if pair_pos.numel() < T * k or not pair_pos.is_contiguous():
         raise ValueError(f"pair_pos must be contiguous with at least {T * k} positions")
-    if pair_pos.device != device:
-        raise ValueError(f"pair_pos must be on {device}, got {pair_pos.device}")
+    if pair_pos.get_device() != device:
+        raise ValueError(f"pair_pos must be on GPU {device}, got {pair_pos.device}")
     w = None if weights is None else _like(weights, "weights", torch.float32, (T, k), device)
     dw = None if dweights is None else _like(dweights, "dweights", torch.float32, (T, k), device)
     return pair_pos.data_ptr(), w, dw
@@ -509,8 +513,7 @@ def moe_permute_into(x, pair_pos, k, rows, weights: Optional[torch.Tensor] = Non
     x [T, d] and rows [num_rows, d] bf16, fp16 or fp32 with any row stride; pair_pos from
     moe_align (AlignOut.pair_pos).  Pairs whose position is negative or past the last row
     are dropped; rows that no pair names keep their contents."""
-    dtype, dev = _row_type(x, "x")
-    T, d = x.shape
+    dtype, dev, T, d = _row_type(x, "x")
     R = rows.shape[0]
     xp, xs = _rows(x, "x", dtype, T, d, dev)
     rp, rs = _rows(rows, "rows", dtype, R, d, dev, True)
@@ -523,8 +526,7 @@ def moe_permute_into(x, pair_pos, k, rows, weights: Optional[torch.Tensor] = Non
 def moe_unpermute_into(rows, pair_pos, k, out, weights: Optional[torch.Tensor] = None, stream=None):
     """out[t] = sum over j of rows[pair_pos[t*k + j]], times weights[t, j] if given
     (float32 sums in slot order, one rounding; dropped pairs add nothing)."""
-    dtype, dev = _row_type(rows, "rows")
-    R, d = rows.shape
+    dtype, dev, R, d = _row_type(rows, "rows")
     T = out.shape[0]
     rp, rs = _rows(rows, "rows", dtype, R, d, dev)
     op, os = _rows(out, "out", dtype, T, d, dev, True)
@@ -538,10 +540,9 @@ def moe_permute_backward_into(drows, pair_pos, k, dx, weights: Optional[torch.Te
                               x: Optional[torch.Tensor] = None, dweights: Optional[torch.Tensor] = None, stream=None):
     """Gradient of moe_permute: dx[t] = sum over j of w drows[pos]; with x and dweights
     also dweights[t, j] = <x[t], drows[pos]> (0 for dropped pairs)."""
-    dtype, dev = _row_type(drows, "drows")
+    dtype, dev, R, d = _row_type(drows, "drows")
     if (x is None) != (dweights is None):
         raise ValueError("x and dweights go together")
-    R, d = drows.shape
     T = dx.shape[0]
     rp, rs = _rows(drows, "drows", dtype, R, d, dev)
     op, os = _rows(dx, "dx", dtype, T, d, dev, True)
@@ -558,10 +559,9 @@ def moe_unpermute_backward_into(dout, pair_pos, k, drows, weights: Optional[torc
     """Gradient of moe_unpermute: drows[pos] = w dout[t]; with rows and dweights also
     dweights[t, j] = <dout[t], rows[pos]> (0 for dropped pairs).  Rows of drows that no
     pair names keep their contents."""
-    dtype, dev = _row_type(dout, "dout")
+    dtype, dev, T, d = _row_type(dout, "dout")
     if (rows is None) != (dweights is None):
         raise ValueError("rows and dweights go together")
-    T, d = dout.shape
     R = drows.shape[0]
     op, os = _rows(dout, "dout", dtype, T, d, dev)
     dp, ds = _rows(drows, "drows", dtype, R, d, dev, True)
@@ -613,9 +613,7 @@ def moe_route_backward_into(x, w_router, route: RouteOut, dweights, dx: Optional
     dw_router [E, d] float32; either may be None.  dlogits [T, E] float32 adds the
     gradient of a loss on the logits themselves.  `route` and `renormalize` as moe_route
     had them."""
-    _row_type(x, "x")
-    dev = x.device
-    T, d = x.shape
+    _, dev, T, d = _row_type(x, "x")
     E, k = w_router.shape[0], route.ids.shape[1]
     bf, f32 = torch.bfloat16, torch.float32
     a = _lib.RouteBackwardArgs()
@@ -675,8 +673,7 @@ class BlockNormGrads:
 
 
 def _block_norm_args(norm: BlockNorm, x, y):
-    dtype, dev = _row_type(x, "x")
-    T, d = x.shape
+    dtype, dev, T, d = _row_type(x, "x")
     a = _lib.BlockNormArgs()
     a.dtype, a.T, a.d = DTYPES[dtype], T, d
     a.x, a.x_stride = _rows(x, "x", dtype, T, d, dev)
