@@ -48,7 +48,7 @@ def stats_error(norm, x, y, d):
     h, _ = orow.block_norm(f64(x), f64(y), **p)
     rel = c * U32 + np.sqrt((eh * eh).mean(axis=1, keepdims=True)
                             / ((h * h).mean(axis=1, keepdims=True) + p["eps"]))
-    return h, eh, rel
+    return h, eh, rel, ax + gz
 
 
 def check_forward(name, norm, x, y, lay=lambda t: t):
@@ -59,7 +59,7 @@ def check_forward(name, norm, x, y, lay=lambda t: t):
     torch.cuda.synchronize()
     p = params(norm)
     rh, rn = orow.block_norm(f64(x), f64(y), **p)
-    _, eh, rel = stats_error(norm, x, y, d)
+    _, eh, rel, _ = stats_error(norm, x, y, d)
     assert_near(name + " h", h, rh, half_step(x.dtype, np.abs(rh) + eh) + eh)
     if n is not None:
         en = np.abs(rn) * (rel + 4 * U32) + np.abs(p["norm_in"]) * orow.rstd(rh, p["eps"]) * eh
@@ -72,12 +72,14 @@ def check_backward(name, norm, x, y, dh, dn, lay=lambda t: t):
     p = params(norm)
     ref = orow.block_norm_backward(f64(x), f64(y), **p, dh=f64(dh), dn=f64(dn))
     # the same formulas with every term's absolute value: what float32 roundings scale with
-    h, _, rel = stats_error(norm, x, y, d)
+    h, _, rel, parts = stats_error(norm, x, y, d)
     D = np.zeros((T, d)) if dh is None else np.abs(f64(dh))
     amount = {}
     if norm.norm_in is not None:
         r = orow.rstd(h, p["eps"])
-        a, hn = np.abs(np.zeros((T, d)) if dn is None else f64(dn)), np.abs(h) * r
+        # h = a x + g z comes with an error of a few 2^-24 of |a x| + |g z|, however far the
+        # two cancel in h itself: that sum, not |h|, is what the errors of hn scale with
+        a, hn = np.abs(np.zeros((T, d)) if dn is None else f64(dn)), parts * r
         u = a * np.abs(p["norm_in"])
         amount["dnorm_in"] = a * hn
         D = D + r * (u + hn * (u * hn).mean(axis=1, keepdims=True))
@@ -186,6 +188,64 @@ def test_in_place_outputs():
             moe.moe_block_norm_backward_into(norm, x, yy, out, ws, dx, dd)
             for q in ("dx", "dy", "dgate", "dnorm_out", "dnorm_in"):
                 assert torch.equal(getattr(out, q), getattr(ref, q)), (dy_is, q)
+
+
+@pytest.mark.parametrize("d", [2052, 4104, 8201])
+def test_in_place_without_norms(d):
+    """Rows of several wavefronts whose last pieces overlap, h in place of x or y, dx in
+    place of dh: no norm, so no row sum orders loads and stores."""
+    say(f"block norm in place, no norms, d={d}")
+    T = 600
+    norm, x, y, dh, _ = make(T, d, torch.bfloat16, "channel", norm_out=False, norm_in=False)
+    ref, _ = moe.moe_block_norm(norm, x, y)
+    for _ in range(5):
+        h = x.clone()
+        moe.moe_block_norm_into(norm, h, y, h)
+        assert torch.equal(h, ref)
+        h = y.clone()
+        moe.moe_block_norm_into(norm, x, h, h)
+        assert torch.equal(h, ref)
+    only = moe.BlockNorm(residual_scale=0.5)
+    ref = moe.moe_block_norm_backward(only, x, None, dh).dx
+    for _ in range(5):
+        dx = dh.clone()
+        moe.moe_block_norm_backward_into(only, x, None, moe.BlockNormGrads(dx=dx), None, dx)
+        assert torch.equal(dx, ref)
+
+
+def test_broadcast_inputs():
+    """One row for every token as residual stream, block output, gate or gradient."""
+    say("block norm of expanded rows")
+    T, d = 9, 520
+    norm, x, y, dh, dn = make(T, d, torch.float32, "full")
+    norm.gate = norm.gate[:1].expand(T, d)
+    x, y, dh, dn = (t[:1].expand(T, d) for t in (x, y, dh, dn))
+    check_forward("expanded", norm, x, y)
+    check_backward("expanded", norm, x, y, dh, dn)
+    norm.gate = norm.gate[:1, :1].expand(T, 1)
+    check_forward("expanded token gate", norm, x, y)
+    check_backward("expanded token gate", norm, x, y, dh, dn)
+
+
+def test_long_rows_captured():
+    """Rows whose vectors need more than 64 KiB of LDS, in a captured graph."""
+    say("block norm d=16384 captured")
+    T, d = 300, 16384
+    norm, x, y, dh, dn = make(T, d, torch.bfloat16, "channel")
+    ws = moe.alloc_block_norm_workspace(T, d, DEV)
+    f = dict(dtype=torch.float32, device=DEV)
+    grads = moe.BlockNormGrads(torch.empty_like(x), torch.empty_like(x), torch.empty(d, **f), torch.empty(d, **f),
+                               torch.empty(d, **f))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_block_norm_backward_into(norm, x, y, grads, ws, dh, dn)
+    ref = moe.moe_block_norm_backward(norm, x, y, dh, dn)
+    for i in range(3):
+        grads.dx.zero_(), grads.dnorm_in.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for q in ("dx", "dy", "dgate", "dnorm_out", "dnorm_in"):
+            assert torch.equal(getattr(grads, q), getattr(ref, q)), (i, q)
 
 
 def test_no_rows():

@@ -167,6 +167,40 @@ def test_weights_bits_and_determinism():
         assert torch.equal(a, b)
 
 
+def test_two_streams_at_once():
+    """Calls that share their inputs run on two streams at a time."""
+    say("permute on two streams at once")
+    T, d, k = 2000, 1032, 4
+    pos, w, x, r, _ = make(T, d, k, torch.bfloat16, True, 0.1)
+    ref = moe.moe_unpermute(r, pos, k, T, w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.empty_like(x) for _ in range(8)] for _ in streams]
+    for i in range(8):
+        for s, o in zip(streams, outs):
+            moe.moe_unpermute_into(r, pos, k, o[i], w, stream=s)
+    torch.cuda.synchronize()
+    for o in outs:
+        for t in o:
+            assert torch.equal(t, ref)
+
+
+def test_timing_hooks():
+    say("timing of the row operators")
+    T, d, k = 64, 256, 2
+    pos, w, x, r, _ = make(T, d, k, torch.bfloat16, True, 0.0)
+    moe.timing_reset()
+    moe.timing_enable(True)
+    moe.moe_permute(x, pos, k)
+    moe.moe_unpermute(r, pos, k, T, w)
+    moe.moe_unpermute(r, pos, k, T, w)
+    moe.timing_enable(False)
+    ms, n = moe.timing_read("permute")
+    assert n == 1 and ms > 0
+    assert moe.timing_read("unpermute")[1] == 2
+    moe.timing_reset()
+
+
 def test_offsets_past_32_bits():
     T, d, k = 1 << 17, 2304, 8  # 2.4e9 elements of sorted rows
     say(f"permute with {T * k * d} elements")

@@ -136,10 +136,16 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
     if (a.v_in) vi[r] = load_raw<kSub>(static_cast<const S*>(a.v_in), c[r], a.d);
   }
   const float gt = token_gate<S, kSub>(a, tc);
+  // (x and y are in registers before the barrier that the first store waits for: h may lie
+  // where they do, and the last pieces of two wavefronts may overlap)
 #pragma unroll
   for (int r = 0; r < R; ++r) {
+    forget(rx[r]);
     unpack<S>(rx[r], h[r]);
-    if (a.y) unpack<S>(ry_[r], z[r]);
+    if (a.y) {
+      forget(ry_[r]);
+      unpack<S>(ry_[r], z[r]);
+    }
   }
   float hh[1] = {0.f};
   if (a.y) {
@@ -167,8 +173,6 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) h[r][i] *= a.scale;
   }
-  // h may lie where x or y does, and pieces of two wavefronts may overlap: no store before
-  // the row's last load
   if (!kSub && p.waves > 1 && !a.v_out) __syncthreads();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
