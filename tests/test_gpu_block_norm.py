@@ -136,6 +136,13 @@ def test_every_part(gate, norm_out, norm_in):
             check_backward(type_ + " dh alone", norm, x, y, dh, None)
 
 
+def test_many_long_rows_without_norm_out():
+    """Rows of several wavefronts, several rows per workgroup, one round of sums each."""
+    say("block norm T=1500 d=4104 without norm_out")
+    norm, x, y, dh, dn = make(1500, 4104, torch.bfloat16, "token", norm_out=False)
+    check_backward("no norm_out", norm, x, y, dh, dn)
+
+
 def test_norm_alone():
     say("block norm without a block output")
     norm, x, _, dh, dn = make(40, 328, torch.bfloat16, "none", y=False, norm_out=False)

@@ -41,7 +41,8 @@ __device__ __forceinline__ float token_gate(const NormDev& a, int64_t t) {
   return a.gate_kind == MOE_GATE_TOKEN ? load_one(row_ptr<S, kSub>(a.gate, t, a.gate_stride)) : 1.f;
 }
 
-// How the threads of a workgroup share rows: `slots` rows at a time, each by 1 << lt lanes of a wavefront or by `waves` whole wavefronts.
+// How the threads of a workgroup share rows: `slots` rows at a time, each by 1 << lt
+// lanes of a wavefront or by `waves` whole wavefronts.
 struct NormSplit {
   int lt, waves, slots, threads, pieces;
 };
@@ -59,9 +60,9 @@ __device__ __forceinline__ void forget(Raw<S>& r) {
 }
 
 // sums over the threads of a row, in each of them.  Rows of several wavefronts meet in
-// LDS; the caller alternates between two buffers, so that one barrier is enough: a
-// wavefront that writes a buffer again has passed the barrier of the other one, which
-// every wavefront reaches after it has read the first.
+// LDS.  One call after the other takes the other of two buffers (the caller counts them),
+// so that one barrier is enough: a wavefront that writes a buffer again has passed the
+// barrier of the other one, which every wavefront reaches after it has read the first.
 template <bool kSub, int K>
 __device__ __forceinline__ void row_sums(float (&v)[K], const NormSplit& p, float* buf) {
 #pragma unroll
@@ -231,6 +232,7 @@ __global__ __launch_bounds__(64 * norm_back_waves(R)) void k_block_norm_backward
   const uint32_t dn_on = __builtin_amdgcn_readfirstlane(a.dn ? ~0u : 0u);
   const uint32_t y_on = __builtin_amdgcn_readfirstlane(a.y ? ~0u : 0u);
   float A[R][kPiece], B[R][kPiece];
+  int turn = 0;  // of the sums' buffers: a row without norm_out has one round of sums, others two
   Piece c[R];
   f32x4_t* const vec_mine = vec + (rl.lane >> 6) * (4 * R * 64) + (rl.lane & 63);
   auto vec_at = [&](int k, int r, int half) -> f32x4_t& { return vec_mine[((k * R + r) * 2 + half) * 64]; };
@@ -322,7 +324,8 @@ __global__ __launch_bounds__(64 * norm_back_waves(R)) void k_block_norm_backward
     }
     float ry = 1.f;
     if (a.v_out) {
-      row_sums<kSub>(sy, p, sums[0]);
+      row_sums<kSub>(sy, p, sums[turn]);
+      turn ^= 1;
       ry = rsqrtf(sy[0] * a.inv_d + a.eps);
     }
     // the piece's u, q and h, scaled: sx x + sq q; own: q and h zero (and with them every
@@ -371,7 +374,8 @@ __global__ __launch_bounds__(64 * norm_back_waves(R)) void k_block_norm_backward
 #pragma unroll
       for (int i = 0; i < 5; ++i) forget(s[i]);
     }
-    row_sums<kSub>(s, p, sums[1]);  // (its barrier also ends the row's loads before a store in their place)
+    row_sums<kSub>(s, p, sums[turn]);  // (its barrier also ends the row's loads before a store in their place)
+    turn ^= 1;
     const float rh = a.dn ? rsqrtf(s[0] * a.inv_d + a.eps) : 0.f;
     const float mh = rh * (s[1] * a.inv_d);  // mean(u hn)
     const float qD = s[2] + rh * (s[3] - mh * (rh * s[4]));
