@@ -380,7 +380,7 @@ int moe_mat_decode_layer(const moe_decode_layer_args* args, float tau, void* str
  *  without weights copies the bits).  Deterministic.  Outputs may not overlap inputs.
  *  dweights may be NULL (not wanted); then x (rows) may be NULL.  weights may be NULL
  *  with dweights wanted.
- *  Limits: 1 <= k <= 16, T*k <= 2^24, 1 <= d <= 2^24.  T == 0 is a no-op.
+ *  Limits: 1 <= k <= 16, T*k <= 2^24, 1 <= d <= 2^24, T*d <= 2^34.  T == 0 is a no-op.
  */
 enum moe_dtype { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 };
 
@@ -413,7 +413,8 @@ int moe_unpermute_backward(const void* dout, int64_t dout_stride, const void* ro
  *  dw_router [E][d] float32 output: (gradient of the logits)^T x.  NULL: not wanted.
  *  The gradient of the logits enters the matrix cores as a sum of bf16 parts: two for
  *  dx (relative error 2^-18, under its bf16 rounding), three for dw_router (2^-27),
- *  with float32 sums.  Deterministic.
+ *  with float32 sums.  Deterministic.  Infinite values may come out as NaN.  Outputs may
+ *  not overlap inputs (but for dx_add) or each other.
  *  workspace moe_route_backward_workspace_bytes(T, d, E, k) bytes, 256-byte aligned.
  *  Entries of topk_ids outside [0, E) are ignored; the ids of a token are distinct.
  *  Limits and errors: those of moe_route; x, w_router, dx and dx_add 16-byte aligned;
@@ -458,11 +459,11 @@ int moe_route_backward(const moe_route_backward_args* args, void* stream);
  *  Every tensor has the type `dtype`.  Rows are contiguous at the given strides
  *  (elements; inputs at least 0, outputs at least d); pointers need the alignment of
  *  their type only.  Statistics and products in float32; n is computed from h before
- *  h is rounded.  h may be x or y itself, n may be y; otherwise outputs may not
- *  overlap inputs or each other.
+ *  h is rounded.  h may be x or y itself, n may be y, at the same stride; otherwise
+ *  outputs may not overlap inputs or each other.
  *  eps at least FLT_MIN; residual_scale finite.  Squares are summed in float32: rows
  *  must have mean squares below 2^127 / d.
- *  Limits: 1 <= d <= 16384, T <= 2^24.  T == 0 is a no-op.
+ *  Limits: 1 <= d <= 16384, T <= 2^24, T*d <= 2^34.  T == 0 is a no-op.
  *
  * moe_block_norm_backward -- its gradient, from dh and dn (either may be NULL: zero;
  *  dn only where norm_in is given), recomputing the statistics from x and y.
@@ -471,8 +472,8 @@ int moe_route_backward(const moe_route_backward_args* args, void* stream);
  *            MOE_GATE_FULL: [T][d], type dtype, rows at dgate_stride.  NULL: not wanted.
  *  dnorm_out, dnorm_in  [d] float32, or NULL: not wanted.
  *  The [d] gradients are summed over the rows in float32, in an order that depends on
- *  T and d alone.  dx may be dh itself and dy may be y or dn itself; otherwise outputs
- *  may not overlap inputs or each other.  workspace:
+ *  T, d and dtype alone.  dx may be dh itself and dy may be y or dn itself, at the same
+ *  stride; otherwise outputs may not overlap inputs or each other.  workspace:
  *  moe_block_norm_backward_workspace_bytes(T, d) bytes, 256-byte aligned, needed for
  *  the [d] gradients only.  T == 0: they are set to zero.
  */

@@ -267,6 +267,33 @@ def test_no_rows():
         assert torch.equal(v, torch.zeros(48, device=DEV))
 
 
+def test_no_rows_of_infinite_weights():
+    """Sums over no rows are zero, whatever they would be multiplied with."""
+    say("block norm T = 0 with infinite weights")
+    norm, x, y, dh, dn = make(1, 48, torch.float32, "channel")
+    norm.norm_out[3], norm.gate[5] = float("inf"), float("nan")
+    e = x[:0]
+    g = moe.moe_block_norm_backward(norm, e, e, e, e)
+    torch.cuda.synchronize()
+    for v in (g.dnorm_in, g.dnorm_out, g.dgate):
+        assert torch.equal(v, torch.zeros(48, device=DEV))
+
+
+@pytest.mark.parametrize("d", [40, 2048])
+def test_large_rows_without_dn(d):
+    """Without dn the statistics of h are not used: squares past float32 change nothing."""
+    say(f"block norm gradient of large rows without dn, d={d}")
+    norm, x, y, dh, _ = make(3, d, torch.float32, "token", norm_out=False)
+    norm.gate[1] = 1.0
+    g = moe.moe_block_norm_backward(norm, x, y * 1e25, dh, None)
+    ref = (f64(dh) * f64(y * 1e25)).sum(axis=1, keepdims=True)
+    size = (np.abs(f64(dh)) * np.abs(f64(y * 1e25))).sum(axis=1, keepdims=True)
+    assert_near("dgate", g.dgate, ref, row_sum_ops(d) * U32 * size)
+    dx = f64(dh) * 0.75
+    assert_near("dx", g.dx, dx, U32 * np.abs(dx))
+    assert not g.dnorm_in.any()
+
+
 def test_some_gradients_only():
     """Gradients that are not wanted change nothing about the others."""
     say("block norm with some gradients")

@@ -123,6 +123,38 @@ def test_positions_past_the_last_row_and_rows_behind():
     assert torch.isfinite(out).all() and torch.isfinite(dw).all()
 
 
+@pytest.mark.parametrize("d", [40, 520, 2048])
+@pytest.mark.parametrize("k", [3, 9])
+def test_infinities_beside_dropped_pairs(d, k):
+    """Infinite and NaN weights and elements reach what the kept pairs make of them only."""
+    say(f"permute with infinities d={d} k={k}")
+    T = 5
+    pos = torch.arange(T * k, dtype=torch.int32).reshape(T, k)
+    pos[0, 1] = -1         # dropped, its weight NaN
+    pos[1, 0] = T * k      # dropped, its weight infinite
+    pos[3] = -1            # a token without pairs, its element infinite
+    x = torch.randint(1, 4, (T, d), generator=torch.Generator().manual_seed(d)).to(torch.float32)
+    r = torch.randint(1, 4, (T * k, d), generator=torch.Generator().manual_seed(k)).to(torch.float32)
+    w = torch.ones(T, k)
+    w[0, 1], w[1, 0], w[2, k - 1] = float("nan"), float("inf"), float("inf")
+    x[3, 5], x[1, 2], r[4 * k, 7] = float("inf"), float("nan"), float("inf")
+    p, wn, xn, rn = pos.numpy().ravel(), f64(w), f64(x), f64(r)
+    pos, w, x, r = pos.to(DEV), w.to(DEV), x.to(DEV), r.to(DEV)
+
+    def same(got, ref):  # small integers: sums are exact
+        np.testing.assert_array_equal(got.cpu().numpy(), ref.astype(np.float32))
+
+    same(moe.moe_unpermute(r, pos, k, T, w), orow.unpermute(rn, p, k, wn))
+    rows, drows, dx = torch.zeros_like(r), torch.zeros_like(r), torch.empty_like(x)
+    same(moe.moe_permute_into(x, pos, k, rows, w), orow.permute(xn, p, k, T * k, wn))
+    dw = torch.full((T, k), 7.0, device=DEV)
+    same(moe.moe_unpermute_backward_into(x, pos, k, drows, w, r, dw), orow.permute(xn, p, k, T * k, wn))
+    same(dw, orow.pair_products(xn, rn, p, k))
+    dw.fill_(7.0)
+    same(moe.moe_permute_backward_into(r, pos, k, dx, w, x, dw), orow.unpermute(rn, p, k, wn))
+    same(dw, orow.pair_products(xn, rn, p, k))
+
+
 def test_no_pair_left_and_no_token():
     say("permute with every pair dropped, and T = 0")
     T, d, k = 6, 40, 3

@@ -49,6 +49,7 @@ def test_permute_refusals(L, name):
     refused(SHAPE, k=17)
     refused(SHAPE, T=1 << 24)
     refused(SHAPE, d=(1 << 24) + 1)
+    refused(SHAPE, T=1 << 15, d=(1 << 19) + 1)  # more elements than a launch has lanes for
     refused(INVALID, pos=None)
     refused(INVALID, pos=P + 2)
     refused(INVALID, w=P + 1)
@@ -133,7 +134,7 @@ def test_block_norm_refusals(L):
     assert fn(None, P, 64, P, 64, None) == INVALID
     for change in BAD_NORM:
         assert fn(norm_args(**change), P, 64, P, 64, None) == INVALID, change
-    for change in (dict(d=16385), dict(T=(1 << 24) + 1)):
+    for change in (dict(d=16385), dict(T=(1 << 24) + 1), dict(T=1 << 21, d=8193)):
         assert fn(norm_args(**change), P, 1 << 20, P, 1 << 20, None) == SHAPE, change
     assert fn(norm_args(), None, 0, None, 0, None) == INVALID      # nothing wanted
     assert fn(norm_args(), P, 64, None, 0, None) == INVALID        # norm_in without n
@@ -168,6 +169,8 @@ def test_block_norm_backward_refusals(L):
     assert L.moe_block_norm_backward_workspace_bytes(-1, 64) == -1
     no_vectors = dict(dgate=None, dnorm_out=None, dnorm_in=None, workspace=None)
     assert fn(norm_args(T=0), grad_args(**no_vectors), None) == 0
+    # a gate of the channels is there without rows too
+    assert fn(norm_args(T=0, gate=None), grad_args(), None) == INVALID
 
 
 def test_binding_refuses_host_tensors():

@@ -9,7 +9,7 @@
 //   D  = dh + r_h (u - hn mean(u hn))        (the whole gradient of h)
 //   dx = a D,  dg = D z,  q = g D v_out,  dy = r_y (q - yn mean(q yn)),
 //   dv_in = sum over rows of dn hn,  dv_out = sum over rows of g D yn.
-// A row stays in the registers of one workgroup from its load to its store, so every
+// A row stays in the registers of its wavefronts from its load to its store, so every
 // tensor crosses memory once.
 #include <cfloat>
 #include <cmath>
@@ -378,7 +378,7 @@ __global__ __launch_bounds__(64 * norm_back_waves(R)) void k_block_norm_backward
     turn ^= 1;
     const float rh = a.dn ? rsqrtf(s[0] * a.inv_d + a.eps) : 0.f;
     const float mh = rh * (s[1] * a.inv_d);  // mean(u hn)
-    const float qD = s[2] + rh * (s[3] - mh * (rh * s[4]));
+    const float qD = a.dn ? s[2] + rh * (s[3] - mh * (rh * s[4])) : s[2];
     // mean(g v_out D yn).  (Factors 1 / rms go with the sum or the element that they
     // scale, one at a time: their cube leaves float32's range for rows of size 1e13.)
     const float my = a.v_out ? gt * (ry * (qD * a.inv_d)) : 0.f;
@@ -500,8 +500,9 @@ __global__ __launch_bounds__(1024) void k_norm_vectors(const float* part, int gr
     if (dv_in) dv_in[c] = v;
     return;
   }
-  if (dgate) dgate[c] = a.v_out ? v * load_one(static_cast<const S*>(a.v_out) + c) : v;
-  if (dv_out) dv_out[c] = a.gate_kind == MOE_GATE_CHANNEL ? v * load_one(static_cast<const S*>(a.gate) + c) : v;
+  // (without rows the sums are zero, whatever the vectors hold)
+  if (dgate) dgate[c] = a.v_out && groups ? v * load_one(static_cast<const S*>(a.v_out) + c) : v;
+  if (dv_out) dv_out[c] = a.gate_kind == MOE_GATE_CHANNEL && groups ? v * load_one(static_cast<const S*>(a.gate) + c) : v;
 }
 
 // Forward: `target` threads per workgroup, more where one row needs them.
@@ -558,6 +559,8 @@ static int check_norm(const char* fn, const moe_block_norm_args* a) {
   MOE_CHECK_ARG(a->T >= 0 && a->d > 0, MOE_ERR_INVALID_ARG, "%s: bad sizes T=%d d=%d", fn, a->T, a->d);
   MOE_CHECK_ARG(a->d <= kNormMaxD && a->T <= (1 << 24), MOE_ERR_UNSUPPORTED_SHAPE,
                 "%s: unsupported T=%d d=%d (T <= 2^24, d <= %d)", fn, a->T, a->d, kNormMaxD);
+  MOE_CHECK_ARG((int64_t)a->T * a->d <= kMaxRowElements, MOE_ERR_UNSUPPORTED_SHAPE, "%s: unsupported T*d=%lld (<= 2^34)",
+                fn, (long long)a->T * a->d);
   MOE_CHECK_ARG(a->gate_kind >= MOE_GATE_NONE && a->gate_kind <= MOE_GATE_FULL, MOE_ERR_INVALID_ARG,
                 "%s: bad gate_kind %d", fn, a->gate_kind);
   MOE_CHECK_ARG(a->eps >= FLT_MIN && std::isfinite(a->eps) && std::isfinite(a->residual_scale), MOE_ERR_INVALID_ARG,
@@ -670,6 +673,7 @@ extern "C" int moe_block_norm_backward(const moe_block_norm_args* a, const moe_b
                 MOE_ERR_INVALID_ARG, "%s: dy, dnorm_out and dgate need y, norm_out and gate", fn);
   float* dgate_vec = a->gate_kind == MOE_GATE_CHANNEL ? static_cast<float*>(g->dgate) : nullptr;
   const bool vectors = g->dnorm_out || g->dnorm_in || dgate_vec;
+  MOE_CHECK_ARG(!vectors || a->gate || a->gate_kind != MOE_GATE_CHANNEL, MOE_ERR_INVALID_ARG, "%s: gate is NULL", fn);
   const int64_t need = moe_block_norm_backward_workspace_bytes(a->T, a->d);
   MOE_CHECK_ARG(!vectors || a->T == 0 ||
                     (g->workspace && g->workspace_bytes >= need && ((uintptr_t)g->workspace % 256) == 0),

@@ -62,6 +62,7 @@ __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __re
   for (int j = 0; j < KM; ++j) {
     kept[j] = live && j < a.k && pos[j] >= 0 && pos[j] < a.num_rows ? ~0u : 0u;
     pos[j] = kept[j] ? pos[j] : 0;
+    w[j] = kept[j] ? w[j] : 0.f;  // (times a masked row: an infinite weight would make NaN of it)
   }
   for (int it = 0; it < p.rounds; ++it) {
     const Piece c = piece_of((part * 64 + lane + it * p.waves * 64) * kPiece, a.d);
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __re
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
       dot[j] = lane_sum(dot[j], 6);
-      if (lane == 0) part_sums[wave][j] = dot[j];
+      if (lane == 0) part_sums[wave][j] = kept[j] ? dot[j] : 0.f;
     }
     __syncthreads();
     if (!live || part != 0 || lane >= a.k) return;
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t*
   for (int j = 0; j < a.k; ++j) {
     const int64_t at = t * a.k + j, pos = pair_pos[at];
     const bool kept = pos >= 0 && pos < a.num_rows;
-    const float w = weights ? weights[at] : 1.f;
+    const float w = !kept ? 0.f : weights ? weights[at] : 1.f;
     float dot = 0.f;
     if (!kSpread || kProducts) {
       Raw<S> row = load_raw<true>(row_ptr<S, true>(a.sorted_in, kept ? pos : 0, a.sorted_in_stride), c, a.d);
@@ -168,7 +169,7 @@ __global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t*
     }
     if (kProducts) {
       dot = lane_sum(dot, p.lt);
-      if (lane == 0) a.dweights[at] = dot;
+      if (lane == 0) a.dweights[at] = kept ? dot : 0.f;
     }
   }
   if (!kSpread) store_piece<true>(row_ptr<S, true>(a.out, t, a.out_stride), c, a.d, acc);
@@ -244,6 +245,8 @@ static int check_rows(const char* fn, int dtype, int T, int d, int k, int64_t nu
                 "%s: bad sizes T=%d d=%d k=%d num_rows=%lld", fn, T, d, k, (long long)num_rows);
   MOE_CHECK_ARG(k <= MOE_MAX_TOPK && (int64_t)T * k <= (1 << 24) && d <= (1 << 24), MOE_ERR_UNSUPPORTED_SHAPE,
                 "%s: unsupported k=%d T*k=%lld d=%d (k <= 16, T*k <= 2^24, d <= 2^24)", fn, k, (long long)T * k, d);
+  MOE_CHECK_ARG((int64_t)T * d <= kMaxRowElements, MOE_ERR_UNSUPPORTED_SHAPE, "%s: unsupported T*d=%lld (<= 2^34)",
+                fn, (long long)T * d);
   if (T == 0) return MOE_OK;
   MOE_CHECK_ARG(pair_pos && ((uintptr_t)pair_pos % 4) == 0 && ((uintptr_t)weights % 4) == 0 &&
                     ((uintptr_t)dweights % 4) == 0,

@@ -138,7 +138,7 @@ __device__ __forceinline__ TilePairs deal_pairs(const RouteBackDev& a, const Pai
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (2 * i >= a.k) break;
-    reinterpret_cast<int*>(tile)[64 * i + lane] = r.id[i];
+    tile[64 * i + lane] = __int_as_float(r.id[i]);
     stage_w[64 * i + lane] = r.w[i];
     stage_g[64 * i + lane] = r.g[i];
   }
@@ -152,7 +152,7 @@ __device__ __forceinline__ TilePairs deal_pairs(const RouteBackDev& a, const Pai
     w[i] = p.g[i] = 0.f;
     if (2 * i >= a.k) continue;
     const int j = (lane & 1) + 2 * i, at = (lane >> 1) * a.k + (j < a.k ? j : 0);
-    const int id = reinterpret_cast<const int*>(tile)[at];
+    const int id = __float_as_int(tile[at]);
     const bool there = live && j < a.k && id >= 0 && id < a.E;
     p.id[i] = there ? id : -1;
     w[i] = there ? stage_w[at] : 0.f;

@@ -24,13 +24,15 @@ typedef uint32_t u32x4_a4_t __attribute__((ext_vector_type(4), aligned(4)));
 inline int64_t dtype_bytes(int dtype) { return dtype == MOE_FP32 ? 4 : 2; }
 
 constexpr int kPiece = 8;  // elements of a row that one lane holds at a time
+// T*d of a call: a lane per piece, rows filled up to whole wavefronts, stays below the 2^32
+// threads that a launch may have
+constexpr int64_t kMaxRowElements = (int64_t)1 << 34;
 
 // Eight consecutive elements as they lie in memory.
 template <typename S>
 struct Raw {
   u32x4_t w[sizeof(S) == 4 ? 2 : 1];
 };
-
 
 // Where a lane's eight elements of a row of d lie.  The last piece of a row whose length
 // is no multiple of 8 starts at d - 8, and so do those of lanes past the end: every load
