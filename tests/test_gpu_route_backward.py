@@ -67,6 +67,23 @@ def test_against_reference(T, d, E, k, renormalize):
         check(f"aux={aux is not None}", x, w, route, dweights, renormalize, aux, plus, dx, dw)
 
 
+@pytest.mark.parametrize("T,d,E,k", [(129, 200, 65, 2), (300, 136, 129, 3), (520, 264, 257, 6), (70, 128, 513, 9),
+                                     (2100, 1024, 128, 8), (300, 136, 63, 16)])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_ways_to_the_logits_gradient(T, d, E, k, renormalize):
+    """Sizes around those where another kernel computes it, each output alone too."""
+    say(f"route backward T={T} d={d} E={E} k={k} renormalize={renormalize}, parts")
+    x, w, route, dweights, _, add = make(T, d, E, k, renormalize)
+    dx, dw = moe.moe_route_backward(x, w, route, dweights, renormalize, None, add)
+    torch.cuda.synchronize()
+    check("both", x, w, route, dweights, renormalize, None, add, dx, dw)
+    ws = moe.alloc_route_backward_workspace(T, d, E, k, DEV)
+    only_x, only_w = torch.empty_like(dx), torch.empty_like(dw)
+    moe.moe_route_backward_into(x, w, route, dweights, only_x, None, ws, renormalize, None, add)
+    moe.moe_route_backward_into(x, w, route, dweights, None, only_w, ws, renormalize)
+    assert torch.equal(only_x, dx) and torch.equal(only_w, dw)
+
+
 def test_parts_and_accumulation_in_place():
     say("route backward: one output alone, dx added in place")
     T, d, E, k = 200, 264, 40, 5
