@@ -112,6 +112,10 @@ __device__ __forceinline__ void unpack_own(Raw<S> r, Piece p, float (&v)[kPiece]
   unpack<S>(r, v);
 }
 
+// Forward: a row by as many lanes as it has pieces, up to 512 of them; longer rows two
+// pieces per lane.  Bound by HBM: T = 16384, d = 2048 in bf16, x and y read, h and n
+// written, 268 MB in 48 us (5.6 TB/s); 16 rows take 3.6 us, a launch and the row's chain of
+// loads and two sums.
 template <typename S, int R, bool kSub>
 __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormSplit p) {
   __shared__ float lds[2][kNormMaxThreads / 64 * 8];
@@ -209,6 +213,12 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
 // Column sums: only A = sum over rows of D yn (g D yn for a token's or full gate) and
 // B = that of dn hn are kept; dnorm_out and a channel gate's gradient are A times the
 // channel gate and v_out.
+// Measured: T = 8192, d = 2048 in bf16 41 us for 201 MB (4.9 TB/s) and 5 for the sums
+// over the workgroups; 1001 rows of 1111 floats 10.6 and 4.6 us.  Many rows are bound by
+// HBM and the vector units together (some 1500 vector instructions per row); few rows by
+// the chain of one row's loads and sums, four rows after each other.  Two wavefronts per
+// SIMD that request x and y of the next row ran faster than one that requests all of it
+// (46.9 to 45.2 us for both launches) or two that request nothing (46.2).
 // What a call leaves out is read from a tensor that it has and masked to zero, so that no
 // load sits under a branch; only a full gate, a fifth stream, has a kernel of its own.
 //
@@ -478,7 +488,8 @@ __global__ __launch_bounds__(64 * norm_back_waves(R)) void k_block_norm_backward
 }
 
 // the [d] gradients: column sums over the workgroups, 32 columns of A (blockIdx.y = 0)
-// or B by 32 rows of threads
+// or B by 32 rows of threads, each with eight loads in flight; 5 us for 256 workgroups
+// of 2048 columns (4 MB), its launch and two dependent steps
 template <typename S>
 __global__ __launch_bounds__(1024) void k_norm_vectors(const float* part, int groups, NormDev a, float* dv_out,
                                                        float* dv_in, float* dgate) {

@@ -8,6 +8,11 @@
 // the scalar products that are the weights' gradients.  So one kernel either spreads a
 // token's row over its k sorted rows or gathers them, with or without the scalar
 // products.  It goes by token, whose row is read (written) once.
+//
+// Bound by HBM where there are many tokens.  T = 4096, d = 2048, k = 8 in bf16: 26.5 us for
+// 151 MB (5.7 TB/s; a plain copy of 1 GiB runs at 5.0), back 26.7 us, the gradient of the
+// way back with the products 54 us for 286 MB (5.3 TB/s).  16 tokens take 3.4 us and one
+// 2.1: a launch and two dependent loads, the positions and then the rows.
 #include "rows.hpp"
 
 namespace moe {
@@ -126,7 +131,8 @@ __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __re
   }
 }
 
-// Rows of at most 256 elements: 1 << lt lanes per token, several tokens per wavefront.
+// Rows of at most 256 elements: 1 << lt lanes per token, several tokens per wavefront (a
+// whole wavefront per token would leave half of its lanes idle or more).
 template <typename S, bool kSpread, bool kProducts>
 __global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t* __restrict__ pair_pos,
                                                     const float* __restrict__ weights, TokenSplit p) {

@@ -510,6 +510,7 @@ __global__ __launch_bounds__(64 * kRbWaves, kPairs ? 2 : 3) void k_route_product
     route_dx<kPairs>(a, blockIdx.x - dw_blocks, lds, tile);
 }
 
+// dW from its parts, in order: 4 us for 8 parts of 64 x 2048, a launch and their loads.
 __global__ __launch_bounds__(256) void k_route_dw_sum(const float* part, int splits, int64_t count, float* dw) {
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= count) return;
