@@ -215,10 +215,11 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
 // channel gate and v_out.
 // Measured: T = 8192, d = 2048 in bf16 41 us for 201 MB (4.9 TB/s) and 5 for the sums
 // over the workgroups; 1001 rows of 1111 floats 10.6 and 4.6 us.  Many rows are bound by
-// HBM and the vector units together (some 1500 vector instructions per row); few rows by
-// the chain of one row's loads and sums, four rows after each other.  Two wavefronts per
-// SIMD that request x and y of the next row ran faster than one that requests all of it
-// (46.9 to 45.2 us for both launches) or two that request nothing (46.2).
+// HBM (7.4 TB/s while the rows run) and the launch around them; few rows by the chain of
+// one row, some 6 us from the first load to the column sums, and the two launches.  Two
+// wavefronts per SIMD that request x and y of the next row ran faster than one that requests all of it
+// (46.9 to 45.2 us for both launches) or two that request nothing (46.2); dn and dh requested
+// early too, or column sums that all slots hand over at once, changed nothing.
 // What a call leaves out is read from a tensor that it has and masked to zero, so that no
 // load sits under a branch; only a full gate, a fifth stream, has a kernel of its own.
 //
