@@ -415,7 +415,8 @@ int moe_unpermute_backward(const void* dout, int64_t dout_stride, const void* ro
  *  dx (relative error 2^-18, under its bf16 rounding), three for dw_router (2^-27),
  *  with float32 sums.  Deterministic.  Infinite values may come out as NaN.  Outputs may
  *  not overlap inputs (but for dx_add) or each other.
- *  workspace moe_route_backward_workspace_bytes(T, d, E, k) bytes, 256-byte aligned.
+ *  workspace moe_route_backward_workspace_bytes(T, d, E, k) bytes, 256-byte aligned (-1
+ *            for sizes outside the limits).
  *  Entries of topk_ids outside [0, E) are ignored; the ids of a token are distinct.
  *  Limits and errors: those of moe_route; x, w_router, dx and dx_add 16-byte aligned;
  *  d <= 2^20, T <= 2^24.  T == 0: dw_router is set to zero.

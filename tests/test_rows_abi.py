@@ -95,6 +95,8 @@ def test_route_backward_refusals(L):
     for change in (dict(workspace=None), dict(workspace=P + 16), dict(workspace_bytes=need - 1)):
         assert fn(route_args(**change), None) == WORKSPACE, change
     assert L.moe_route_backward_workspace_bytes(-1, 64, 8, 2) == -1
+    for sizes in ((2 ** 31 - 1, 64, 8, 2), (4, 2 ** 31 - 8, 8, 2), (4, 64, 2 ** 31 - 1, 2)):
+        assert L.moe_route_backward_workspace_bytes(*sizes) == -1
     assert L.moe_route_backward_workspace_bytes(0, 64, 8, 2) >= 0
     assert fn(route_args(T=0, dw_router=None), None) == 0
 

@@ -551,7 +551,7 @@ static RouteBackPlan route_back_plan(int T, int d, int E) {
 using namespace moe;
 
 extern "C" int64_t moe_route_backward_workspace_bytes(int T, int d, int E, int k) {
-  if (T < 0 || d <= 0 || E <= 0 || k <= 0) return -1;
+  if (T < 0 || d <= 0 || E <= 0 || k <= 0 || E > MOE_MAX_EXPERTS || d > (1 << 20) || T > (1 << 24)) return -1;
   return route_back_plan(T, d, E).total;
 }
 
