@@ -136,6 +136,17 @@ def test_every_part(gate, norm_out, norm_in):
             check_backward(type_ + " dh alone", norm, x, y, dh, None)
 
 
+@pytest.mark.parametrize("type_", list(TYPES))
+@pytest.mark.parametrize("T,d", [(1, 1100), (2, 4096), (8, 2048), (9, 2048), (40, 64), (300, 1100), (300, 2304), (260, 5120),
+                                 (70, 6144), (40, 12288)])
+def test_ways_to_share_rows(T, d, type_):
+    """One workgroup for all rows and several, rows of one wavefront and of many."""
+    say(f"block norm gradient T={T} d={d} {type_}")
+    for gate in ("channel", "full"):
+        norm, x, y, dh, dn = make(T, d, TYPES[type_], gate)
+        check_backward(gate, norm, x, y, dh, dn)
+
+
 def test_many_long_rows_without_norm_out():
     """Rows of several wavefronts, several rows per workgroup, one round of sums each."""
     say("block norm T=1500 d=4104 without norm_out")

@@ -34,6 +34,7 @@ struct NormDev {
   void *dx, *dy, *dgate;
   int64_t dh_stride, dn_stride, dx_stride, dy_stride, dgate_stride;
   float* part;  // [workgroup][2][d]: column sums for v_out and gate, and for v_in; or null
+  float *dv_out, *dv_in, *dgate_vec;  // the [d] gradients, null where not wanted
 };
 
 template <typename S, bool kSub>
@@ -198,13 +199,26 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
   }
 }
 
+// a piece of `out` (null: not wanted) = v times that of `factor` (null: 1)
+template <bool kSub, typename S>
+__device__ __forceinline__ void store_times(float* out, const S* factor, const Piece& c, int d, const float (&v)[kPiece]) {
+  if (!out) return;
+  float f[kPiece];
+#pragma unroll
+  for (int i = 0; i < kPiece; ++i) f[i] = 1.f;
+  if (factor) unpack<S>(load_raw<kSub>(factor, c, d), f);
+#pragma unroll
+  for (int i = 0; i < kPiece; ++i) f[i] = factor ? v[i] * f[i] : v[i];
+  store_piece<kSub, false>(out, c, d, f);
+}
+
 // The gradient.  D = dh + r_h (u - mean(u hn) r_h h) is linear in dh, u and h, and with
 // q = g v_out y (g the channel or full gate) the sum over q D that dy and a token's gate
 // need is the same combination of the sums over q dh, q u and q h: so a row takes two
 // rounds of sums (y^2, then the other five) and not four, each of which would wait for
 // the one before.
 //
-// A row belongs to one wavefront up to 2048 elements (R pieces per lane), so that its
+// A row belongs to one wavefront where R pieces per lane hold it, so that its
 // sums need no barrier and the wavefronts of a CU drift apart: some load while others
 // compute.  Only the row as loaded and the column sums stay in registers; h, u and q are
 // computed again for the outputs, one piece after the other, v_out times the channel gate
@@ -225,10 +239,10 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_block_norm(NormDev a, NormS
 //
 // Wavefronts per workgroup, one workgroup per CU: what the registers of a row of `bytes`
 // per element and R pieces allow.
-constexpr int norm_back_waves(int R) { return R == 1 ? 16 : R == 2 ? 12 : 8; }
+constexpr int norm_back_waves(int R, int bytes) { return R == 1 ? 16 : R == 2 && bytes == 2 ? 12 : 8; }
 
 template <typename S, int R, bool kSub, bool kFull>
-__global__ __launch_bounds__(64 * norm_back_waves(R)) void k_block_norm_backward(NormDev a, NormSplit p) {
+__global__ __launch_bounds__(64 * norm_back_waves(R, sizeof(S))) void k_block_norm_backward(NormDev a, NormSplit p) {
   __shared__ float sums[2][16 * 8];
   // [wavefront of the row][W, V][R][half][lane]: four elements of a lane's piece each
   extern __shared__ f32x4_t vec[];
@@ -480,6 +494,16 @@ __global__ __launch_bounds__(64 * norm_back_waves(R)) void k_block_norm_backward
     n = half;
   }
   if (rl.slot != 0) return;
+  if (gridDim.x == 1) {  // every row was this workgroup's
+    const S* gate = a.gate_kind == MOE_GATE_CHANNEL ? static_cast<const S*>(a.gate) : nullptr;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (a.dv_in) store_piece<kSub, false>(a.dv_in, c[r], a.d, B[r]);
+      store_times<kSub>(a.dgate_vec, static_cast<const S*>(a.v_out), c[r], a.d, A[r]);
+      store_times<kSub>(a.dv_out, gate, c[r], a.d, A[r]);
+    }
+    return;
+  }
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.d;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -492,8 +516,7 @@ __global__ __launch_bounds__(64 * norm_back_waves(R)) void k_block_norm_backward
 // or B by 32 rows of threads, each with eight loads in flight; 5 us for 256 workgroups
 // of 2048 columns (4 MB), its launch and two dependent steps
 template <typename S>
-__global__ __launch_bounds__(1024) void k_norm_vectors(const float* part, int groups, NormDev a, float* dv_out,
-                                                       float* dv_in, float* dgate) {
+__global__ __launch_bounds__(1024) void k_norm_vectors(const float* part, int groups, NormDev a) {
   __shared__ float lds[32][33];
   const int x = threadIdx.x & 31, row = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + x;
@@ -509,12 +532,13 @@ __global__ __launch_bounds__(1024) void k_norm_vectors(const float* part, int gr
   float v = 0.f;
   for (int r = 0; r < 32; ++r) v += lds[r][x];
   if (blockIdx.y == 1) {
-    if (dv_in) dv_in[c] = v;
+    if (a.dv_in) a.dv_in[c] = v;
     return;
   }
   // (without rows the sums are zero, whatever the vectors hold)
-  if (dgate) dgate[c] = a.v_out && groups ? v * load_one(static_cast<const S*>(a.v_out) + c) : v;
-  if (dv_out) dv_out[c] = a.gate_kind == MOE_GATE_CHANNEL && groups ? v * load_one(static_cast<const S*>(a.gate) + c) : v;
+  if (a.dgate_vec) a.dgate_vec[c] = a.v_out && groups ? v * load_one(static_cast<const S*>(a.v_out) + c) : v;
+  if (a.dv_out)
+    a.dv_out[c] = a.gate_kind == MOE_GATE_CHANNEL && groups ? v * load_one(static_cast<const S*>(a.gate) + c) : v;
 }
 
 // Forward: `target` threads per workgroup, more where one row needs them.
@@ -531,25 +555,37 @@ static NormSplit norm_split(int d, int target) {
   return p;
 }
 
-// Gradient: a row of up to 2048 elements of two bytes or 1536 floats has one wavefront
-// with one to four pieces per lane, a longer one several; fewer rows per workgroup where
-// there are few, so that every CU has some.
+// Gradient: the pieces per lane (one to four) with which a workgroup has the most rows at
+// once; among equals a row of one wavefront, which needs no barrier, then the fewest pieces
+// per lane, that is the most wavefronts.  So rows of up to 2048 elements of two bytes or 1536
+// floats have one wavefront.  (bf16: d = 2560 three pieces 34.7 us, four 38.6; 5120 two
+// 46.8, four 52.7; 4096 four 49.4, two 51.1; 8192 four 50.4, two 54.3.)  Four pieces of floats
+// spill: only rows that nothing else takes have them.  Fewer rows per workgroup where there
+// are few, so that every CU has some.
 static NormSplit norm_back_split(int T, int d, int dtype) {
   NormSplit p;
   const int bytes = (int)dtype_bytes(dtype);
   const int pieces = (int)ceil_div(d, kPiece);
-  if (bytes == 4)
-    p.pieces = pieces <= 64 ? 1 : pieces <= 128 ? 2 : pieces <= 192 ? 3 : pieces <= 1024 ? 2 : 4;
-  else
-    p.pieces = pieces <= 64 ? 1 : pieces <= 128 ? 2 : pieces <= 192 ? 3 : 4;
+  int rows = 0;
+  for (int R = 1; R <= 4; ++R) {
+    const int waves = (int)ceil_div(pieces, 64 * R), slots = norm_back_waves(R, bytes) / waves;
+    if (R == 4 && bytes == 4 && rows > 0) continue;
+    if (slots > rows || (slots == rows && slots > 0 && waves == 1 && p.waves > 1)) {
+      rows = slots;
+      p.pieces = R;
+      p.waves = waves;
+    }
+  }
   const int lanes = (int)ceil_div(pieces, p.pieces);
   p.lt = 0;
   while (p.lt < 6 && (1 << p.lt) < lanes) ++p.lt;
-  p.waves = (int)ceil_div(lanes, 64);
-  const int most = norm_back_waves(p.pieces);
+  const int most = norm_back_waves(p.pieces, bytes);
   const int per_wave = 64 >> p.lt;
   int groups = p.waves > 1 ? most / p.waves : most;  // wavefronts (or groups of them) per workgroup
-  groups = (int)std::max<int64_t>(1, std::min<int64_t>(groups, ceil_div(T, 256 * per_wave)));
+  // as many rows as a workgroup takes at once are its own, without a launch for the column
+  // sums (calls of one row of 2048 bf16 12.1 to 9.0 us, of eight 11.9 to 11.0)
+  const bool one = T <= groups * per_wave;
+  groups = (int)std::max<int64_t>(1, std::min<int64_t>(groups, ceil_div(T, one ? per_wave : 256 * per_wave)));
   p.slots = groups * per_wave;
   p.threads = groups * p.waves * 64;
   return p;
@@ -704,6 +740,9 @@ extern "C" int moe_block_norm_backward(const moe_block_norm_args* a, const moe_b
   v.dgate = g->dgate;
   v.dgate_stride = g->dgate_stride;
   v.part = vectors ? static_cast<float*>(g->workspace) : nullptr;
+  v.dv_out = g->dnorm_out;
+  v.dv_in = g->dnorm_in;
+  v.dgate_vec = dgate_vec;
   hipStream_t s = (hipStream_t)stream;
   const NormSplit p = norm_back_split(a->T, a->d, a->dtype);
   const int groups = norm_groups(a->T, p);
@@ -737,9 +776,8 @@ extern "C" int moe_block_norm_backward(const moe_block_norm_args* a, const moe_b
       else
         go(integral_constant<int, 4>{}, std::false_type{});
     }
-    if (vectors)
-      hipLaunchKernelGGL(k_norm_vectors<S>, dim3((unsigned)ceil_div(a->d, 32), 2), dim3(1024), 0, s, v.part, groups, v,
-                         g->dnorm_out, g->dnorm_in, dgate_vec);
+    if (vectors && groups != 1)
+      hipLaunchKernelGGL(k_norm_vectors<S>, dim3((unsigned)ceil_div(a->d, 32), 2), dim3(1024), 0, s, v.part, groups, v);
   });
   timing_end(K_BLOCK_NORM_BWD, s);
   return check_launch(fn);
