@@ -47,6 +47,10 @@ template <typename S, bool kSpread, bool kProducts, int KM, int KB, bool kStream
 __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __restrict__ pair_pos,
                                                const float* __restrict__ weights, TokenSplit p) {
   __shared__ float part_sums[kProducts ? 16 : 1][KM];
+  // (Floats are two stores of 16 bytes per lane, each of half of every 32: spread alone they
+  // go through the L2, which puts them together; T = 4096, d = 2048, k = 8 121 to 63 us.  With
+  // products the loads pace them, 123 past it and 125 through it.)
+  constexpr bool kPast = sizeof(S) == 2 || kProducts;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int part = wave % p.waves, lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * p.tokens + wave / p.waves;
@@ -106,9 +110,9 @@ __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __re
           if (weights) {
 #pragma unroll
             for (int i = 0; i < kPiece; ++i) acc[i] = w[j] * v[i];
-            store_piece<false>(dst, c, a.d, acc);
+            store_piece<false, kPast>(dst, c, a.d, acc);
           } else {
-            store_raw<false>(dst, c, a.d, mine);
+            store_raw<false, kPast>(dst, c, a.d, mine);
           }
         }
       }
@@ -181,14 +185,19 @@ __global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t*
   if (!kSpread) store_piece<true>(row_ptr<S, true>(a.out, t, a.out_stride), c, a.d, acc);
 }
 
-static TokenSplit token_split(int d) {
+// At most 16 wavefronts share a token, four where they hold much of it: the sums of the
+// products, or more than eight sorted rows.  Larger workgroups leave registers of a CU over
+// (d = 4288, T = 1011, bf16, nine wavefronts against three with three pieces per lane:
+// gradient of the way back k = 8 34.3 and 30.3 us, of permute 21.1 and 17.0, unpermute k = 12
+// 24.6 and 22.6; the others lose by it, permute k = 8 19.3 and 20.9, unpermute 14.7 and 15.0).
+static TokenSplit token_split(int d, bool heavy) {
   TokenSplit p;
   const int pieces = (int)ceil_div(d, kPiece);
   p.lt = 0;
   while (p.lt < 6 && (1 << p.lt) < pieces) ++p.lt;
   const int64_t full = ceil_div(pieces, 64);
-  p.waves = (int)std::min<int64_t>(full, 16);
-  p.rounds = (int)ceil_div(full, p.waves);
+  p.rounds = (int)ceil_div(full, heavy ? 4 : 16);
+  p.waves = (int)ceil_div(full, p.rounds);
   p.tokens = p.lt < 6 ? 256 >> p.lt : std::max(1, 4 / p.waves);
   p.threads = p.lt < 6 ? 256 : p.tokens * p.waves * 64;
   return p;
@@ -196,7 +205,7 @@ static TokenSplit token_split(int d) {
 
 static int launch_rows(const char* name, int timing_id, bool spread, int dtype, PermuteDev a, const int32_t* pair_pos,
                        const float* weights, hipStream_t s) {
-  const TokenSplit p = token_split(a.d);
+  const TokenSplit p = token_split(a.d, a.dweights || (!spread && a.k > 8));
   const dim3 grid((unsigned)ceil_div(a.T, p.tokens));
   if (a.num_rows == 0) {  // every pair is dropped: what they read is masked, any row will do
     a.sorted_in = spread ? a.token_in : a.out;
@@ -218,7 +227,9 @@ static int launch_rows(const char* name, int timing_id, bool spread, int dtype, 
       else if (a.k <= 8)
         launch(k_rows<S, kSpread, kProducts, 8, 8, kStream>);
       else
-        launch(k_rows<S, kSpread, kProducts, 16, 8, kStream>);
+        // (all rows of a token at once where the registers hold them: unpermute, T = 4096,
+        // d = 2048, k = 12 in bf16 41.6 to 37.5 us)
+        launch(k_rows<S, kSpread, kProducts, 16, sizeof(S) == 2 && !kSpread && !kProducts ? 16 : 8, kStream>);
     };
     const std::true_type yes;
     const std::false_type no;
