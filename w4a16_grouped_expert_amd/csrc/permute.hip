@@ -40,17 +40,19 @@ struct TokenSplit {
 // rows' addresses stay in scalar registers, and the loads of KB rows go out before the
 // first use.  Pairs that were dropped read some row that is there (`sorted_in` always has
 // one) and are masked, so that no load sits under a branch.
-// kStream: the sorted rows, each read once, by non-temporal loads.  That is for rows on
-// 16-byte boundaries (unpermute at T = 4096, d = 2048, k = 8: 29.0 to 26.8 us): off them
-// two lanes share a cache line, which is then fetched twice (odd gradient 4.8 to 5.5 us).
+// kStream: the sorted rows start on 16-byte boundaries.  Then they are read, each once, by
+// non-temporal loads (unpermute at T = 4096, d = 2048, k = 8: 29.0 to 26.8 us); off them
+// two lanes share a cache line, which would be fetched twice (odd gradient 4.8 to 5.5 us).
 template <typename S, bool kSpread, bool kProducts, int KM, int KB, bool kStream>
 __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __restrict__ pair_pos,
                                                const float* __restrict__ weights, TokenSplit p) {
   __shared__ float part_sums[kProducts ? 16 : 1][KM];
-  // (Floats are two stores of 16 bytes per lane, each of half of every 32: spread alone they
-  // go through the L2, which puts them together; T = 4096, d = 2048, k = 8 121 to 63 us.  With
-  // products the loads pace them, 123 past it and 125 through it.)
-  constexpr bool kPast = sizeof(S) == 2 || kProducts;
+  // Spread alone, rows go past the L2 only where every store fills whole lines: floats are two
+  // stores of 16 bytes per lane, each of half of every 32, and rows off 16-byte boundaries
+  // end inside lines; the L2 puts those together (T = 4096, k = 8: d = 2048 in fp32 121 to
+  // 63 us, d = 1111 in bf16 23.2 to 15.9).  With products, whose loads the L2 has to hold,
+  // it does not pay (d = 1111 in bf16 29.8 to 37.5 us).
+  constexpr bool kPast = kProducts || (sizeof(S) == 2 && kStream);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int part = wave % p.waves, lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * p.tokens + wave / p.waves;
@@ -136,7 +138,9 @@ __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __re
 }
 
 // Rows of at most 256 elements: 1 << lt lanes per token, several tokens per wavefront (a
-// whole wavefront per token would leave half of its lanes idle or more).
+// whole wavefront per token would leave half of its lanes idle or more).  Spread alone they go
+// through the L2: most such rows end inside lines (T = 16384, k = 8 in bf16: d = 250 25.3 to
+// 14.9 us, 81 11.5 to 9.4, but 128 7.8 to 9.0; in fp32 250 71 to 41).
 template <typename S, bool kSpread, bool kProducts>
 __global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t* __restrict__ pair_pos,
                                                     const float* __restrict__ weights, TokenSplit p) {
@@ -172,9 +176,9 @@ __global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t*
       if (weights) {
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) r[i] = w * v[i];
-        store_piece<true>(dst, c, a.d, r);
+        store_piece<true, kProducts>(dst, c, a.d, r);
       } else {
-        store_raw<true>(dst, c, a.d, mine);
+        store_raw<true, kProducts>(dst, c, a.d, mine);
       }
     }
     if (kProducts) {
@@ -233,9 +237,12 @@ static int launch_rows(const char* name, int timing_id, bool spread, int dtype, 
     };
     const std::true_type yes;
     const std::false_type no;
-    const bool stream = ((uintptr_t)a.sorted_in | (uintptr_t)(a.sorted_in_stride * (int64_t)sizeof(S))) % 16 == 0;
-    if (spread && !a.dweights)
-      go(yes, no, no);
+    const bool products = a.dweights != nullptr;
+    const void* sorted = spread && !products ? a.out : a.sorted_in;
+    const int64_t sorted_stride = spread && !products ? a.out_stride : a.sorted_in_stride;
+    const bool stream = ((uintptr_t)sorted | (uintptr_t)(sorted_stride * (int64_t)sizeof(S))) % 16 == 0;
+    if (spread && !products)
+      stream ? go(yes, no, yes) : go(yes, no, no);
     else if (spread)
       stream ? go(yes, yes, yes) : go(yes, yes, no);
     else if (a.dweights)
