@@ -47,12 +47,10 @@ template <typename S, bool kSpread, bool kProducts, int KM, int KB, bool kStream
 __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __restrict__ pair_pos,
                                                const float* __restrict__ weights, TokenSplit p) {
   __shared__ float part_sums[kProducts ? 16 : 1][KM];
-  // Spread alone, rows go past the L2 only where every store fills whole lines: floats are two
-  // stores of 16 bytes per lane, each of half of every 32, and rows off 16-byte boundaries
-  // end inside lines; the L2 puts those together (T = 4096, k = 8: d = 2048 in fp32 121 to
-  // 63 us, d = 1111 in bf16 23.2 to 15.9).  With products, whose loads the L2 has to hold,
-  // it does not pay (d = 1111 in bf16 29.8 to 37.5 us).
-  constexpr bool kPast = kProducts || (sizeof(S) == 2 && kStream);
+  // Spread alone, rows of two bytes off 16-byte boundaries go through the L2, which puts the
+  // lines together that they end in (T = 4096, d = 1111, k = 8 23.2 to 15.9 us).  With
+  // products, whose loads the L2 has to hold, it does not pay (29.8 to 37.5 us).
+  constexpr bool kPast = kProducts || kStream || sizeof(S) == 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int part = wave % p.waves, lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * p.tokens + wave / p.waves;

@@ -133,6 +133,23 @@ __device__ __forceinline__ void store_raw(S* row, const Piece& p, int d, const R
       __builtin_nontemporal_store(r.w[0], (MOE_GLOBAL u32x4_a2_t*)q);
     } else if constexpr (sizeof(S) == 2) {
       *(MOE_GLOBAL u32x4_a2_t*)q = r.w[0];
+    } else if constexpr (kStream && !kTiny) {
+      // (the whole wavefront has one row.)  32 lanes' pieces per instruction, both halves of
+      // each, so that it fills whole lines: the lower lanes' second halves change places with
+      // the upper lanes' first ones.  Without, T = 4096, d = 2048, k = 8: permute 121 in place
+      // of 53 us, its gradient's rows 122 in place of 111
+      const uint32_t at = piece_offset<S>(p);
+      const u32x2_t o = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(at, at + 16, false, false));
+      u32x4_t lo, hi;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a = r.w[0][i], b = r.w[1][i];
+        const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(a, b, false, false));
+        lo[i] = v[0];
+        hi[i] = v[1];
+      }
+      __builtin_nontemporal_store(lo, (MOE_GLOBAL u32x4_a4_t*)((MOE_GLOBAL char*)row + o[0]));
+      __builtin_nontemporal_store(hi, (MOE_GLOBAL u32x4_a4_t*)((MOE_GLOBAL char*)row + o[1]));
     } else if constexpr (kStream) {
       __builtin_nontemporal_store(r.w[0], (MOE_GLOBAL u32x4_a4_t*)q);
       __builtin_nontemporal_store(r.w[1], (MOE_GLOBAL u32x4_a4_t*)(q + 16));
