@@ -441,7 +441,7 @@ def _launch(fn, device, stream, *args):
         raise ValueError(f"stream on {stream.device} for tensors on GPU {device}")
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:  # (a tensor is on it: the GPU is initialised)
         return fn(*args, handle)
     with torch.cuda.device(device):
         return fn(*args, handle)
@@ -494,6 +494,16 @@ def _row_type(t, name):
     return dtype, device, *shape
 
 
+def _first_rows(t, name):
+    """_row_type and _rows of a call's first input: type, GPU index, sizes, address and row
+    stride."""
+    dtype, device, T, d = _row_type(t, name)
+    stride, inner = t.stride()
+    if inner != 1 and d > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return dtype, device, T, d, t.data_ptr(), stride if T > 1 else d
+
+
 def _pairs(pair_pos, weights, dweights, T, k, device):
     """Addresses of pair_pos (at least T*k positions), weights and dweights ([T, k])."""
     if pair_pos.dtype is not torch.int32:
@@ -513,9 +523,8 @@ def moe_permute_into(x, pair_pos, k, rows, weights: Optional[torch.Tensor] = Non
     x [T, d] and rows [num_rows, d] bf16, fp16 or fp32 with any row stride; pair_pos from
     moe_align (AlignOut.pair_pos).  Pairs whose position is negative or past the last row
     are dropped; rows that no pair names keep their contents."""
-    dtype, dev, T, d = _row_type(x, "x")
+    dtype, dev, T, d, xp, xs = _first_rows(x, "x")
     R = rows.shape[0]
-    xp, xs = _rows(x, "x", dtype, T, d, dev)
     rp, rs = _rows(rows, "rows", dtype, R, d, dev, True)
     pp, wp, _ = _pairs(pair_pos, weights, None, T, k, dev)
     check("moe_permute", _launch(
@@ -526,9 +535,8 @@ def moe_permute_into(x, pair_pos, k, rows, weights: Optional[torch.Tensor] = Non
 def moe_unpermute_into(rows, pair_pos, k, out, weights: Optional[torch.Tensor] = None, stream=None):
     """out[t] = sum over j of rows[pair_pos[t*k + j]], times weights[t, j] if given
     (float32 sums in slot order, one rounding; dropped pairs add nothing)."""
-    dtype, dev, R, d = _row_type(rows, "rows")
+    dtype, dev, R, d, rp, rs = _first_rows(rows, "rows")
     T = out.shape[0]
-    rp, rs = _rows(rows, "rows", dtype, R, d, dev)
     op, os = _rows(out, "out", dtype, T, d, dev, True)
     pp, wp, _ = _pairs(pair_pos, weights, None, T, k, dev)
     check("moe_unpermute", _launch(
@@ -540,11 +548,10 @@ def moe_permute_backward_into(drows, pair_pos, k, dx, weights: Optional[torch.Te
                               x: Optional[torch.Tensor] = None, dweights: Optional[torch.Tensor] = None, stream=None):
     """Gradient of moe_permute: dx[t] = sum over j of w drows[pos]; with x and dweights
     also dweights[t, j] = <x[t], drows[pos]> (0 for dropped pairs)."""
-    dtype, dev, R, d = _row_type(drows, "drows")
+    dtype, dev, R, d, rp, rs = _first_rows(drows, "drows")
     if (x is None) != (dweights is None):
         raise ValueError("x and dweights go together")
     T = dx.shape[0]
-    rp, rs = _rows(drows, "drows", dtype, R, d, dev)
     op, os = _rows(dx, "dx", dtype, T, d, dev, True)
     xp, xs = (None, 0) if x is None else _rows(x, "x", dtype, T, d, dev)
     pp, wp, dwp = _pairs(pair_pos, weights, dweights, T, k, dev)
@@ -559,11 +566,10 @@ def moe_unpermute_backward_into(dout, pair_pos, k, drows, weights: Optional[torc
     """Gradient of moe_unpermute: drows[pos] = w dout[t]; with rows and dweights also
     dweights[t, j] = <dout[t], rows[pos]> (0 for dropped pairs).  Rows of drows that no
     pair names keep their contents."""
-    dtype, dev, T, d = _row_type(dout, "dout")
+    dtype, dev, T, d, op, os = _first_rows(dout, "dout")
     if (rows is None) != (dweights is None):
         raise ValueError("rows and dweights go together")
     R = drows.shape[0]
-    op, os = _rows(dout, "dout", dtype, T, d, dev)
     dp, ds = _rows(drows, "drows", dtype, R, d, dev, True)
     rp, rs = (None, 0) if rows is None else _rows(rows, "rows", dtype, R, d, dev)
     pp, wp, dwp = _pairs(pair_pos, weights, dweights, T, k, dev)
@@ -673,10 +679,9 @@ class BlockNormGrads:
 
 
 def _block_norm_args(norm: BlockNorm, x, y):
-    dtype, dev, T, d = _row_type(x, "x")
     a = _lib.BlockNormArgs()
+    dtype, dev, T, d, a.x, a.x_stride = _first_rows(x, "x")
     a.dtype, a.T, a.d = DTYPES[dtype], T, d
-    a.x, a.x_stride = _rows(x, "x", dtype, T, d, dev)
     if y is not None:
         a.y, a.y_stride = _rows(y, "y", dtype, T, d, dev)
     if norm.norm_out is not None:
