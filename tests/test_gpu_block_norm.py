@@ -266,6 +266,25 @@ def test_long_rows_captured():
             assert torch.equal(getattr(grads, q), getattr(ref, q)), (i, q)
 
 
+def test_two_streams_at_once():
+    say("block norm gradient on two streams, each with its workspace")
+    jobs = []
+    for T, d, gate in ((700, 1100, "channel"), (6, 2048, "token")):
+        norm, x, y, dh, dn = make(T, d, torch.bfloat16, gate)
+        ref = moe.moe_block_norm_backward(norm, x, y, dh, dn)
+        out = moe.BlockNormGrads(*(torch.zeros_like(getattr(ref, q))
+                                   for q in ("dx", "dy", "dgate", "dnorm_out", "dnorm_in")))
+        jobs.append((norm, x, y, dh, dn, ref, out, moe.alloc_block_norm_workspace(T, d, DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for norm, x, y, dh, dn, _ref, out, ws, stream in jobs:
+            moe.moe_block_norm_backward_into(norm, x, y, out, ws, dh, dn, stream)
+    torch.cuda.synchronize()
+    for *_, ref, out, _ws, _stream in jobs:
+        for q in ("dx", "dy", "dgate", "dnorm_out", "dnorm_in"):
+            assert torch.equal(getattr(out, q), getattr(ref, q)), q
+
+
 def test_no_rows():
     say("block norm T = 0")
     norm, x, y, dh, dn = make(1, 48, torch.bfloat16, "channel")

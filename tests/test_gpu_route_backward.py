@@ -168,6 +168,50 @@ def test_graph_side_stream_and_determinism():
     assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
 
 
+def test_two_graphs_share_a_workspace_and_two_streams():
+    say("route backward: two graphs on one workspace, two streams on two")
+    calls = []
+    for T, d, E, k, renormalize in ((300, 520, 64, 8, True), (200, 264, 130, 4, False)):
+        x, w, route, dweights, _, add = make(T, d, E, k, renormalize)
+        dx, dw = torch.empty_like(x), torch.empty(E, d, device=DEV)
+        calls.append((x, w, route, dweights, renormalize, add, dx, dw))
+    size = max(moe.route_backward_workspace_bytes(c[0].shape[0], c[0].shape[1], c[1].shape[0], c[2].ids.shape[1])
+               for c in calls)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+
+    def step(c, ws, stream=None):
+        x, w, route, dweights, renormalize, add, dx, dw = c
+        moe.moe_route_backward_into(x, w, route, dweights, dx, dw, ws, renormalize, None, add, stream)
+
+    refs, graphs = [], []
+    for c in calls:
+        step(c, ws)
+        torch.cuda.synchronize()
+        refs.append((c[6].clone(), c[7].clone()))
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(c, ws)
+        graphs.append(g)
+    for _ in range(3):
+        for g, c, ref in zip(graphs, calls, refs):
+            c[6].zero_(), c[7].zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(c[6], ref[0]) and torch.equal(c[7], ref[1])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [ws, torch.empty_like(ws)]
+    for c in calls:
+        c[6].zero_(), c[7].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, space, st in zip(calls, spaces, streams):
+            step(c, space, st)
+    torch.cuda.synchronize()
+    for c, ref in zip(calls, refs):
+        assert torch.equal(c[6], ref[0]) and torch.equal(c[7], ref[1])
+
+
 def test_binding_refusals():
     say("route backward refusals")
     x, w, route, dweights, dlogits, add = make(4, 64, 8, 2, True)
