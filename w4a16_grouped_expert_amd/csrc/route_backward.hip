@@ -179,9 +179,10 @@ __global__ __launch_bounds__(512) void k_route_g(RouteBackDev a) {
   }
 }
 
-// G from the pairs.  What a wavefront needs to build tiles of 32 tokens: two lanes per token, each with
-// every other of its pairs.  The tokens' pairs lie one after the other: they are loaded
-// in that order (whole cache lines) and dealt out through the wavefront's tile.
+// G from the pairs.  What a wavefront needs to build tiles of 32 tokens: two lanes per
+// token, each with every other of its pairs.  The tokens' pairs lie one after the other:
+// they are loaded in that order (whole cache lines) and dealt out through the wavefront's
+// tile.
 // (LDS operations of one wavefront take effect in order.)
 struct TilePairs {
   int id[8];
@@ -500,7 +501,7 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, f32x4
 // Both products in one launch: the first dw_blocks workgroups sum dW, the others dx.
 template <int EB, bool kPairs>
 __global__ __launch_bounds__(64 * kRbWaves, kPairs ? 2 : 3) void k_route_products(RouteBackDev a, int dw_blocks) {
-  // dW: the wavefronts' sums; dx: 128 rows of W, 64 of them beside tiles
+  // dW: the wavefronts' sums; dx: 128 rows of W
   __shared__ u32x4_t lds[kRbWaves * 8 * 64];
   __shared__ alignas(16) float tiles[kPairs ? kRbWaves : 1][kPairs ? kTileFloats : 1];
   float* tile = tiles[kPairs ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) : 0];
