@@ -192,13 +192,15 @@ __global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t*
 // (d = 4288, T = 1011, bf16, nine wavefronts against three with three pieces per lane:
 // gradient of the way back k = 8 34.3 and 30.3 us, of permute 21.1 and 17.0, unpermute k = 12
 // 24.6 and 22.6; the others lose by it, permute k = 8 19.3 and 20.9, unpermute 14.7 and 15.0).
-static TokenSplit token_split(int d, bool heavy) {
+// Tokens of which every CU has one at most keep all: their time is that of one token's rounds
+// (permute gradient, d = 4864, k = 12 in fp32: T = 128 17.4 and 26.3 us, T = 768 57.7 and 50.6).
+static TokenSplit token_split(int T, int d, bool heavy) {
   TokenSplit p;
   const int pieces = (int)ceil_div(d, kPiece);
   p.lt = 0;
   while (p.lt < 6 && (1 << p.lt) < pieces) ++p.lt;
   const int64_t full = ceil_div(pieces, 64);
-  p.rounds = (int)ceil_div(full, heavy ? 4 : 16);
+  p.rounds = (int)ceil_div(full, heavy && T > 256 ? 4 : 16);
   p.waves = (int)ceil_div(full, p.rounds);
   p.tokens = p.lt < 6 ? 256 >> p.lt : std::max(1, 4 / p.waves);
   p.threads = p.lt < 6 ? 256 : p.tokens * p.waves * 64;
@@ -207,7 +209,7 @@ static TokenSplit token_split(int d, bool heavy) {
 
 static int launch_rows(const char* name, int timing_id, bool spread, int dtype, PermuteDev a, const int32_t* pair_pos,
                        const float* weights, hipStream_t s) {
-  const TokenSplit p = token_split(a.d, a.dweights || (!spread && a.k > 8));
+  const TokenSplit p = token_split(a.T, a.d, a.dweights || (!spread && a.k > 8));
   const dim3 grid((unsigned)ceil_div(a.T, p.tokens));
   if (a.num_rows == 0) {  // every pair is dropped: what they read is masked, any row will do
     a.sorted_in = spread ? a.token_in : a.out;
