@@ -560,8 +560,7 @@ static NormSplit norm_split(int d, int target) {
 // per lane, that is the most wavefronts.  So rows of up to 2048 elements of two bytes or 1536
 // floats have one wavefront.  (bf16: d = 2560 three pieces 34.7 us, four 38.6; 5120 two
 // 46.8, four 52.7; 4096 four 49.4, two 51.1; 8192 four 50.4, two 54.3.)  Four pieces of floats
-// spill: only rows that nothing else takes have them.  Fewer rows per workgroup where there
-// are few, so that every CU has some.
+// spill: only rows that nothing else takes have them.
 static NormSplit norm_back_split(int T, int d, int dtype) {
   NormSplit p;
   const int bytes = (int)dtype_bytes(dtype);
@@ -585,7 +584,10 @@ static NormSplit norm_back_split(int T, int d, int dtype) {
   // as many rows as a workgroup takes at once are its own, without a launch for the column
   // sums (calls of one row of 2048 bf16 12.1 to 9.0 us, of eight 11.9 to 11.0)
   const bool one = T <= groups * per_wave;
-  groups = (int)std::max<int64_t>(1, std::min<int64_t>(groups, ceil_div(T, one ? per_wave : 256 * per_wave)));
+  // otherwise as many as its share of rows takes in as few rounds (fp16, T = 3894, d = 704: two
+  // rounds of 8 rows 17.1 us, of 12 and 4 20.2)
+  const int64_t share = ceil_div(T, one ? 1 : 256), rounds = std::max<int64_t>(1, ceil_div(share, groups * per_wave));
+  groups = (int)std::max<int64_t>(1, ceil_div(share, per_wave * rounds));
   p.slots = groups * per_wave;
   p.threads = groups * p.waves * 64;
   return p;
