@@ -35,6 +35,18 @@ struct TokenSplit {
   int lt, waves, tokens, threads, rounds;
 };
 
+// Elements that belong to the piece before are in its sum: here both factors of their
+// products become zero (an infinite one times zero would be NaN).  The masks are vector
+// registers.  As conditions of the sums they would take scalar ones, which the sorted rows'
+// addresses fill (permute gradient, d = 4864, k = 12, T = 768 in fp32: 54.9 in place of 50.4 us;
+// T = 16384, d = 200, k = 8 in fp16: 18.7 in place of 15.2).
+__device__ __forceinline__ uint32_t own_mask(const Piece& p, int i) {
+  uint32_t m = i < p.skip ? 0u : ~0u;
+  asm("" : "+v"(m));
+  return m;
+}
+__device__ __forceinline__ float masked(float v, uint32_t mask) { return __uint_as_float(__float_as_uint(v) & mask); }
+
 // Rows of more than 256 elements.  A wavefront handles 64 pieces of 8 elements of one
 // token with at most KM pairs: its positions and weights come through scalar loads, the
 // rows' addresses stay in scalar registers, and the loads of KB rows go out before the
@@ -79,11 +91,12 @@ __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __re
     if (kSpread || kProducts)
       mine = load_raw<false>(row_ptr<S, false>(a.token_in, tc, a.token_in_stride), c, a.d);
     float v[kPiece], own[kPiece], r[kPiece], acc[kPiece];
+    uint32_t mask[kPiece];
     if (kSpread || kProducts) unpack<S>(mine, v);
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) {
       acc[i] = 0.f;
-      if (kProducts) own[i] = i < c.skip ? 0.f : v[i];  // (elements of the piece before: in its sum)
+      if (kProducts) own[i] = masked(v[i], mask[i] = own_mask(c, i));
     }
 #pragma unroll
     for (int j0 = 0; j0 < KM; j0 += KB) {
@@ -102,7 +115,7 @@ __global__ __launch_bounds__(1024) void k_rows(PermuteDev a, const int32_t* __re
 #pragma unroll
           for (int i = 0; i < kPiece; ++i) {
             if (!kSpread) acc[i] = fmaf(w[j], r[i], acc[i]);
-            if (kProducts) dot[j] = fmaf(own[i], r[i], dot[j]);
+            if (kProducts) dot[j] = fmaf(own[i], masked(r[i], mask[i]), dot[j]);
           }
         }
         if (kSpread && kept[j]) {
@@ -149,11 +162,12 @@ __global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t*
   Raw<S> mine{};
   if (kSpread || kProducts) mine = load_raw<true>(row_ptr<S, true>(a.token_in, t, a.token_in_stride), c, a.d);
   float v[kPiece], own[kPiece], r[kPiece], acc[kPiece];
+  uint32_t mask[kPiece];
   unpack<S>(mine, v);
 #pragma unroll
   for (int i = 0; i < kPiece; ++i) {
     acc[i] = 0.f;
-    own[i] = i < c.skip ? 0.f : v[i];
+    own[i] = masked(v[i], mask[i] = own_mask(c, i));
   }
   for (int j = 0; j < a.k; ++j) {
     const int64_t at = t * a.k + j, pos = pair_pos[at];
@@ -166,7 +180,7 @@ __global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t*
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) {
         if (!kSpread) acc[i] = fmaf(w, r[i], acc[i]);
-        if (kProducts) dot = fmaf(own[i], r[i], dot);
+        if (kProducts) dot = fmaf(own[i], masked(r[i], mask[i]), dot);
       }
     }
     if (kSpread && kept) {
