@@ -530,6 +530,11 @@ struct RouteBackPlan {
   int Ep, EB, splits;
 };
 
+// what the call takes, of sizes that are positive (T: not negative)
+static bool route_back_takes(int T, int d, int E, int k) {
+  return E <= MOE_MAX_EXPERTS && k <= MOE_MAX_TOPK && k <= E && d % 8 == 0 && d <= (1 << 20) && T <= (1 << 24);
+}
+
 static RouteBackPlan route_back_plan(int T, int d, int E) {
   RouteBackPlan p;
   p.Tp = ceil_div(T, kRbStep) * kRbStep;
@@ -552,7 +557,7 @@ static RouteBackPlan route_back_plan(int T, int d, int E) {
 using namespace moe;
 
 extern "C" int64_t moe_route_backward_workspace_bytes(int T, int d, int E, int k) {
-  if (T < 0 || d <= 0 || E <= 0 || k <= 0 || E > MOE_MAX_EXPERTS || d > (1 << 20) || T > (1 << 24)) return -1;
+  if (T < 0 || d <= 0 || E <= 0 || k <= 0 || !route_back_takes(T, d, E, k)) return -1;
   return route_back_plan(T, d, E).total;
 }
 
@@ -561,9 +566,7 @@ extern "C" int moe_route_backward(const moe_route_backward_args* a, void* stream
   MOE_CHECK_ARG(a != nullptr, MOE_ERR_INVALID_ARG, "moe_route_backward: args is NULL");
   MOE_CHECK_ARG(a->T >= 0 && a->d > 0 && a->E > 0 && a->k > 0, MOE_ERR_INVALID_ARG,
                 "moe_route_backward: bad sizes T=%d d=%d E=%d k=%d", a->T, a->d, a->E, a->k);
-  MOE_CHECK_ARG(a->E <= MOE_MAX_EXPERTS && a->k <= MOE_MAX_TOPK && a->k <= a->E && a->d % 8 == 0 &&
-                    a->d <= (1 << 20) && a->T <= (1 << 24),
-                MOE_ERR_UNSUPPORTED_SHAPE,
+  MOE_CHECK_ARG(route_back_takes(a->T, a->d, a->E, a->k), MOE_ERR_UNSUPPORTED_SHAPE,
                 "moe_route_backward: unsupported E=%d k=%d d=%d T=%d (E <= 1024, k <= min(E,16), d %% 8 == 0, "
                 "d <= 2^20, T <= 2^24)",
                 a->E, a->k, a->d, a->T);
