@@ -96,7 +96,7 @@ __device__ __forceinline__ float lane_max(float v) {
 template <int kEL>
 __global__ __launch_bounds__(512) void k_route_g(RouteBackDev a) {
   constexpr int kLd = 64 * kEL + 4;  // (rows stay 16-byte aligned)
-  __shared__ float tile[8][kLd];
+  __shared__ alignas(16) float tile[8][kLd];
   const int lane = lane_id();
   const int64_t t0 = (int64_t)blockIdx.x * 8, t = t0 + (threadIdx.x >> 6);
   float v[kEL];
