@@ -402,7 +402,8 @@ __global__ __launch_bounds__(64 * norm_back_waves(R, sizeof(S))) void k_block_no
     row_sums<kSub>(s, p, sums[turn]);  // (its barrier also ends the row's loads before a store in their place)
     turn ^= 1;
     const float rh = a.dn ? rsqrtf(s[0] * a.inv_d + a.eps) : 0.f;
-    const float mh = rh * (s[1] * a.inv_d);  // mean(u hn)
+    // (without dn neither h nor its sums are used: y, and so h, may be infinite)
+    const float mh = a.dn ? rh * (s[1] * a.inv_d) : 0.f;  // mean(u hn)
     const float qD = a.dn ? s[2] + rh * (s[3] - mh * (rh * s[4])) : s[2];
     // mean(g v_out D yn).  (Factors 1 / rms go with the sum or the element that they
     // scale, one at a time: their cube leaves float32's range for rows of size 1e13.)
@@ -417,16 +418,19 @@ __global__ __launch_bounds__(64 * norm_back_waves(R, sizeof(S))) void k_block_no
       forget(dh[r]);
       if (kFull) forget(g[r]);
       float h[kPiece], u[kPiece], D[kPiece], f[kPiece], e[kPiece];
-      piece(r, rh * a.scale, rh * (gt * ry), false, h, u, f);  // hn in place of h
-      unpack<S>(dn[r], f);
       unpack<S>(dh[r], D);
+      if (a.dn) {
+        piece(r, rh * a.scale, rh * (gt * ry), false, h, u, f);  // hn in place of h
+        unpack<S>(dn[r], f);
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) {
-        B[r][i] = fmaf(f[i], h[i], B[r][i]);
-        D[i] = fmaf(-rh * mh, h[i], fmaf(rh, u[i], D[i]));
-        f[i] = a.scale * D[i];
-        forget(B[r][i]);  // (put off, the addition would keep its operands to the end of the row)
+        for (int i = 0; i < kPiece; ++i) {
+          B[r][i] = fmaf(f[i], h[i], B[r][i]);
+          D[i] = fmaf(-rh * mh, h[i], fmaf(rh, u[i], D[i]));
+          forget(B[r][i]);  // (put off, the addition would keep its operands to the end of the row)
+        }
       }
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) f[i] = a.scale * D[i];
       if (a.dx) store_piece<kSub>(row_ptr<S, kSub>(a.dx, tc, a.dx_stride), c[r], a.d, f);
       if (a.y) {
         unpack<S>(y[r], e);
@@ -451,7 +455,8 @@ __global__ __launch_bounds__(64 * norm_back_waves(R, sizeof(S))) void k_block_no
 #pragma unroll
         for (int i = 0; i < kPiece; ++i) {
           A[r][i] = fmaf(D[i], e[i], A[r][i]);
-          f[i] = fmaf(-ry * my, e[i], ry * (u[i] * D[i]));
+          f[i] = ry * (u[i] * D[i]);
+          if (a.v_out) f[i] = fmaf(-ry * my, e[i], f[i]);  // (without norm_out y may be infinite)
           forget(A[r][i]);
         }
         if (a.dy) store_piece<kSub>(row_ptr<S, kSub>(a.dy, tc, a.dy_stride), c[r], a.d, f);
