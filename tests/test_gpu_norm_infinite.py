@@ -54,6 +54,70 @@ def same_bits(name, a, b, but=None):
 
 
 @pytest.mark.parametrize("type_", list(TYPES))
+@pytest.mark.parametrize("gate", ["channel", "token", "full"])
+@pytest.mark.parametrize("d", WIDTHS)
+def test_infinite_gradient_in_the_last_column(d, gate, type_):
+    say(f"block norm gradient, infinite dh in the last columns, d={d} {gate} {type_}")
+    T = 5
+    for norm_out in (True, False):
+        norm, x, y, dh, _ = make(T, d, TYPES[type_], gate, norm_out, False)
+        plain = moe.moe_block_norm_backward(norm, x, y, dh)
+        bad = dh.clone()
+        bad[1, d - 1], bad[3, d - 8] = INF, -INF
+        got = moe.moe_block_norm_backward(norm, x, y, bad)
+        ref = reference(norm, x, y, bad, None)
+        for q, r in ref.items():
+            same_kind(f"{q} norm_out={norm_out}", getattr(got, q), r)
+        rows = torch.zeros(T, d, dtype=torch.bool, device=DEV)
+        at = rows.clone()
+        rows[1], rows[3] = True, True
+        at[1, d - 1], at[3, d - 8] = True, True
+        same_bits("dx", got.dx, plain.dx, at)
+        same_bits("dy", got.dy, plain.dy, rows if norm_out else at)
+
+
+@pytest.mark.parametrize("type_", list(TYPES))
+@pytest.mark.parametrize("d", WIDTHS)
+def test_infinite_gradient_of_the_next_norm(d, type_):
+    say(f"block norm gradient, infinite dn in the last columns, d={d} {type_}")
+    T = 4
+    norm, x, y, dh, dn = make(T, d, TYPES[type_], "channel", True, True)
+    plain = moe.moe_block_norm_backward(norm, x, y, dh, dn)
+    bad = dn.clone()
+    bad[0, d - 1], bad[2, d - 8] = INF, -INF
+    got = moe.moe_block_norm_backward(norm, x, y, dh, bad)
+    ref = reference(norm, x, y, dh, bad)
+    same_kind("dx", got.dx, ref["dx"])
+    same_kind("dnorm_in", got.dnorm_in, ref["dnorm_in"])
+    rows = torch.zeros(T, d, dtype=torch.bool, device=DEV)
+    rows[0], rows[2] = True, True
+    same_bits("dx", got.dx, plain.dx, rows)
+    same_bits("dy", got.dy, plain.dy, rows)
+
+
+@pytest.mark.parametrize("type_", list(TYPES))
+@pytest.mark.parametrize("d", WIDTHS)
+def test_infinite_weights_in_the_last_column(d, type_):
+    """An infinite weight of the norm behind the block, of the next norm, or of the gate."""
+    say(f"block norm gradient, infinite weights in the last columns, d={d} {type_}")
+    for which in ("norm_out", "norm_in", "gate"):
+        norm, x, y, dh, dn = make(3, d, TYPES[type_], "channel", True, True)
+        getattr(norm, which)[d - 1] = INF
+        if which == "norm_in":
+            got, ref = moe.moe_block_norm_backward(norm, x, y, dh, dn), reference(norm, x, y, dh, dn)
+            same_kind("norm_in dx", got.dx, ref["dx"])
+            same_kind("norm_in dnorm_in", got.dnorm_in, ref["dnorm_in"])
+        else:  # h is infinite, and without dn not used
+            got, ref = moe.moe_block_norm_backward(norm, x, y, dh), reference(norm, x, y, dh, None)
+            same_kind(f"{which} dy", got.dy, ref["dy"])
+            # A column of dgate is the sum of D yn over the rows times norm_out, one of dnorm_out
+            # the same times the gate: an infinite factor times the sum is infinite where the sum of
+            # infinite terms of either sign is NaN, so the kind in that column is left open.
+            for q in ("dgate", "dnorm_out"):
+                np.testing.assert_array_equal(np.isfinite(f64(getattr(got, q))), np.isfinite(ref[q]), err_msg=q)
+
+
+@pytest.mark.parametrize("type_", list(TYPES))
 @pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
 @pytest.mark.parametrize("d", WIDTHS + [64, 2048])
 def test_infinite_block_output_without_dn(d, gate, type_):
