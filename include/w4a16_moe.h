@@ -468,6 +468,8 @@ int moe_route_backward(const moe_route_backward_args* args, void* stream);
  *
  * moe_block_norm_backward -- its gradient, from dh and dn (either may be NULL: zero;
  *  dn only where norm_in is given), recomputing the statistics from x and y.
+ *  Without dn the gradient does not depend on h: an infinite or NaN element of y reaches
+ *  dgate and, behind a norm_out, its row of dy and dnorm_out, and nothing else.
  *  dx, dy    [T][d], type dtype, or NULL: not wanted.
  *  dgate     MOE_GATE_CHANNEL: [d] float32; MOE_GATE_TOKEN: [T] float32;
  *            MOE_GATE_FULL: [T][d], type dtype, rows at dgate_stride.  NULL: not wanted.
@@ -475,8 +477,9 @@ int moe_route_backward(const moe_route_backward_args* args, void* stream);
  *  The [d] gradients are summed over the rows in float32, in an order that depends on
  *  T, d and dtype alone.  dx may be dh itself and dy may be y or dn itself, at the same
  *  stride; otherwise outputs may not overlap inputs or each other.  workspace:
- *  moe_block_norm_backward_workspace_bytes(T, d) bytes, 256-byte aligned, needed for
- *  the [d] gradients only.  T == 0: they are set to zero.
+ *  moe_block_norm_backward_workspace_bytes(T, d) bytes (-1 for T < 0 or d < 1; the limits
+ *  above are checked by the call alone), 256-byte aligned, needed for the [d] gradients
+ *  only.  T == 0: they are set to zero.
  */
 enum moe_gate_kind { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 };
 

@@ -227,10 +227,11 @@ __device__ __forceinline__ void store_times(float* out, const S* factor, const P
 // Column sums: only A = sum over rows of D yn (g D yn for a token's or full gate) and
 // B = that of dn hn are kept; dnorm_out and a channel gate's gradient are A times the
 // channel gate and v_out.
-// Measured: T = 8192, d = 2048 in bf16 41 us for 201 MB (4.9 TB/s) and 5 for the sums
-// over the workgroups; 1001 rows of 1111 floats 10.6 and 4.6 us.  Many rows are bound by
-// HBM (7.4 TB/s while the rows run) and the launch around them; few rows by the chain of
-// one row, some 6 us from the first load to the column sums, and the two launches.  Two
+// Measured: T = 8192, d = 2048 in bf16 42 us for 201 MB (4.7 TB/s) and 5 for the sums
+// over the workgroups, with a full gate 56 us for 268 MB (4.8 TB/s); 1001 rows of 1111 floats
+// 11.0 and 4.4 us; 4096 rows of 1280 floats with a full gate 38 us for 168 MB (4.4 TB/s).
+// Many rows are bound by HBM and the launch around them; few rows by the chain of one row,
+// some 6 us from the first load to the column sums, and the two launches.  Two
 // wavefronts per SIMD that request x and y of the next row ran faster than one that requests all of it
 // (46.9 to 45.2 us for both launches) or two that request nothing (46.2); dn and dh requested
 // early too, or column sums that all slots hand over at once, changed nothing.
@@ -582,7 +583,9 @@ static NormSplit norm_split(int d, int target) {
 // per lane, that is the most wavefronts.  So rows of up to 2048 elements of two bytes or 1536
 // floats have one wavefront.  (bf16: d = 2560 three pieces 34.7 us, four 38.6; 5120 two
 // 46.8, four 52.7; 4096 four 49.4, two 51.1; 8192 four 50.4, two 54.3.)  Four pieces of floats
-// spill: only rows that nothing else takes have them.
+// spill some 100 registers, 180 with a full gate: only rows that nothing else takes have them.
+// (Of the others, floats with a full gate spill one register in rows by parts of a wavefront
+// and two with three pieces.)
 static NormSplit norm_back_split(int T, int d, int dtype) {
   NormSplit p;
   const int bytes = (int)dtype_bytes(dtype);

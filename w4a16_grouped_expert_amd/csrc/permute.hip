@@ -49,8 +49,11 @@ __device__ __forceinline__ float masked(float v, uint32_t mask) { return __uint_
 
 // Rows of more than 256 elements.  A wavefront handles 64 pieces of 8 elements of one
 // token with at most KM pairs: its positions and weights come through scalar loads, the
-// rows' addresses stay in scalar registers, and the loads of KB rows go out before the
-// first use.  Pairs that were dropped read some row that is there (`sorted_in` always has
+// rows' addresses are scalar, and the loads of KB rows go out before the first use.  Up to
+// four pairs fit the scalar registers in every form, eight without products.  With more of
+// them some wait in lanes of vector registers (25 to 41 for eight pairs with products, two
+// bytes gathered excepted; for sixteen 14 to 48, floats gathered 116, and 130 to 226 with
+// products).  Pairs that were dropped read some row that is there (`sorted_in` always has
 // one) and are masked, so that no load sits under a branch.
 // kStream: the sorted rows start on 16-byte boundaries.  Then they are read, each once, by
 // non-temporal loads (unpermute at T = 4096, d = 2048, k = 8: 29.0 to 26.8 us); off them
@@ -207,7 +210,8 @@ __global__ __launch_bounds__(256) void k_rows_short(PermuteDev a, const int32_t*
 // gradient of the way back k = 8 34.3 and 30.3 us, of permute 21.1 and 17.0, unpermute k = 12
 // 24.6 and 22.6; the others lose by it, permute k = 8 19.3 and 20.9, unpermute 14.7 and 15.0).
 // Tokens of which every CU has one at most keep all: their time is that of one token's rounds
-// (permute gradient, d = 4864, k = 12 in fp32: T = 128 17.4 and 26.3 us, T = 768 57.7 and 50.6).
+// (permute gradient, d = 4864, k = 12 in fp32: T = 128 17.4 and 26.3 us, T = 768 57.7 and 50.6;
+// nothing between the two was timed).
 static TokenSplit token_split(int T, int d, bool heavy) {
   TokenSplit p;
   const int pieces = (int)ceil_div(d, kPiece);

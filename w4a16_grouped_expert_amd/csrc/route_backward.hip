@@ -21,10 +21,12 @@
 // registers of their wavefront, without a barrier behind which the next loads would wait
 // (x through LDS too: dW alone 11.3 to 12.5 us at T = 4096, d = 2048, E = 64).
 //
-// Measured: T = 4096, d = 2048, E = 64, k = 8 from the pairs 16.2 us and 4.0 for the sum of
-// dW's parts (35 MB of x, W and results, without dx_add); T = 1021, d = 4096, E = 257 5.6 us for G,
-// 18.7 for the products.  What bounds the products is the vector memory path of a CU: a
-// step of 32 rows loads 14 KB per wavefront of dW (x and three parts of G) for 48 MFMA.
+// Measured: T = 4096, d = 2048, E = 64, k = 8 from the pairs 16.4 us and 3.9 for the sum of
+// dW's parts (52 MB with dx_add); T = 1021, d = 4096, E = 257 5.6 us for G, 19.7 for the
+// products.  A step of 32 rows loads 14 KB per wavefront of dW (x and three parts of G) for
+// 48 MFMA.  From the pairs a wavefront of dW has few such steps (four at T = 4096) and waits in each
+// for its pairs, which are not requested early.  With many experts the workgroups spread
+// unevenly (see route_back_plan).
 #include "rows.hpp"
 
 namespace moe {
@@ -35,7 +37,7 @@ constexpr int kRbStep = 32;    // rows of one MFMA
 // With the softmax over the selected experts, no loss on the logits and at most this many
 // experts, the wavefronts of the products build G from the pairs themselves, in tiles of
 // 32 tokens in LDS: no first launch (E = 64, d = 2048: T = 64 5.8 us in place of 8.1,
-// T = 4096 20.2 either way).  A tile of more experts would be built once per 64.
+// at T = 4096 the same either way).  A tile of more experts would be built once per 64.
 constexpr int kPairExperts = 64;
 constexpr int kTileFloats = 32 * (kPairExperts + 4);
 static_assert(MOE_MAX_TOPK <= 16, "a lane holds every other pair of its token, at most eight");
@@ -498,7 +500,8 @@ __device__ __forceinline__ void route_dw(const RouteBackDev& a, int block, f32x4
   }
 }
 
-// Both products in one launch: the first dw_blocks workgroups sum dW, the others dx.
+// Both products in one launch: the first dw_blocks workgroups sum dW, the others dx.  (Three
+// workgroups per CU leave 168 registers: with EB = 2 and G read three of them are spilled.)
 template <int EB, bool kPairs>
 __global__ __launch_bounds__(64 * kRbWaves, kPairs ? 2 : 3) void k_route_products(RouteBackDev a, int dw_blocks) {
   // dW: the wavefronts' sums; dx: 128 rows of W
@@ -542,8 +545,10 @@ static RouteBackPlan route_back_plan(int T, int d, int E) {
   p.EB = E <= 16 ? 1 : 2;
   const int64_t tiles = ceil_div(d, kRbCols) * ceil_div(E, 16 * p.EB);
   const int64_t most = std::max<int64_t>(1, ceil_div(p.Tp / kRbStep, kRbWaves));
-  // about 256 workgroups sum dW beside those of dx: T = 4096, d = 2048, E = 64 20.2 us, with
-  // 192 or 384 of them 21.9 or 22.1
+  // About 256 workgroups sum dW beside those of dx: at T = 4096, d = 2048, E = 64, the one size
+  // tried, 192 or 384 of them take 8 % longer.  Those of dx are not counted, nor a last tile of
+  // few experts: T = 1021, d = 4096, E = 257 has 288 and 256 workgroups for 256 CUs, 32 of them for
+  // one expert.
   p.splits = (int)std::min<int64_t>(most, std::max<int64_t>(1, ceil_div(256, tiles)));
   p.g_dx_bytes = 2 * p.Tp * p.Ep * 2;  // (multiples of 4096)
   p.g_dw_bytes = 3 * p.Tp * p.Ep * 2;
