@@ -522,6 +522,117 @@ int64_t moe_block_norm_backward_workspace_bytes(int T, int d);
 int moe_block_norm_backward(const moe_block_norm_args* args, const moe_block_norm_grads* grads, void* stream);
 
 /*
+ * moe_dropout -- dropout from a counter-based generator, with the residual's addition; no
+ * mask is stored.  (ExactMoE, Abstract: the layers around the routed experts stay in 16
+ * bits; in training they are regularised between the blocks.)
+ *
+ *    out[r][c] = residual[r][c] + (keep(r, c) ? x[r][c] / (1 - p) : 0)
+ *
+ *  The gradient of x is the same call on dout without a residual, that of the residual is
+ *  dout itself.
+ *  keep(r, c): ten rounds of Philox-4x32 (Salmon, Moraes, Dror and Shaw, "Parallel random
+ *  numbers: as easy as 1, 2, 3", 2011) on the counter (c / 8 + site 2^21, r, step mod 2^32,
+ *  step / 2^32) with the key (seed mod 2^32, seed / 2^32) give four words, that is eight
+ *  16-bit numbers, low halves first; the element is kept where number c mod 8 is at least
+ *  t = round(p 2^16) (halves up).  1 / (1 - p) is taken at p = t / 2^16, so that the
+ *  expectation is exact; p below 2^-17 drops nothing, t = 2^16 everything.
+ *  state     {seed, step}, two int64 in device memory (8-byte aligned), read when the call
+ *            runs: a caller that replays a graph advances step in between.  May be NULL for
+ *            p = 0.
+ *  site      which use of the step this is, 0 <= site < MOE_DROPOUT_SITES: calls with
+ *            different sites draw different numbers.
+ *  dtype     moe_dtype of x, residual and out [T][d]: contiguous rows at the given strides
+ *            (elements; inputs at least 0, out at least d), aligned to their type.
+ *  residual  or NULL: zero.  out may be x or residual itself, at the same stride; otherwise
+ *            it may not overlap them.
+ *  One float32 multiply-add, one rounding.  Dropped elements reach nothing, infinities and
+ *  NaN among them.
+ *  Limits: d <= 2^24, T ceil(d / 8) < 2^31 - 2^24 (ceil(d / 4) for MOE_FP32).  T == 0 is a
+ *  no-op.
+ */
+#define MOE_DROPOUT_SITES 2048
+int moe_dropout(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, int dtype, int T, int d,
+                double p, const int64_t* state, int site, void* out, int64_t out_stride, void* stream);
+
+/*
+ * moe_gated_ffn -- gated feed-forward blocks with 16-bit weights over rows sorted by expert
+ * (from moe_permute), or one dense block over all rows: experts in training, a shared expert
+ * beside the routed ones.  (ExactMoE, Abstract: SwiGLU experts, every selected expert of a
+ * step through fused grouped kernels.)  With W13 = [Wg; Wu] of the row's expert:
+ *
+ *    g = x Wg^T, u = x Wu^T, h = drop(act(g) u), y = h W2^T
+ *
+ *  dtype     MOE_BF16 or MOE_FP16, of every tensor.
+ *  rows      [num_rows][d].  expert_offsets [E+1] int32 from moe_align: rows
+ *            expert_offsets[e] .. expert_offsets[e+1] - 1 are expert e's (clamped to
+ *            num_rows); NULL with E = 1: all rows.  Rows behind the last expert's are
+ *            neither read nor written in any tensor of the call.
+ *  w13       [E][2I][d], gate rows then up rows; w2 [E][d][I]; contiguous (the layouts that
+ *            pack_w4_g128 takes, so trained weights are packed as they are).
+ *  activation  MOE_ACT_SILU, or MOE_ACT_GELU in its tanh form.
+ *  drop_p, drop_state, drop_site   dropout of h: moe_dropout's keep of element (row, column
+ *            of h).  0: none.
+ *  gu        [num_rows][2I] output, g then u, as the backward call takes them; or NULL.
+ *  h         [num_rows][I] output.  y [num_rows][d] output, or NULL: not wanted (w2 may be
+ *            NULL then).
+ *  Rows are contiguous at the given strides: multiples of 8 elements, at least a row, at most
+ *  2^20; pointers 16-byte aligned.  Outputs may not overlap inputs or each other.
+ *  Sums, activation and dropout in float32; g, u, h and y rounded once each; y is computed
+ *  from the rounded h (the operand of its product).  Deterministic.
+ *  Limits: d and I multiples of 8 up to 65536, E <= 1024, num_rows <= 2^24.  num_rows == 0
+ *  is a no-op.
+ *
+ * moe_gated_ffn_backward -- its gradient from dy, at the g, u and h that the forward call
+ *  stored, with the same dropout arguments:
+ *
+ *    dh = drop(dy W2), dg = dh u act'(g), du = dh act(g)
+ *    drows = [dg, du] W13, dw13[e] = [dg, du]^T rows, dw2[e] = dy^T h   (over e's rows)
+ *
+ *  drows [num_rows][d], dw13 [E][2I][d], dw2 [E][d][I]: NULL where not wanted; inputs that
+ *  only they need may be NULL then.  Gradients of experts without rows are zero.
+ *  Float32 sums; dg and du are rounded to dtype as the operands of their products, the
+ *  gradients once.  Deterministic.  dy and drows may not be the same tensor.
+ *  workspace moe_gated_ffn_backward_workspace_bytes(num_rows, d, I, E) bytes, 256-byte
+ *            aligned (-1 for sizes outside the limits); needed for drows and dw13.
+ *  num_rows == 0: dw13 and dw2 are set to zero.
+ */
+enum moe_activation { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1 };
+
+typedef struct {
+  int dtype;                      /* MOE_BF16 or MOE_FP16 */
+  int num_rows, d, I, E;
+  int activation;                 /* moe_activation */
+  const void* rows;
+  int64_t rows_stride;
+  const int32_t* expert_offsets;  /* [E+1] or NULL */
+  const void* w13;
+  const void* w2;
+  double drop_p;
+  const int64_t* drop_state;
+  int drop_site;
+} moe_gated_ffn_args;
+
+typedef struct {
+  const void* dy;
+  int64_t dy_stride;
+  const void* gu;
+  int64_t gu_stride;
+  const void* h;
+  int64_t h_stride;
+  void* drows;
+  int64_t drows_stride;
+  void* dw13;
+  void* dw2;
+  void* workspace;
+  int64_t workspace_bytes;
+} moe_gated_ffn_grads;
+
+int moe_gated_ffn(const moe_gated_ffn_args* args, void* gu, int64_t gu_stride, void* h, int64_t h_stride, void* y,
+                  int64_t y_stride, void* stream);
+int64_t moe_gated_ffn_backward_workspace_bytes(int num_rows, int d, int I, int E);
+int moe_gated_ffn_backward(const moe_gated_ffn_args* args, const moe_gated_ffn_grads* grads, void* stream);
+
+/*
  * Expert slot cache (ExactMoE, Abstract: quantised experts in pinned host
  * memory, executed from a configurable GPU-resident slot cache).
  *
@@ -638,7 +749,8 @@ int moe_slot_cache_state(const moe_slot_cache* cache, int32_t* slot_expert,
  * (BF16 experts), 8 = down (BF16 experts), 9 = gate/up (nested two/four-bit),
  * 10 = down (nested two/four-bit), 11 = moe_permute and moe_unpermute_backward,
  * 12 = moe_unpermute and moe_permute_backward, 13 = moe_route_backward (its launches
- * together), 14 = moe_block_norm, 15 = moe_block_norm_backward (its launches together).
+ * together), 14 = moe_block_norm, 15 = moe_block_norm_backward (its launches together),
+ * 16 = moe_gated_ffn, 17 = moe_gated_ffn_backward (their launches together), 18 = moe_dropout.
  */
 int moe_timing_enable(int on);
 int moe_timing_reset(void);

@@ -18,5 +18,7 @@ from .api import (MODE_AUTO, active_experts, MODE_DECODE, MODE_PREFILL, AlignOut
                   alloc_route_backward_workspace, moe_route_backward, moe_route_backward_into, BlockNorm,
                   BlockNormGrads, moe_block_norm, moe_block_norm_into, moe_block_norm_backward,
                   moe_block_norm_backward_into, block_norm_workspace_bytes, alloc_block_norm_workspace,
-                  GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL)
+                  GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL, Dropout, DROPOUT_SITES, moe_dropout, moe_dropout_into,
+                  ACT_SILU, ACT_GELU, GatedFfnGrads, moe_gated_ffn, moe_gated_ffn_into, gated_ffn_workspace_bytes,
+                  alloc_gated_ffn_workspace, moe_gated_ffn_backward, moe_gated_ffn_backward_into)
 from ._lib import LIB_PATH, MoeError, lib  # noqa: F401

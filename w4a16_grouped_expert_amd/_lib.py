@@ -83,6 +83,22 @@ class BlockNormGradArgs(ctypes.Structure):
     ]
 
 
+class GatedFfnArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", c_int), ("num_rows", c_int), ("d", c_int), ("I", c_int), ("E", c_int), ("activation", c_int),
+        ("rows", c_vp), ("rows_stride", c_i64), ("expert_offsets", c_vp), ("w13", c_vp), ("w2", c_vp),
+        ("drop_p", c_double), ("drop_state", c_vp), ("drop_site", c_int),
+    ]
+
+
+class GatedFfnGradArgs(ctypes.Structure):
+    _fields_ = [
+        ("dy", c_vp), ("dy_stride", c_i64), ("gu", c_vp), ("gu_stride", c_i64), ("h", c_vp), ("h_stride", c_i64),
+        ("drows", c_vp), ("drows_stride", c_i64), ("dw13", c_vp), ("dw2", c_vp), ("workspace", c_vp),
+        ("workspace_bytes", c_i64),
+    ]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [c_int]),
@@ -117,6 +133,10 @@ SIGNATURES = {
     "moe_block_norm": (c_int, [ctypes.POINTER(BlockNormArgs), c_vp, c_i64, c_vp, c_i64, c_vp]),
     "moe_block_norm_backward_workspace_bytes": (c_i64, [c_int, c_int]),
     "moe_block_norm_backward": (c_int, [ctypes.POINTER(BlockNormArgs), ctypes.POINTER(BlockNormGradArgs), c_vp]),
+    "moe_dropout": (c_int, [c_vp, c_i64, c_vp, c_i64, c_int, c_int, c_int, c_double, c_vp, c_int, c_vp, c_i64, c_vp]),
+    "moe_gated_ffn": (c_int, [ctypes.POINTER(GatedFfnArgs), c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "moe_gated_ffn_backward_workspace_bytes": (c_i64, [c_int, c_int, c_int, c_int]),
+    "moe_gated_ffn_backward": (c_int, [ctypes.POINTER(GatedFfnArgs), ctypes.POINTER(GatedFfnGradArgs), c_vp]),
     "moe_slot_cache_create": (c_int, [c_int, c_int, c_i64, c_vp, c_vp, ctypes.POINTER(c_vp)]),
     "moe_slot_cache_destroy": (c_int, [c_vp]),
     "slot_cache_load": (c_int, [c_vp, c_u64p, c_u64p, c_vp, c_i32p, c_i32p, c_vp, c_vp, c_vp]),

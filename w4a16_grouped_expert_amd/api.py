@@ -789,6 +789,172 @@ def moe_block_norm_backward(norm: BlockNorm, x, y: Optional[torch.Tensor] = None
     return moe_block_norm_backward_into(norm, x, y, grads, ws, dh, dn, stream)
 
 
+# ---------------------------------------------------------------- dropout
+
+DROPOUT_SITES = 2048  # MOE_DROPOUT_SITES in w4a16_moe.h
+
+
+@dataclass
+class Dropout:
+    """Dropout of one use in a step: elements are dropped with probability p, the others
+    scaled by 1 / (1 - p).  Which ones is a function of state, site, row and column alone, so
+    the gradient draws the same mask again.  state: int64 [2] on the GPU, seed and step,
+    read when the kernel runs (advance step between steps, also between a graph's replays);
+    site < 2048 tells the uses of one step apart."""
+    p: float
+    state: Optional[torch.Tensor] = None  # may be None for p = 0
+    site: int = 0
+
+
+def _drop(dropout, device):
+    """Probability, address of the state, and site."""
+    if dropout is None:
+        return 0.0, None, 0
+    state = None if dropout.state is None else _like(dropout.state, "dropout.state", torch.int64, (2,), device)
+    return dropout.p, state, dropout.site
+
+
+def moe_dropout_into(x, dropout: Dropout, out, residual: Optional[torch.Tensor] = None, stream=None):
+    """out = residual + dropped x (one rounding); x, residual and out [T, d] bf16, fp16 or
+    fp32 with any row stride.  out may be x or residual itself.  The gradient of x is the
+    same call on the gradient of out, without a residual."""
+    dtype, dev, T, d, xp, xs = _first_rows(x, "x")
+    rp, rs = (None, 0) if residual is None else _rows(residual, "residual", dtype, T, d, dev)
+    op, os = _rows(out, "out", dtype, T, d, dev, True)
+    p, state, site = _drop(dropout, dev)
+    check("moe_dropout", _launch(
+        lib().moe_dropout, dev, stream, xp, xs, rp, rs, DTYPES[dtype], T, d, p, state, site, op, os))
+    return out
+
+
+def moe_dropout(x, dropout: Dropout, residual: Optional[torch.Tensor] = None, stream=None):
+    """Allocating form of moe_dropout_into."""
+    _row_type(x, "x")
+    with _alloc_on(x.device, stream):
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return moe_dropout_into(x, dropout, out, residual, stream)
+
+
+# ---------------------------------------------------------------- gated feed-forward blocks
+
+ACT_SILU, ACT_GELU = 0, 1
+
+
+@dataclass
+class GatedFfnGrads:
+    """Outputs of moe_gated_ffn_backward, of the rows' type; None: not wanted."""
+    drows: Optional[torch.Tensor] = None  # [R, d]
+    dw13: Optional[torch.Tensor] = None   # [E, 2I, d]
+    dw2: Optional[torch.Tensor] = None    # [E, d, I]
+
+
+def _weights_shape(w, name, per_expert):
+    """E and the two sizes of a weight tensor [E, n, k], or [n, k] for one expert."""
+    if not isinstance(w, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if w.dim() not in (2, 3):
+        raise ValueError(f"{name} must be {per_expert} or [E, ...], got {tuple(w.shape)}")
+    return (1 if w.dim() == 2 else w.shape[0]), w.shape[-2], w.shape[-1]
+
+
+def _gated_ffn_args(rows, w13, w2, offsets, activation, dropout):
+    a = _lib.GatedFfnArgs()
+    dtype, dev, R, d, a.rows, a.rows_stride = _first_rows(rows, "rows")
+    E, twoI, _ = _weights_shape(w13, "w13", "[2I, d]")
+    I = twoI // 2
+    if twoI % 2:
+        raise ValueError(f"w13 must have 2I rows, got {twoI}")
+    lead = () if w13.dim() == 2 else (E,)
+    a.dtype, a.num_rows, a.d, a.I, a.E, a.activation = DTYPES[dtype], R, d, I, E, activation
+    a.w13 = _like(w13, "w13", dtype, (*lead, 2 * I, d), dev)
+    a.w2 = None if w2 is None else _like(w2, "w2", dtype, (*lead, d, I), dev)
+    if offsets is not None:
+        a.expert_offsets = _like(offsets, "offsets", torch.int32, (E + 1,), dev)
+    a.drop_p, a.drop_state, a.drop_site = _drop(dropout, dev)
+    return a, dtype, R, d, I, E, dev
+
+
+def moe_gated_ffn_into(rows, w13, w2, y, h, offsets: Optional[torch.Tensor] = None,
+                       gu: Optional[torch.Tensor] = None, activation=ACT_SILU, dropout: Optional[Dropout] = None,
+                       stream=None):
+    """y = drop(act(rows Wg^T) * (rows Wu^T)) W2^T per expert, with 16-bit weights.
+
+    rows [R, d] bf16 or fp16, sorted by expert (moe_permute) with offsets [E + 1] int32
+    (AlignOut.offsets), or offsets None for one dense block; w13 [E, 2I, d] gate rows then up
+    rows, w2 [E, d, I] ([2I, d] and [d, I] for one block).  h [R, I] receives the gated
+    product, gu [R, 2I] (for the backward call) both projections.  y None: h alone."""
+    a, dtype, R, d, I, E, dev = _gated_ffn_args(rows, w13, w2, offsets, activation, dropout)
+    hp, hs = _rows(h, "h", dtype, R, I, dev, True)
+    gp, gs = (None, 0) if gu is None else _rows(gu, "gu", dtype, R, 2 * I, dev, True)
+    yp, ys = (None, 0) if y is None else _rows(y, "y", dtype, R, d, dev, True)
+    check("moe_gated_ffn", _launch(
+        lib().moe_gated_ffn, dev, stream, ctypes.byref(a), gp, gs, hp, hs, yp, ys))
+    return y
+
+
+def moe_gated_ffn(rows, w13, w2, offsets: Optional[torch.Tensor] = None, activation=ACT_SILU,
+                  dropout: Optional[Dropout] = None, save=False, stream=None):
+    """Allocating form of moe_gated_ffn_into: y, or (y, h, gu) with save.  Rows behind the
+    last expert's come out as zeros."""
+    _row_type(rows, "rows")
+    (R, d), I, dev = rows.shape, _weights_shape(w13, "w13", "[2I, d]")[1] // 2, rows.device
+    new = torch.empty if offsets is None else torch.zeros
+    with _alloc_on(dev, stream):
+        y = new((R, d), dtype=rows.dtype, device=dev)
+        h = new((R, I), dtype=rows.dtype, device=dev)
+        gu = new((R, 2 * I), dtype=rows.dtype, device=dev) if save else None
+    moe_gated_ffn_into(rows, w13, w2, y, h, offsets, gu, activation, dropout, stream)
+    return (y, h, gu) if save else y
+
+
+def gated_ffn_workspace_bytes(R, d, I, E) -> int:
+    return int(lib().moe_gated_ffn_backward_workspace_bytes(R, d, I, E))
+
+
+def alloc_gated_ffn_workspace(R, d, I, E, device) -> torch.Tensor:
+    return torch.empty(max(gated_ffn_workspace_bytes(R, d, I, E), 256), dtype=torch.uint8, device=device)
+
+
+def moe_gated_ffn_backward_into(dy, rows, w13, w2, gu, h, grads: GatedFfnGrads, workspace: Optional[torch.Tensor],
+                                offsets: Optional[torch.Tensor] = None, activation=ACT_SILU,
+                                dropout: Optional[Dropout] = None, stream=None) -> GatedFfnGrads:
+    """Gradient of moe_gated_ffn from dy [R, d], at the gu and h of the forward call and with
+    its dropout.  The workspace (alloc_gated_ffn_workspace) is needed for drows and dw13."""
+    a, dtype, R, d, I, E, dev = _gated_ffn_args(rows, w13, w2, offsets, activation, dropout)
+    g = _lib.GatedFfnGradArgs()
+    g.dy, g.dy_stride = _rows(dy, "dy", dtype, R, d, dev)
+    if gu is not None:
+        g.gu, g.gu_stride = _rows(gu, "gu", dtype, R, 2 * I, dev)
+    if h is not None:
+        g.h, g.h_stride = _rows(h, "h", dtype, R, I, dev)
+    if grads.drows is not None:
+        g.drows, g.drows_stride = _rows(grads.drows, "drows", dtype, R, d, dev, True)
+    if grads.dw13 is not None:
+        g.dw13 = _like(grads.dw13, "dw13", dtype, w13.shape, dev)
+    if grads.dw2 is not None:
+        g.dw2 = _like(grads.dw2, "dw2", dtype, (*w13.shape[:-2], d, I), dev)
+    if workspace is not None:
+        g.workspace = _like(workspace, "workspace", torch.uint8, workspace.shape, dev)
+        g.workspace_bytes = workspace.numel()
+    check("moe_gated_ffn_backward", _launch(
+        lib().moe_gated_ffn_backward, dev, stream, ctypes.byref(a), ctypes.byref(g)))
+    return grads
+
+
+def moe_gated_ffn_backward(dy, rows, w13, w2, gu, h, offsets: Optional[torch.Tensor] = None, activation=ACT_SILU,
+                           dropout: Optional[Dropout] = None, stream=None) -> GatedFfnGrads:
+    """Allocating form of moe_gated_ffn_backward_into: every gradient.  Rows behind the last
+    expert's have a drows of zeros."""
+    _row_type(rows, "rows")
+    R, d = rows.shape
+    dev, (E, twoI, _) = rows.device, _weights_shape(w13, "w13", "[2I, d]")
+    new = torch.empty if offsets is None else torch.zeros
+    with _alloc_on(dev, stream):
+        grads = GatedFfnGrads(new((R, d), dtype=rows.dtype, device=dev), torch.empty_like(w13), torch.empty_like(w2))
+        ws = alloc_gated_ffn_workspace(R, d, twoI // 2, E, dev)
+    return moe_gated_ffn_backward_into(dy, rows, w13, w2, gu, h, grads, ws, offsets, activation, dropout, stream)
+
+
 class MoELayer:
     """One W4A16 MoE layer step with preallocated buffers (no allocation per call).
 
@@ -977,7 +1143,7 @@ class SlotCache:
 KERNELS = {"gateup_decode": 0, "down_decode": 1, "gateup_prefill": 2, "down_prefill": 3, "combine": 4,
            "gateup_bf16": 7, "down_bf16": 8, "gateup_mat": 9, "down_mat": 10,
            "route": 5, "align": 6, "permute": 11, "unpermute": 12, "route_backward": 13, "block_norm": 14,
-           "block_norm_backward": 15}
+           "block_norm_backward": 15, "gated_ffn": 16, "gated_ffn_backward": 17, "dropout": 18}
 
 
 def timing_enable(on: bool):

@@ -1,0 +1,489 @@
+// Gated feed-forward blocks with 16-bit weights, and their gradient: the experts of a
+// training step over rows sorted by expert, or one dense block over all rows (ExactMoE, page
+// "Every Expert Counts: ExactMoE for Memory-Efficient W4A16 Inference", Abstract: SwiGLU
+// experts; every selected expert of a step runs through fused grouped kernels).
+//
+//   g = x Wg^T, u = x Wu^T, h = drop(act(g) u), y = h Wd^T
+//   dh = drop(dy Wd), dg = dh u act'(g), du = dh act(g)
+//   dx = [dg, du] W13, dW13 = [dg, du]^T x, dWd = dy^T h
+//
+// Six products on the matrix cores (tile_product.hpp), each one launch over all experts:
+//   gate/up   A = rows (k = d), B = W13, gate and up rows of the same 128 columns in one tile:
+//             activation, product and dropout are applied to the float32 sums
+//   down      A = h, B = Wd
+//   dh        A = dy, B = Wd with n contiguous; dg and du are formed from the float32 sums
+//   dx        A = [dg, du], B = W13 with n contiguous
+//   dW13, dWd A and B with the rows as k, per expert
+// h, dg and du are rounded to the tensors' type once, as the operands of the next product.
+#include "philox.hpp"
+#include "tile_product.hpp"
+
+namespace moe {
+
+enum ProductKind { kGateUp, kDown, kGateBack, kRowsBack, kWeightBack };
+
+constexpr int kXcds = 8;
+
+struct ProductDev {
+  const char* a;
+  const char* b;
+  int64_t b_expert;   // bytes between two experts' weights
+  int lda, ldb;       // elements
+  int M, N, K;        // kWeightBack: K by expert; else M by expert
+  int R, E;
+  const int32_t* offsets;  // or NULL: one expert, all rows
+  char* out;          // kGateUp: h; kGateBack: [dg, du]
+  int ldo;
+  char* gu;           // kGateUp: written unless NULL; kGateBack: read
+  int ldgu;
+  int activation;
+  DropDev drop;
+};
+
+// Rows of expert e, clamped to the R that are there.
+__device__ __forceinline__ void expert_rows(const ProductDev& p, int e, int& row0, int& count) {
+  if (!p.offsets) {
+    row0 = 0;
+    count = p.R;
+    return;
+  }
+  row0 = min(max(p.offsets[e], 0), p.R);
+  count = max(min(p.offsets[e + 1], p.R) - row0, 0);
+}
+
+// The activation and its derivative, both by one logistic function (gelu in its tanh form is
+// g / (1 + exp(-2 z)), z = sqrt(2 / pi) (g + 0.044715 g^3)); hardware exp and reciprocal, a
+// few units in the last place of float32 before a rounding to 16 bits.
+__device__ __forceinline__ float activate(int activation, float g, float& slope) {
+  float s = g, ds = 1.f;
+  if (activation == MOE_ACT_GELU) {
+    const float c = fminf(fmaxf(g, -30.f), 30.f), c2 = c * c;  // saturated beyond
+    s = 1.5957691216f * c * fmaf(0.044715f, c2, 1.f);
+    ds = 1.5957691216f * fmaf(0.134145f, c2, 1.f);
+  }
+  const float p = __builtin_amdgcn_rcpf(1.f + __expf(-s));
+  const float a = g * p;
+  slope = fmaf(a * (1.f - p), ds, p);
+  return a;
+}
+
+template <typename S>
+__device__ __forceinline__ u32x4_t pack8(const float (&v)[8]) {
+  return pack<S>(v).w[0];
+}
+
+template <typename S, int kKind, int kMI>
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_product(ProductDev p) {
+  constexpr int kTileM = kMI * 32;
+  constexpr bool kDual = kKind == kGateUp;
+  constexpr bool kAMContig = kKind == kWeightBack;
+  constexpr bool kBMContig = kKind >= kGateBack;
+  constexpr int kCols = kDual ? kTileN / 2 : kTileN;
+  typedef Stager<kTileM, kAMContig> StageA;
+  typedef Stager<kTileN, kBMContig, kDual> StageB;
+  constexpr int kStage = StageA::kBytes + StageB::kBytes;
+  __shared__ __attribute__((aligned(1024))) char s_stage[2 * kStage];
+  __shared__ int s_first[kKind == kWeightBack ? 1 : MOE_MAX_EXPERTS + 1];  // first m tile of each expert
+
+  const int tid = threadIdx.x, lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const int NT = (p.N + kCols - 1) / kCols;
+
+  // ---- the tiles: m tiles of each expert, one expert behind the other
+  int m_tiles;
+  if constexpr (kKind == kWeightBack) {
+    m_tiles = (p.M + kTileM - 1) / kTileM;
+  } else {
+    if (wave == 0) {
+      int carry = 0;
+      for (int base = 0; base < p.E; base += 64) {
+        int row0 = 0, v = 0;
+        if (base + lane < p.E) expert_rows(p, base + lane, row0, v);
+        v = (v + kTileM - 1) / kTileM;
+        for (int off = 1; off < 64; off <<= 1) {
+          const int o = __shfl_up(v, off);
+          if (lane >= off) v += o;
+        }
+        if (base + lane < p.E) s_first[base + lane + 1] = carry + v;
+        carry += __shfl(v, 63);
+      }
+      if (lane == 0) s_first[0] = 0;
+    }
+    __syncthreads();
+    m_tiles = s_first[p.E];
+  }
+  const int total = kKind == kWeightBack ? p.E * m_tiles * NT : m_tiles * NT;
+  // each XCD takes a contiguous run of tiles, so that those that share operands meet in its L2
+  const int chunk = (total + kXcds - 1) / kXcds;
+  const int xcd = blockIdx.x % kXcds, per_xcd = gridDim.x / kXcds;
+  const int last = min(total, (xcd + 1) * chunk);
+
+  Reader<kTileM, kAMContig> ra;
+  Reader<kTileN, kBMContig> rb;
+  ra.start(wm, 2, lane);
+  rb.start(kDual ? 2 * wn : 4 * wn, 1, lane);
+  const uint32_t lds = (uint32_t)(uintptr_t)s_stage;
+
+  for (int tile = xcd * chunk + blockIdx.x / kXcds; tile < last; tile += per_xcd) {
+    // ---- expert, rows, first row and column of the tile.  Panels of eight m tiles, m fastest.
+    int e = 0, row0, count, mt = 0, mts;
+    int idx;
+    if constexpr (kKind == kWeightBack) {
+      e = tile / (m_tiles * NT);
+      idx = tile - e * m_tiles * NT;
+      mts = m_tiles;
+    } else {
+      int lo = 0, hi = p.E;
+      const int mtile = tile / NT;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_first[mid] <= mtile) lo = mid; else hi = mid;
+      }
+      e = lo;
+      idx = tile - s_first[e] * NT;
+      mts = s_first[e + 1] - s_first[e];
+    }
+    e = __builtin_amdgcn_readfirstlane(e);
+    idx = __builtin_amdgcn_readfirstlane(idx);
+    mts = __builtin_amdgcn_readfirstlane(mts);
+    expert_rows(p, e, row0, count);
+    row0 = __builtin_amdgcn_readfirstlane(row0);
+    count = __builtin_amdgcn_readfirstlane(count);
+    const int panel = idx / (8 * NT), rest = idx - panel * 8 * NT;
+    const int high = min(8, mts - panel * 8);
+    const int nt = rest / high;
+    mt = panel * 8 + rest - nt * high;
+    const int m0 = mt * kTileM, n0 = nt * kCols;
+    const int K = kKind == kWeightBack ? count : p.K;
+    const int m_left = (kKind == kWeightBack ? p.M : count) - m0;
+
+    StageA sa;
+    StageB sb;
+    if constexpr (kKind == kWeightBack) {
+      sa.start({p.a + ((int64_t)row0 * p.lda + m0) * 2, p.lda, m_left}, K, wave, lane);
+      sb.start({p.b + ((int64_t)row0 * p.ldb + n0) * 2, p.ldb, p.N - n0}, K, wave, lane);
+    } else {
+      sa.start({p.a + ((int64_t)row0 + m0) * p.lda * 2, p.lda, m_left}, K, wave, lane);
+      const char* b = p.b + e * p.b_expert;
+      if constexpr (kDual) {
+        const OperandTile up{b + ((int64_t)p.N + n0) * p.ldb * 2, p.ldb, p.N - n0};
+        sb.start({b + (int64_t)n0 * p.ldb * 2, p.ldb, p.N - n0}, K, wave, lane, &up);
+      } else if constexpr (kBMContig) {
+        sb.start({b + (int64_t)n0 * 2, p.ldb, p.N - n0}, K, wave, lane);
+      } else {
+        sb.start({b + (int64_t)n0 * p.ldb * 2, p.ldb, p.N - n0}, K, wave, lane);
+      }
+    }
+
+    f32x4_t acc[kMI][kNI];
+#pragma unroll
+    for (int i = 0; i < kMI; ++i)
+#pragma unroll
+      for (int j = 0; j < kNI; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    const int steps = (K + kStepK - 1) / kStepK;
+    stage_barrier();  // the previous tile's stages are read
+    if (steps > 0) {
+      sa.issue(0, lds, wave);
+      sb.issue(0, lds + StageA::kBytes, wave);
+    }
+    // blocks of 16 rows that this wavefront has at all
+    const int blocks = min(kMI, (min((m_left + 15) / 16, 2 * kMI) - wm + 1) / 2);
+    auto run = [&](auto count_c) {
+      constexpr int kCount = decltype(count_c)::value;
+      for (int step = 0; step < steps; ++step) {
+        stage_barrier();
+        const uint32_t other = lds + ((step + 1) & 1) * kStage;
+        if (step + 1 < steps) {
+          sa.issue((step + 1) * kStepK, other, wave);
+          sb.issue((step + 1) * kStepK, other + StageA::kBytes, wave);
+        }
+        const char* st = s_stage + (step & 1) * kStage;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          u32x4_t fa[kCount], fb[kNI];
+#pragma unroll
+          for (int j = 0; j < kNI; ++j)
+            fb[j] = rb.template get<1>(st + StageA::kBytes, kDual ? (j & 1) + 8 * (j >> 1) : j, s);
+#pragma unroll
+          for (int i = 0; i < kCount; ++i) fa[i] = ra.template get<2>(st, kAMContig ? i : 2 * i, s);
+#pragma unroll
+          for (int i = 0; i < kCount; ++i)
+#pragma unroll
+            for (int j = 0; j < kNI; ++j) acc[i][j] = mfma16<S>(fb[j], fa[i], acc[i][j]);
+        }
+      }
+    };
+    if (blocks > kMI / 2)
+      run(std::integral_constant<int, kMI>{});
+    else
+      run(std::integral_constant<int, kMI / 2>{});
+
+    // ---- epilogue: eight consecutive columns of a row per lane and pair of blocks
+    DropKey key{};
+    const bool drops = (kKind == kGateUp || kKind == kGateBack) && p.drop.threshold;
+    if (drops) key = drop_key(p.drop);
+#pragma unroll
+    for (int i = 0; i < kMI; ++i) {
+      const int m = m0 + 16 * (2 * i + wm) + (lane & 15);
+      const bool inside = m - m0 < m_left;
+      const int64_t row = kKind == kWeightBack ? m : (int64_t)row0 + m;
+      if constexpr (kKind == kGateUp) {
+        const int col = n0 + 32 * wn + eight_column(lane);
+        float g[8], u[8];
+        eight_columns(acc[i][0], acc[i][1], g);
+        eight_columns(acc[i][2], acc[i][3], u);
+        if (!inside || col >= p.N) continue;
+        if (p.gu) {
+          char* at = p.gu + (row * p.ldgu + col) * 2;
+          *reinterpret_cast<u32x4_t*>(at) = pack8<S>(g);
+          *reinterpret_cast<u32x4_t*>(at + (int64_t)p.N * 2) = pack8<S>(u);
+        }
+        u32x4_t n{};
+        if (drops) n = drop_numbers(key, p.drop.site, (uint32_t)row, (uint32_t)col >> 3);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float slope;
+          g[c] = activate(p.activation, g[c], slope) * u[c];
+          if (drops) g[c] = drop_keeps(n, c, p.drop.threshold) ? g[c] * p.drop.scale : 0.f;
+        }
+        *reinterpret_cast<u32x4_t*>(p.out + (row * p.ldo + col) * 2) = pack8<S>(g);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kNI; j += 2) {
+          const int col = n0 + 64 * wn + 16 * j + eight_column(lane);
+          float v[8];
+          eight_columns(acc[i][j], acc[i][j + 1], v);
+          if (!inside || col >= p.N) continue;
+          if constexpr (kKind == kGateBack) {
+            const char* at = p.gu + (row * p.ldgu + col) * 2;
+            Raw<S> rg, ru;
+            rg.w[0] = *reinterpret_cast<const u32x4_t*>(at);
+            ru.w[0] = *reinterpret_cast<const u32x4_t*>(at + (int64_t)p.N * 2);
+            float g[8], u[8];
+            unpack(rg, g);
+            unpack(ru, u);
+            u32x4_t n{};
+            if (drops) n = drop_numbers(key, p.drop.site, (uint32_t)row, (uint32_t)col >> 3);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              if (drops) v[c] = drop_keeps(n, c, p.drop.threshold) ? v[c] * p.drop.scale : 0.f;
+              float slope;
+              const float act = activate(p.activation, g[c], slope);
+              g[c] = v[c] * u[c] * slope;
+              u[c] = v[c] * act;
+            }
+            char* to = p.out + (row * p.ldo + col) * 2;
+            *reinterpret_cast<u32x4_t*>(to) = pack8<S>(g);
+            *reinterpret_cast<u32x4_t*>(to + (int64_t)p.N * 2) = pack8<S>(u);
+          } else {
+            char* to = p.out + (kKind == kWeightBack ? (int64_t)e * p.M * p.N * 2 : 0) + (row * p.ldo + col) * 2;
+            *reinterpret_cast<u32x4_t*>(to) = pack8<S>(v);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Tiles of 256 rows where the experts' rows fill them, else of 128.
+template <int kKind>
+static void launch_product(const ProductDev& p, int dtype, hipStream_t s) {
+  const int64_t cols = kKind == kGateUp ? kTileN / 2 : kTileN;
+  const bool big = kKind == kWeightBack ? p.M > 128 : (int64_t)p.R >= (int64_t)p.E * 1024;
+  const int64_t tm = big ? 256 : 128;
+  const int64_t m_tiles = kKind == kWeightBack ? p.E * ceil_div(p.M, tm) : p.R / tm + std::min(p.E, p.R);
+  const int64_t tiles = m_tiles * ceil_div(p.N, cols);
+  const unsigned grid = (unsigned)std::min<int64_t>(256, ceil_div(tiles, kXcds) * kXcds);
+  auto go = [&](auto type) {
+    using S = decltype(type);
+    if (big)
+      hipLaunchKernelGGL((k_product<S, kKind, 8>), dim3(grid), dim3(kTileThreads), 0, s, p);
+    else
+      hipLaunchKernelGGL((k_product<S, kKind, 4>), dim3(grid), dim3(kTileThreads), 0, s, p);
+  };
+  if (dtype == MOE_BF16)
+    go(bf16_row_t{});
+  else
+    go(_Float16{});
+}
+
+constexpr int kFfnMaxSize = 1 << 16;    // d and I
+constexpr int kFfnMaxStride = 1 << 20;  // elements between rows: a tile's rows lie within 2^31 bytes
+
+static int check_ffn(const char* fn, const moe_gated_ffn_args* a) {
+  MOE_CHECK_ARG(a != nullptr, MOE_ERR_INVALID_ARG, "%s: args is NULL", fn);
+  MOE_CHECK_ARG(a->dtype == MOE_BF16 || a->dtype == MOE_FP16, MOE_ERR_INVALID_ARG, "%s: bad dtype %d (bf16 or fp16)", fn,
+                a->dtype);
+  MOE_CHECK_ARG(a->activation == MOE_ACT_SILU || a->activation == MOE_ACT_GELU, MOE_ERR_INVALID_ARG,
+                "%s: bad activation %d", fn, a->activation);
+  MOE_CHECK_ARG(a->num_rows >= 0 && a->d > 0 && a->I > 0 && a->E > 0, MOE_ERR_INVALID_ARG,
+                "%s: bad sizes num_rows=%d d=%d I=%d E=%d", fn, a->num_rows, a->d, a->I, a->E);
+  MOE_CHECK_ARG(a->d % 8 == 0 && a->I % 8 == 0 && a->d <= kFfnMaxSize && a->I <= kFfnMaxSize &&
+                    a->E <= MOE_MAX_EXPERTS && a->num_rows <= (1 << 24),
+                MOE_ERR_UNSUPPORTED_SHAPE,
+                "%s: unsupported num_rows=%d d=%d I=%d E=%d (d and I multiples of 8 up to %d, E <= %d, num_rows <= 2^24)",
+                fn, a->num_rows, a->d, a->I, a->E, kFfnMaxSize, MOE_MAX_EXPERTS);
+  MOE_CHECK_ARG(a->expert_offsets ? ((uintptr_t)a->expert_offsets % 4) == 0 : a->E == 1, MOE_ERR_INVALID_ARG,
+                "%s: expert_offsets is misaligned, or NULL for E=%d", fn, a->E);
+  return check_dropout(fn, a->drop_p, a->drop_state, a->drop_site);
+}
+
+static int check_matrix(const char* fn, const char* name, const void* p, int64_t stride, int64_t least, bool wanted) {
+  if (!wanted) return MOE_OK;
+  MOE_CHECK_ARG(p && ((uintptr_t)p % 16) == 0, MOE_ERR_INVALID_ARG, "%s: %s is NULL or not 16-byte aligned", fn, name);
+  MOE_CHECK_ARG(stride >= least && stride % 8 == 0, MOE_ERR_INVALID_ARG,
+                "%s: stride %lld of %s below %lld or no multiple of 8", fn, (long long)stride, name, (long long)least);
+  MOE_CHECK_ARG(stride <= kFfnMaxStride, MOE_ERR_UNSUPPORTED_SHAPE, "%s: stride %lld of %s above 2^20", fn,
+                (long long)stride, name);
+  return MOE_OK;
+}
+
+static ProductDev product(const moe_gated_ffn_args* a) {
+  ProductDev p{};
+  p.R = a->num_rows;
+  p.E = a->E;
+  p.offsets = a->expert_offsets;
+  p.activation = a->activation;
+  p.drop = drop_dev(a->drop_p, a->drop_state, a->drop_site);
+  return p;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_gated_ffn(const moe_gated_ffn_args* a, void* gu, int64_t gu_stride, void* h, int64_t h_stride, void* y,
+                             int64_t y_stride, void* stream) {
+  clear_error();
+  const char* fn = "moe_gated_ffn";
+  int rc = check_ffn(fn, a);
+  if (rc || a->num_rows == 0) return rc;
+  const int64_t d = a->d, I = a->I;
+  if ((rc = check_matrix(fn, "rows", a->rows, a->rows_stride, d, true))) return rc;
+  if ((rc = check_matrix(fn, "w13", a->w13, d, d, true))) return rc;
+  if ((rc = check_matrix(fn, "w2", a->w2, I, I, y != nullptr))) return rc;
+  if ((rc = check_matrix(fn, "gu", gu, gu_stride, 2 * I, gu != nullptr))) return rc;
+  if ((rc = check_matrix(fn, "h", h, h_stride, I, true))) return rc;
+  if ((rc = check_matrix(fn, "y", y, y_stride, d, y != nullptr))) return rc;
+  hipStream_t s = (hipStream_t)stream;
+  timing_begin(K_GATED_FFN, s);
+  ProductDev p = product(a);
+  p.a = static_cast<const char*>(a->rows);
+  p.lda = (int)a->rows_stride;
+  p.b = static_cast<const char*>(a->w13);
+  p.ldb = a->d;
+  p.b_expert = 2 * I * d * 2;
+  p.N = a->I;
+  p.K = a->d;
+  p.out = static_cast<char*>(h);
+  p.ldo = (int)h_stride;
+  p.gu = static_cast<char*>(gu);
+  p.ldgu = (int)gu_stride;
+  launch_product<kGateUp>(p, a->dtype, s);
+  if (y) {
+    ProductDev q = product(a);
+    q.a = static_cast<const char*>(h);
+    q.lda = (int)h_stride;
+    q.b = static_cast<const char*>(a->w2);
+    q.ldb = a->I;
+    q.b_expert = d * I * 2;
+    q.N = a->d;
+    q.K = a->I;
+    q.out = static_cast<char*>(y);
+    q.ldo = (int)y_stride;
+    launch_product<kDown>(q, a->dtype, s);
+  }
+  timing_end(K_GATED_FFN, s);
+  return check_launch(fn);
+}
+
+extern "C" int64_t moe_gated_ffn_backward_workspace_bytes(int num_rows, int d, int I, int E) {
+  if (num_rows < 0 || d <= 0 || I <= 0 || E <= 0) return -1;
+  if (d % 8 || I % 8 || d > kFfnMaxSize || I > kFfnMaxSize || E > MOE_MAX_EXPERTS || num_rows > (1 << 24)) return -1;
+  return ceil_div((int64_t)num_rows * 2 * I * 2, 256) * 256;
+}
+
+extern "C" int moe_gated_ffn_backward(const moe_gated_ffn_args* a, const moe_gated_ffn_grads* g, void* stream) {
+  clear_error();
+  const char* fn = "moe_gated_ffn_backward";
+  int rc = check_ffn(fn, a);
+  if (rc) return rc;
+  MOE_CHECK_ARG(g != nullptr, MOE_ERR_INVALID_ARG, "%s: grads is NULL", fn);
+  MOE_CHECK_ARG(g->drows || g->dw13 || g->dw2 || a->num_rows == 0, MOE_ERR_INVALID_ARG, "%s: no gradient is wanted", fn);
+  const int64_t d = a->d, I = a->I;
+  const bool some = a->num_rows > 0, through = g->drows || g->dw13;
+  if ((rc = check_matrix(fn, "dy", g->dy, g->dy_stride, d, some))) return rc;
+  if ((rc = check_matrix(fn, "rows", a->rows, a->rows_stride, d, some && g->dw13))) return rc;
+  if ((rc = check_matrix(fn, "w13", a->w13, d, d, some && g->drows))) return rc;
+  if ((rc = check_matrix(fn, "w2", a->w2, I, I, some && through))) return rc;
+  if ((rc = check_matrix(fn, "gu", g->gu, g->gu_stride, 2 * I, some && through))) return rc;
+  if ((rc = check_matrix(fn, "h", g->h, g->h_stride, I, some && g->dw2))) return rc;
+  if ((rc = check_matrix(fn, "drows", g->drows, g->drows_stride, d, some && g->drows))) return rc;
+  if ((rc = check_matrix(fn, "dw13", g->dw13, d, d, g->dw13 != nullptr))) return rc;
+  if ((rc = check_matrix(fn, "dw2", g->dw2, I, I, g->dw2 != nullptr))) return rc;
+  const int64_t need = moe_gated_ffn_backward_workspace_bytes(a->num_rows, a->d, a->I, a->E);
+  MOE_CHECK_ARG(!some || !through ||
+                    (g->workspace && g->workspace_bytes >= need && ((uintptr_t)g->workspace % 256) == 0),
+                MOE_ERR_WORKSPACE, "%s: workspace of %lld bytes < %lld needed, NULL or misaligned", fn,
+                (long long)g->workspace_bytes, (long long)need);
+  if (!some && !g->dw13 && !g->dw2) return MOE_OK;
+  hipStream_t s = (hipStream_t)stream;
+  timing_begin(K_GATED_FFN_BWD, s);
+  char* dgu = static_cast<char*>(g->workspace);
+  if (some && through) {
+    ProductDev p = product(a);
+    p.a = static_cast<const char*>(g->dy);
+    p.lda = (int)g->dy_stride;
+    p.b = static_cast<const char*>(a->w2);
+    p.ldb = a->I;
+    p.b_expert = d * I * 2;
+    p.N = a->I;
+    p.K = a->d;
+    p.out = dgu;
+    p.ldo = 2 * a->I;
+    p.gu = static_cast<char*>(const_cast<void*>(g->gu));
+    p.ldgu = (int)g->gu_stride;
+    launch_product<kGateBack>(p, a->dtype, s);
+  }
+  if (some && g->drows) {
+    ProductDev p = product(a);
+    p.a = dgu;
+    p.lda = 2 * a->I;
+    p.b = static_cast<const char*>(a->w13);
+    p.ldb = a->d;
+    p.b_expert = 2 * I * d * 2;
+    p.N = a->d;
+    p.K = 2 * a->I;
+    p.out = static_cast<char*>(g->drows);
+    p.ldo = (int)g->drows_stride;
+    launch_product<kRowsBack>(p, a->dtype, s);
+  }
+  if (g->dw13) {
+    ProductDev p = product(a);
+    p.a = dgu;
+    p.lda = 2 * a->I;
+    p.b = static_cast<const char*>(a->rows);
+    p.ldb = (int)a->rows_stride;
+    p.M = 2 * a->I;
+    p.N = a->d;
+    p.out = static_cast<char*>(g->dw13);
+    p.ldo = a->d;
+    launch_product<kWeightBack>(p, a->dtype, s);
+  }
+  if (g->dw2) {
+    ProductDev p = product(a);
+    p.a = static_cast<const char*>(g->dy);
+    p.lda = (int)g->dy_stride;
+    p.b = static_cast<const char*>(g->h);
+    p.ldb = (int)g->h_stride;
+    p.M = a->d;
+    p.N = a->I;
+    p.out = static_cast<char*>(g->dw2);
+    p.ldo = a->I;
+    launch_product<kWeightBack>(p, a->dtype, s);
+  }
+  timing_end(K_GATED_FFN_BWD, s);
+  return check_launch(fn);
+}

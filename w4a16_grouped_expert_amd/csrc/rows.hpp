@@ -9,7 +9,8 @@
 namespace moe {
 
 // timing ids of the row operators, behind those of the grouped passes
-enum RowKernelId { K_PERMUTE = K_NUM, K_UNPERMUTE, K_ROUTE_BWD, K_BLOCK_NORM, K_BLOCK_NORM_BWD, K_NUM_ALL };
+enum RowKernelId { K_PERMUTE = K_NUM, K_UNPERMUTE, K_ROUTE_BWD, K_BLOCK_NORM, K_BLOCK_NORM_BWD, K_GATED_FFN,
+                   K_GATED_FFN_BWD, K_DROPOUT, K_NUM_ALL };
 static_assert(K_PERMUTE == 11, "the ids the header lists");
 
 struct bf16_row_t {
