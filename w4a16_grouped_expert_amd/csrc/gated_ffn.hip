@@ -72,6 +72,24 @@ __device__ __forceinline__ u32x4_t pack8(const float (&v)[8]) {
   return pack<S>(v).w[0];
 }
 
+// Stages of a workgroup: as many as fit beside the table of the experts' first tiles.
+constexpr int product_depth(int mi) { return mi == 8 ? 4 : 6; }
+
+// The lane's number as a value that the compiler does not see through: what follows from it is
+// computed where it is used, in place of registers held through the products.
+__device__ __forceinline__ int fresh_lane() {
+  int l = lane_id();
+  asm volatile("" : "+v"(l));
+  return l;
+}
+
+// One tile of a product.
+struct Tile {
+  int e, row0, m0, n0, m_left, K;
+};
+
+// Persistent workgroups, each with its tiles in turn.  All loads are issued kDepth steps ahead of
+// the products by a cursor of its own, which runs into the next tile while this one ends.
 template <typename S, int kKind, int kMI>
 __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_product(ProductDev p) {
   constexpr int kTileM = kMI * 32;
@@ -79,21 +97,71 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2,
   constexpr bool kAMContig = kKind == kWeightBack;
   constexpr bool kBMContig = kKind >= kGateBack;
   constexpr int kCols = kDual ? kTileN / 2 : kTileN;
+  constexpr int kDepth = product_depth(kMI);
   typedef Stager<kTileM, kAMContig> StageA;
   typedef Stager<kTileN, kBMContig, kDual> StageB;
   constexpr int kStage = StageA::kBytes + StageB::kBytes;
-  __shared__ __attribute__((aligned(1024))) char s_stage[2 * kStage];
+  constexpr int kIssues = StageA::kIssues + StageB::kIssues;
+  constexpr int kPending = (kDepth - 2) * kIssues;
+  constexpr int kAhead = 4;  // tiles that the cursor may be ahead, and one
+  // stores of a tile's epilogue per wavefront (without those of g and u, which may be missing)
+  constexpr int kStores = kKind == kGateUp ? kMI : kKind == kGateBack ? 4 * kMI : 2 * kMI;
+  static_assert(kPending + kStores < 64, "the counter's six bits");
+  static_assert(kDepth % 2 == 0 && kDepth / 2 < kAhead, "a tile has two steps at least");
+  __shared__ __attribute__((aligned(1024))) char s_stage[kDepth * kStage];
   __shared__ int s_first[kKind == kWeightBack ? 1 : MOE_MAX_EXPERTS + 1];  // first m tile of each expert
+  __shared__ Tile s_tile[kTileWaves][kAhead];  // each wavefront's own copy of the tiles ahead
 
   const int tid = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave & 1, wn = wave >> 1;
   const int NT = (p.N + kCols - 1) / kCols;
 
-  // ---- the tiles: m tiles of each expert, one expert behind the other
+  // ---- the tiles: m tiles of each expert, one expert behind the other.  Each XCD takes a
+  // contiguous run of them, so that those that share operands meet in its L2, of an equal share of
+  // the work: for the weights' gradients, whose experts have unequal K, steps and the store.
   int m_tiles;
+  const int xcd = blockIdx.x % kXcds, per_xcd = gridDim.x / kXcds;
+  int from_tile, last_tile;
   if constexpr (kKind == kWeightBack) {
     m_tiles = (p.M + kTileM - 1) / kTileM;
+    const int per_expert = m_tiles * NT;
+    // (a tile's store costs about as much as kStoreSteps steps)
+    constexpr int kStoreSteps = 8;
+    auto cost_of = [&](int e) {
+      int row0, count = 0;
+      if (e < p.E) expert_rows(p, e, row0, count);
+      return e < p.E ? (count + kStepK - 1) / kStepK + kStoreSteps : 0;
+    };
+    int whole = 0;  // cost of one tile of every expert: below 2^24 / 32 + 9 E
+    for (int base = 0; base < p.E; base += 64) whole += cost_of(base + lane);
+    for (int off = 32; off; off >>= 1) whole += __shfl_xor(whole, off);
+    whole = __builtin_amdgcn_readfirstlane(whole);
+    // first tile of XCD x: the first one whose predecessors have at least x eighths of the work
+    auto first_of = [&](int x) {
+      const int64_t target = ((int64_t)whole * per_expert * x + kXcds - 1) / kXcds;
+      int64_t before = 0;
+      for (int base = 0; base < p.E; base += 64) {
+        const int mine = cost_of(base + lane);
+        int v = mine;
+        for (int off = 1; off < 64; off <<= 1) {
+          const int o = __shfl_up(v, off);
+          if (lane >= off) v += o;
+        }
+        const int64_t end = before + (int64_t)v * per_expert;
+        const uint64_t past = __ballot(end > target);
+        if (past) {
+          const int l = __ffsll((unsigned long long)past) - 1;
+          const int64_t start = before + (int64_t)(__shfl(v, l) - __shfl(mine, l)) * per_expert;
+          const int cost = __shfl(mine, l);
+          return (base + l) * per_expert + (int)((target - start + cost - 1) / cost);
+        }
+        before += (int64_t)__shfl(v, 63) * per_expert;
+      }
+      return p.E * per_expert;
+    };
+    from_tile = __builtin_amdgcn_readfirstlane(first_of(xcd));
+    last_tile = __builtin_amdgcn_readfirstlane(first_of(xcd + 1));
   } else {
     if (wave == 0) {
       int carry = 0;
@@ -111,70 +179,109 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2,
       if (lane == 0) s_first[0] = 0;
     }
     __syncthreads();
-    m_tiles = s_first[p.E];
+    m_tiles = __builtin_amdgcn_readfirstlane(s_first[p.E]);
+    const int total = m_tiles * NT, chunk = (total + kXcds - 1) / kXcds;
+    from_tile = xcd * chunk;
+    last_tile = min(total, from_tile + chunk);
   }
-  const int total = kKind == kWeightBack ? p.E * m_tiles * NT : m_tiles * NT;
-  // each XCD takes a contiguous run of tiles, so that those that share operands meet in its L2
-  const int chunk = (total + kXcds - 1) / kXcds;
-  const int xcd = blockIdx.x % kXcds, per_xcd = gridDim.x / kXcds;
-  const int last = min(total, (xcd + 1) * chunk);
+  const int first_tile = from_tile + blockIdx.x / kXcds;
+  if (first_tile >= last_tile) return;
 
-  Reader<kTileM, kAMContig> ra;
-  Reader<kTileN, kBMContig> rb;
-  ra.start(wm, 2, lane);
-  rb.start(kDual ? 2 * wn : 4 * wn, 1, lane);
-  const uint32_t lds = (uint32_t)(uintptr_t)s_stage;
-
-  for (int tile = xcd * chunk + blockIdx.x / kXcds; tile < last; tile += per_xcd) {
-    // ---- expert, rows, first row and column of the tile.  Panels of eight m tiles, m fastest.
-    int e = 0, row0, count, mt = 0, mts;
-    int idx;
+  // expert, rows, first row and column of a tile: panels of eight m tiles, m fastest
+  auto tile_at = [&](int tile) {
+    int e = 0, idx, mts;
     if constexpr (kKind == kWeightBack) {
       e = tile / (m_tiles * NT);
       idx = tile - e * m_tiles * NT;
       mts = m_tiles;
     } else {
-      int lo = 0, hi = p.E;
       const int mtile = tile / NT;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_first[mid] <= mtile) lo = mid; else hi = mid;
-      }
-      e = lo;
-      idx = tile - s_first[e] * NT;
-      mts = s_first[e + 1] - s_first[e];
+      // the last expert whose first tile is not behind: the experts with a first tile up to it, less one
+      for (int base = 1; base <= p.E; base += 64)
+        e += __popcll(__ballot(base + lane <= p.E && s_first[min(base + lane, p.E)] <= mtile));
+      const int from = __builtin_amdgcn_readfirstlane(s_first[e]);
+      idx = tile - from * NT;
+      mts = __builtin_amdgcn_readfirstlane(s_first[e + 1]) - from;
     }
-    e = __builtin_amdgcn_readfirstlane(e);
-    idx = __builtin_amdgcn_readfirstlane(idx);
-    mts = __builtin_amdgcn_readfirstlane(mts);
-    expert_rows(p, e, row0, count);
-    row0 = __builtin_amdgcn_readfirstlane(row0);
+    Tile t;
+    int count;
+    t.e = __builtin_amdgcn_readfirstlane(e);
+    expert_rows(p, t.e, t.row0, count);
+    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
     count = __builtin_amdgcn_readfirstlane(count);
     const int panel = idx / (8 * NT), rest = idx - panel * 8 * NT;
     const int high = min(8, mts - panel * 8);
     const int nt = rest / high;
-    mt = panel * 8 + rest - nt * high;
-    const int m0 = mt * kTileM, n0 = nt * kCols;
-    const int K = kKind == kWeightBack ? count : p.K;
-    const int m_left = (kKind == kWeightBack ? p.M : count) - m0;
+    t.m0 = (panel * 8 + rest - nt * high) * kTileM;
+    t.n0 = nt * kCols;
+    t.K = kKind == kWeightBack ? count : p.K;
+    t.m_left = (kKind == kWeightBack ? p.M : count) - t.m0;
+    return t;
+  };
+  auto pairs_of = [](int K) { return K > 0 ? (K + 2 * kStepK - 1) / (2 * kStepK) : 1; };  // of steps
 
-    StageA sa;
-    StageB sb;
+  // ---- the cursor that stages
+  StageA sa;
+  StageB sb;
+  int ahead_tile = first_tile, ahead_steps = 0, ahead_slot = 0;
+  auto advance = [&] {  // to the next tile
+    if (ahead_tile >= last_tile) {
+      sa.stop();
+      sb.stop();
+      ahead_steps = 1 << 30;
+      return;
+    }
+    const Tile t = tile_at(ahead_tile);
+    ahead_tile += per_xcd;
+    const int lane = fresh_lane();
+    if (lane == 0) s_tile[wave][ahead_slot] = t;
+    ahead_slot = (ahead_slot + 1) % kAhead;
+    ahead_steps = 2 * pairs_of(t.K);
     if constexpr (kKind == kWeightBack) {
-      sa.start({p.a + ((int64_t)row0 * p.lda + m0) * 2, p.lda, m_left}, K, wave, lane);
-      sb.start({p.b + ((int64_t)row0 * p.ldb + n0) * 2, p.ldb, p.N - n0}, K, wave, lane);
+      sa.start({p.a + ((int64_t)t.row0 * p.lda + t.m0) * 2, p.lda, t.m_left}, t.K, wave, lane);
+      sb.start({p.b + ((int64_t)t.row0 * p.ldb + t.n0) * 2, p.ldb, p.N - t.n0}, t.K, wave, lane);
     } else {
-      sa.start({p.a + ((int64_t)row0 + m0) * p.lda * 2, p.lda, m_left}, K, wave, lane);
-      const char* b = p.b + e * p.b_expert;
+      sa.start({p.a + ((int64_t)t.row0 + t.m0) * p.lda * 2, p.lda, t.m_left}, t.K, wave, lane);
+      const char* b = p.b + t.e * p.b_expert;
       if constexpr (kDual) {
-        const OperandTile up{b + ((int64_t)p.N + n0) * p.ldb * 2, p.ldb, p.N - n0};
-        sb.start({b + (int64_t)n0 * p.ldb * 2, p.ldb, p.N - n0}, K, wave, lane, &up);
+        const OperandTile up{b + ((int64_t)p.N + t.n0) * p.ldb * 2, p.ldb, p.N - t.n0};
+        sb.start({b + (int64_t)t.n0 * p.ldb * 2, p.ldb, p.N - t.n0}, t.K, wave, lane, &up);
       } else if constexpr (kBMContig) {
-        sb.start({b + (int64_t)n0 * 2, p.ldb, p.N - n0}, K, wave, lane);
+        sb.start({b + (int64_t)t.n0 * 2, p.ldb, p.N - t.n0}, t.K, wave, lane);
       } else {
-        sb.start({b + (int64_t)n0 * p.ldb * 2, p.ldb, p.N - n0}, K, wave, lane);
+        sb.start({b + (int64_t)t.n0 * p.ldb * 2, p.ldb, p.N - t.n0}, t.K, wave, lane);
       }
     }
+  };
+  const uint32_t lds = (uint32_t)(uintptr_t)s_stage;
+  int stage = 0;  // of the step that is multiplied: the step that is staged goes there, kDepth further
+  auto issue = [&](int at) {
+    sa.issue(lds + at * kStage, wave);
+    sb.issue(lds + at * kStage + StageA::kBytes, wave);
+    --ahead_steps;
+  };
+
+  Reader<kTileM, kAMContig, 2> ra;
+  Reader<kTileN, kBMContig, 1> rb;
+  ra.start(wm, lane);
+  rb.start(kDual ? 2 * wn : 4 * wn, lane);
+
+  for (int i = 0; i < kDepth; ++i) {
+    if (ahead_steps == 0) advance();
+    issue(i);
+  }
+  stage_barrier<(kDepth - 1) * kIssues>();
+
+  int slot = 0;
+  for (int tile = first_tile; tile < last_tile; tile += per_xcd) {
+    Tile t = s_tile[wave][slot];
+    t.e = __builtin_amdgcn_readfirstlane(t.e);
+    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+    t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
+    t.n0 = __builtin_amdgcn_readfirstlane(t.n0);
+    t.m_left = __builtin_amdgcn_readfirstlane(t.m_left);
+    t.K = __builtin_amdgcn_readfirstlane(t.K);
+    slot = (slot + 1) % kAhead;
 
     f32x4_t acc[kMI][kNI];
 #pragma unroll
@@ -182,37 +289,59 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
       for (int j = 0; j < kNI; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    const int steps = (K + kStepK - 1) / kStepK;
-    stage_barrier();  // the previous tile's stages are read
-    if (steps > 0) {
-      sa.issue(0, lds, wave);
-      sb.issue(0, lds + StageA::kBytes, wave);
-    }
     // blocks of 16 rows that this wavefront has at all
-    const int blocks = min(kMI, (min((m_left + 15) / 16, 2 * kMI) - wm + 1) / 2);
+    const int blocks = (min((t.m_left + 15) / 16, 2 * kMI) - wm + 1) / 2;
     auto run = [&](auto count_c) {
       constexpr int kCount = decltype(count_c)::value;
-      for (int step = 0; step < steps; ++step) {
-        stage_barrier();
-        const uint32_t other = lds + ((step + 1) & 1) * kStage;
-        if (step + 1 < steps) {
-          sa.issue((step + 1) * kStepK, other, wave);
-          sb.issue((step + 1) * kStepK, other + StageA::kBytes, wave);
+      u32x4_t fa[2][kCount], fb[2][kNI];
+      auto read = [&](int which, int at, int i) {  // the i-th of kNI + kCount operands
+        const uint32_t st = lds + at * kStage;
+        if (i < kNI)
+          fb[which][i] = rb.get(st + StageA::kBytes, kDual ? (i & 1) + 8 * (i >> 1) : i);
+        else
+          fa[which][i - kNI] = ra.get(st, i - kNI);
+      };
+      // One step: groups of four products, in their gaps the reads of the next step's operands and,
+      // last, the DMA into this step's stage.  The order is pinned: left to itself the compiler
+      // moves the products behind the barrier, where they wait for the reads of the step after.
+      auto step = [&](int which) {
+        constexpr int kReads = kNI + kCount, kPerGap = kCount > 4 ? 2 : (kReads + 1) / 2;
+        const int here = stage;
+        stage = stage + 1 == kDepth ? 0 : stage + 1;
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) {
+#pragma unroll
+          for (int j = 0; j < kNI; ++j) acc[i][j] = mfma16<S>(fb[which][j], fa[which][i], acc[i][j]);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int r = i * kPerGap; r < (i + 1) * kPerGap && r < kReads; ++r) read(1 - which, stage, r);
+          if (i == kCount - 2) sa.issue(lds + here * kStage, wave);
+          if (i == kCount - 1) sb.issue(lds + here * kStage + StageA::kBytes, wave);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        const char* st = s_stage + (step & 1) * kStage;
+        --ahead_steps;
+      };
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          u32x4_t fa[kCount], fb[kNI];
-#pragma unroll
-          for (int j = 0; j < kNI; ++j)
-            fb[j] = rb.template get<1>(st + StageA::kBytes, kDual ? (j & 1) + 8 * (j >> 1) : j, s);
-#pragma unroll
-          for (int i = 0; i < kCount; ++i) fa[i] = ra.template get<2>(st, kAMContig ? i : 2 * i, s);
-#pragma unroll
-          for (int i = 0; i < kCount; ++i)
-#pragma unroll
-            for (int j = 0; j < kNI; ++j) acc[i][j] = mfma16<S>(fb[j], fa[i], acc[i][j]);
-        }
+      for (int r = 0; r < kNI + kCount; ++r) read(0, stage, r);
+      bool behind = tile != first_tile;  // the last tile's stores may still be in flight
+      for (int pair = pairs_of(t.K); pair > 0; --pair) {
+        // At the barrier of a step the next one has landed, and every wavefront has read this one.
+        // (The last step of a tile reads the next tile's first, which that tile reads again.)
+        // The steps that a tile's first two wait for were staged before the last tile's stores.
+        if (ahead_steps == 0) advance();
+        if (behind)
+          stage_barrier<kPending + kStores>();
+        else
+          stage_barrier<kPending>();
+        __builtin_amdgcn_sched_barrier(0);
+        step(0);
+        if (behind)
+          stage_barrier<kPending + kStores>();
+        else
+          stage_barrier<kPending>();
+        __builtin_amdgcn_sched_barrier(0);
+        step(1);
+        behind = false;
       }
     };
     if (blocks > kMI / 2)
@@ -220,52 +349,71 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2,
     else
       run(std::integral_constant<int, kMI / 2>{});
 
-    // ---- epilogue: eight consecutive columns of a row per lane and pair of blocks
+    // ---- epilogue: eight consecutive columns of a row per lane and pair of blocks; all lanes
+    // execute all loads and stores, those outside at kOutside
     DropKey key{};
     const bool drops = (kKind == kGateUp || kKind == kGateBack) && p.drop.threshold;
     if (drops) key = drop_key(p.drop);
+    const int64_t row0 = kKind == kWeightBack ? (int64_t)t.e * p.M + t.m0 : (int64_t)t.row0 + t.m0;
+    const __amdgpu_buffer_rsrc_t out = open_resource(p.out + (row0 * p.ldo + t.n0) * 2);
+    const int here = fresh_lane();
+    const int col0 = (kDual ? 32 : 64) * wn + eight_column(here);  // within the tile
+    auto row_of = [&](int i) { return 16 * (2 * i + wm) + (here & 15); };
+    auto offset_of = [&](int row, int col, int ld) {
+      return row < t.m_left && t.n0 + col < p.N ? ((uint32_t)row * (uint32_t)ld + (uint32_t)col) * 2u : kOutside;
+    };
+    if constexpr (kKind == kGateUp) {
+      const __amdgpu_buffer_rsrc_t gate = open_resource(p.gu + (row0 * p.ldgu + t.n0) * 2);
+      const __amdgpu_buffer_rsrc_t up = open_resource(p.gu + (row0 * p.ldgu + p.N + t.n0) * 2);
 #pragma unroll
-    for (int i = 0; i < kMI; ++i) {
-      const int m = m0 + 16 * (2 * i + wm) + (lane & 15);
-      const bool inside = m - m0 < m_left;
-      const int64_t row = kKind == kWeightBack ? m : (int64_t)row0 + m;
-      if constexpr (kKind == kGateUp) {
-        const int col = n0 + 32 * wn + eight_column(lane);
+      for (int i = 0; i < kMI; ++i) {
+        const int row = row_of(i);
         float g[8], u[8];
         eight_columns(acc[i][0], acc[i][1], g);
         eight_columns(acc[i][2], acc[i][3], u);
-        if (!inside || col >= p.N) continue;
         if (p.gu) {
-          char* at = p.gu + (row * p.ldgu + col) * 2;
-          *reinterpret_cast<u32x4_t*>(at) = pack8<S>(g);
-          *reinterpret_cast<u32x4_t*>(at + (int64_t)p.N * 2) = pack8<S>(u);
+          const uint32_t at = offset_of(row, col0, p.ldgu);
+          store16(pack8<S>(g), gate, at);
+          store16(pack8<S>(u), up, at);
         }
         u32x4_t n{};
-        if (drops) n = drop_numbers(key, p.drop.site, (uint32_t)row, (uint32_t)col >> 3);
+        if (drops) n = drop_numbers(key, p.drop.site, (uint32_t)(row0 + row), (uint32_t)(t.n0 + col0) >> 3);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           float slope;
           g[c] = activate(p.activation, g[c], slope) * u[c];
           if (drops) g[c] = drop_keeps(n, c, p.drop.threshold) ? g[c] * p.drop.scale : 0.f;
         }
-        *reinterpret_cast<u32x4_t*>(p.out + (row * p.ldo + col) * 2) = pack8<S>(g);
-      } else {
+        store16(pack8<S>(g), out, offset_of(row, col0, p.ldo));
+      }
+    } else if constexpr (kKind == kGateBack) {
+      // g and u of two row blocks are requested at once, before the first is used
+      constexpr int kAtOnce = 2;
+      const __amdgpu_buffer_rsrc_t gate = open_resource(p.gu + (row0 * p.ldgu + t.n0) * 2);
+      const __amdgpu_buffer_rsrc_t up = open_resource(p.gu + (row0 * p.ldgu + p.N + t.n0) * 2);
+      const __amdgpu_buffer_rsrc_t out_up = open_resource(p.out + (row0 * p.ldo + p.N + t.n0) * 2);
 #pragma unroll
-        for (int j = 0; j < kNI; j += 2) {
-          const int col = n0 + 64 * wn + 16 * j + eight_column(lane);
-          float v[8];
-          eight_columns(acc[i][j], acc[i][j + 1], v);
-          if (!inside || col >= p.N) continue;
-          if constexpr (kKind == kGateBack) {
-            const char* at = p.gu + (row * p.ldgu + col) * 2;
-            Raw<S> rg, ru;
-            rg.w[0] = *reinterpret_cast<const u32x4_t*>(at);
-            ru.w[0] = *reinterpret_cast<const u32x4_t*>(at + (int64_t)p.N * 2);
-            float g[8], u[8];
-            unpack(rg, g);
-            unpack(ru, u);
+      for (int i0 = 0; i0 < kMI; i0 += kAtOnce) {
+        Raw<S> rg[kAtOnce][2], ru[kAtOnce][2];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t at = offset_of(row_of(i0 + i), col0 + 32 * j, p.ldgu);
+            rg[i][j].w[0] = load16(gate, at);
+            ru[i][j].w[0] = load16(up, at);
+          }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int row = row_of(i0 + i), col = col0 + 32 * j;
+            float v[8], g[8], u[8];
+            eight_columns(acc[i0 + i][2 * j], acc[i0 + i][2 * j + 1], v);
+            unpack(rg[i][j], g);
+            unpack(ru[i][j], u);
             u32x4_t n{};
-            if (drops) n = drop_numbers(key, p.drop.site, (uint32_t)row, (uint32_t)col >> 3);
+            if (drops) n = drop_numbers(key, p.drop.site, (uint32_t)(row0 + row), (uint32_t)(t.n0 + col) >> 3);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               if (drops) v[c] = drop_keeps(n, c, p.drop.threshold) ? v[c] * p.drop.scale : 0.f;
@@ -274,24 +422,30 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2,
               g[c] = v[c] * u[c] * slope;
               u[c] = v[c] * act;
             }
-            char* to = p.out + (row * p.ldo + col) * 2;
-            *reinterpret_cast<u32x4_t*>(to) = pack8<S>(g);
-            *reinterpret_cast<u32x4_t*>(to + (int64_t)p.N * 2) = pack8<S>(u);
-          } else {
-            char* to = p.out + (kKind == kWeightBack ? (int64_t)e * p.M * p.N * 2 : 0) + (row * p.ldo + col) * 2;
-            *reinterpret_cast<u32x4_t*>(to) = pack8<S>(v);
+            const uint32_t to = offset_of(row, col, p.ldo);
+            store16(pack8<S>(g), out, to);
+            store16(pack8<S>(u), out_up, to);
           }
-        }
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kMI; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v[8];
+          eight_columns(acc[i][2 * j], acc[i][2 * j + 1], v);
+          store16(pack8<S>(v), out, offset_of(row_of(i), col0 + 32 * j, p.ldo));
+        }
     }
   }
+  stage_barrier<0>();  // no DMA outlives the workgroup's LDS
 }
 
 // Tiles of 256 rows where the experts' rows fill them, else of 128.
 template <int kKind>
 static void launch_product(const ProductDev& p, int dtype, hipStream_t s) {
   const int64_t cols = kKind == kGateUp ? kTileN / 2 : kTileN;
-  const bool big = kKind == kWeightBack ? p.M > 128 : (int64_t)p.R >= (int64_t)p.E * 1024;
+  const bool big = kKind == kWeightBack ? p.M > 128 : (int64_t)p.R >= (int64_t)p.E * 192;
   const int64_t tm = big ? 256 : 128;
   const int64_t m_tiles = kKind == kWeightBack ? p.E * ceil_div(p.M, tm) : p.R / tm + std::min(p.E, p.R);
   const int64_t tiles = m_tiles * ceil_div(p.N, cols);

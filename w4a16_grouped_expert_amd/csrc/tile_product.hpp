@@ -1,12 +1,13 @@
 // Products of 16-bit matrices on the matrix cores, C[m][n] = sum_k A(m, k) B(n, k) with
 // float32 sums, tiled for one workgroup of eight wavefronts: 128 or 256 m by 256 n.
 //
-// Either operand may have its k or its m (n) contiguous in memory.  A K step of 64 is staged in
-// LDS by DMA (buffer_load ... lds, no registers), two steps deep: while one is multiplied the
-// next one lands.
-//  - k contiguous: rows of 64 k, 128 bytes; 16-byte chunk c of row r at slot c ^ (r & 7), so
-//    that the eight lanes of a phase of ds_read_b128 hit eight different chunks.
-//  - m contiguous: rows of one k; 32-byte pair p of row k at slot p ^ (k & 3 | (k >> 1) & 4).
+// Either operand may have its k or its m (n) contiguous in memory.  Steps of 32 k are staged
+// in a ring in LDS by DMA (buffer_load ... lds, no registers), several steps ahead and across
+// the tiles of a workgroup: the first steps of a tile land while the tile before it is stored.
+// Each wavefront reads a step's operands into registers while it multiplies the step before.
+//  - k contiguous: rows of 32 k, 64 bytes; 16-byte chunk c of row r at slot c ^ row_swizzle(r),
+//    so that the lanes of a phase of ds_read_b128 hit different banks.
+//  - m contiguous: rows of one k; 32-byte pair p of row k at slot p ^ pair_swizzle(k).
 //    ds_read_b64_tr_b16 reads four k by 16 m per 16 lanes and hands each lane the four k of its
 //    m, which is half of an MFMA operand; the rows of one instruction hit different pairs.
 // Bounds are the buffer resource's: what lies past a tensor, an expert's rows or the K range
@@ -19,7 +20,7 @@
 namespace moe {
 
 constexpr int kTileN = 256;       // n per workgroup
-constexpr int kStepK = 64;        // k per stage
+constexpr int kStepK = 32;        // k per stage
 constexpr int kTileWaves = 8;     // 2 in m (rows of 16 in turn) x 4 in n (64 each)
 constexpr int kTileThreads = 64 * kTileWaves;
 constexpr int kNI = 4;            // 16-column blocks of a wavefront
@@ -40,16 +41,34 @@ __device__ __forceinline__ f32x4_t mfma16(const u32x4_t& a, const u32x4_t& b, f3
 
 // 16 bytes per lane from a buffer resource to LDS at lds + 16 lane.  The compiler neither
 // counts these loads nor knows what they write: every reader waits for them itself
-// (stage_barrier below).
+// (stage_barrier below).  (M0 is left as it is: no other instruction here reads it.)
 __device__ __forceinline__ void dma16(const i32x4_t& rsrc, uint32_t offset, uint32_t lds) {
-  uint32_t saved;
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds\n\ts_mov_b32 m0, %0"
-               : "=&s"(saved) : "v"(offset), "s"(rsrc), "s"(lds) : "memory");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :: "v"(offset), "s"(rsrc), "s"(lds) : "memory");
 }
-// This wavefront's DMA has landed and its LDS reads are done; then the workgroup's.
+// At most kPending of this wavefront's vector memory operations are in flight (they end in
+// order) and its LDS reads are done; then the workgroup meets.
+template <int kPending>
 __device__ __forceinline__ void stage_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kPending) : "memory");
 }
+// Loads and stores of an epilogue through a resource of 2^31 - 1 bytes: kOutside reads zero
+// and stores nothing, so that every lane executes every one of them.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t open_resource(const void* base) {
+  const uint64_t a = (uint64_t)(uintptr_t)base;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo), 0, 0x7FFFFFFF,
+                                           kBufferRsrcWord3);
+}
+template <int kPolicy = 0>
+__device__ __forceinline__ void store16(const u32x4_t& v, __amdgpu_buffer_rsrc_t r, uint32_t offset) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, offset, 0, kPolicy);
+}
+__device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t offset) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0);
+}
+__device__ __forceinline__ int row_swizzle(int r) { return ((r >> 3) & 1) | ((((r >> 2) ^ (r >> 3)) & 1) << 1); }
+__device__ __forceinline__ int pair_swizzle(int k) { return (k & 3) | ((k >> 1) & 4); }
 __device__ __forceinline__ i32x4_t resource(const void* base, uint32_t bytes) {
   const uint64_t a = (uint64_t)(uintptr_t)base;
   return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
@@ -64,20 +83,23 @@ struct OperandTile {
   int rows;          // m that are there from m0 on (at least 1)
 };
 
-// The staging of one operand of kX m (a multiple of 128) by the wavefronts of a workgroup.
+// The staging of one operand of kX m (128 or 256) by the wavefronts of a workgroup, one step
+// after the other.
 // kDual: two tensors of kX / 2 rows each, one behind the other in the stage (k contiguous).
 template <int kX, bool kMContig, bool kDual = false>
 struct Stager {
   static constexpr int kBytes = kX * kStepK * 2;
   static constexpr int kIssues = kBytes / 1024 / kTileWaves;  // DMA instructions per wavefront and step
+  static constexpr int kChunks = kX / 8;                      // m contiguous: 16-byte chunks of a row,
+  static constexpr int kRows = 64 / kChunks;                  // rows of k per instruction
   static_assert(!(kMContig && kDual), "two tensors lie one behind the other with k contiguous only");
-  const char* base;
+  static_assert(kIssues <= 2, "");
+  const char* base;  // m contiguous: moves on with the steps
   int ld2;           // bytes between rows
-  int rows;
-  int K;
-  uint32_t off[2];   // this lane's offset; m contiguous: of even and odd instructions
-  int kc8;           // k contiguous: first k of this lane's chunk
-  uint32_t bytes;    // k contiguous: size of the resource
+  int left;          // k from the next step on
+  uint32_t edge;     // k contiguous: size of the resource; m contiguous: bytes of a row
+  uint32_t off[2];   // this lane's offset in the next step; m contiguous: of both instructions
+  int kc8;           // k contiguous: first k of this lane's chunk within a step
 
   // t: the operand's tile; for kDual t2 is the second tensor's
   __device__ __forceinline__ void start(const OperandTile& t, int k_total, int wave, int lane,
@@ -85,71 +107,66 @@ struct Stager {
     const OperandTile& mine = kDual && wave >= kTileWaves / 2 ? *t2 : t;
     base = mine.base;
     ld2 = mine.ld * 2;
-    rows = mine.rows;
-    K = k_total;
+    left = k_total;
     if constexpr (!kMContig) {
-      // instruction j of a wavefront fills rows 8 (wave kIssues + j) .. + 7: lane l the slot l & 7 of row l >> 3
-      const int first = 8 * kIssues * (kDual ? wave & (kTileWaves / 2 - 1) : wave) + (lane >> 3);
-      kc8 = 8 * ((lane & 7) ^ (lane >> 3));
+      // instruction j of a wavefront fills 16 rows from 16 (wave kIssues + j): lane l the slot l & 3 of row l >> 2
+      const int first = 16 * kIssues * (kDual ? wave & (kTileWaves / 2 - 1) : wave) + (lane >> 2);
+      kc8 = 8 * ((lane & 3) ^ row_swizzle(lane >> 2));
       off[0] = (uint32_t)first * (uint32_t)ld2 + 2u * kc8;
-      const int there = rows < (kDual ? kX / 2 : kX) ? rows : (kDual ? kX / 2 : kX);
-      bytes = (uint32_t)(there - 1) * (uint32_t)ld2 + 2u * K;
+      edge = (uint32_t)(min(mine.rows, kDual ? kX / 2 : kX) - 1) * (uint32_t)ld2 + 2u * k_total;
     } else {
-      constexpr int kChunks = kX / 8, kRows = 64 / kChunks;  // 16-byte chunks per row, rows per instruction
       const int pos = lane & (kChunks - 1);
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
+      for (int v = 0; v < kIssues; ++v) {
         const int k = (wave * kIssues + v) * kRows + lane / kChunks;
-        const int s = (k & 3) | ((k >> 1) & 4);
-        off[v] = (uint32_t)k * (uint32_t)ld2 + 16u * (pos ^ (2 * s));
+        off[v] = (uint32_t)k * (uint32_t)ld2 + 16u * (pos ^ (2 * pair_swizzle(k)));
       }
+      edge = 2u * mine.rows;
     }
   }
-  // stage the step that starts at k0 (a multiple of kStepK below K)
-  __device__ __forceinline__ void issue(int k0, uint32_t lds, int wave) const {
+  // nothing more to stage: the steps from here on are zeros
+  __device__ __forceinline__ void stop() { left = 0; }
+  // stage the next step
+  __device__ __forceinline__ void issue(uint32_t lds, int wave) {
     const uint32_t to = lds + wave * kIssues * 1024;
     if constexpr (!kMContig) {
-      const i32x4_t r = resource(base, bytes);
-      const uint32_t from = k0 + kc8 < K ? off[0] + 2u * k0 : kOutside;
+      const i32x4_t r = resource(base, edge);
+      const uint32_t from = kc8 < left ? off[0] : kOutside;
 #pragma unroll
-      for (int j = 0; j < kIssues; ++j) dma16(r, from + (uint32_t)(8 * j * ld2), to + 1024 * j);
+      for (int j = 0; j < kIssues; ++j) dma16(r, from + (uint32_t)(16 * j * ld2), to + 1024 * j);
+      off[0] += 2 * kStepK;
     } else {
-      constexpr int kRows = 64 / (kX / 8);
-      static_assert(kIssues * kRows == 8, "the k of a wavefront's instructions: 8 wave .. + 7");
-      const int left = K - k0 < kStepK ? K - k0 : kStepK;
-      const i32x4_t r = resource(base + (int64_t)k0 * ld2, (uint32_t)(left - 1) * (uint32_t)ld2 + 2u * rows);
+      const i32x4_t r = resource(base, left > 0 ? (uint32_t)(min(left, kStepK) - 1) * (uint32_t)ld2 + edge : 0u);
 #pragma unroll
-      for (int j = 0; j < kIssues; ++j) dma16(r, off[j & 1] + (uint32_t)((j & ~1) * kRows * ld2), to + 1024 * j);
+      for (int j = 0; j < kIssues; ++j) dma16(r, off[j], to + 1024 * j);
+      base += (int64_t)kStepK * ld2;
     }
+    left -= kStepK;
   }
 };
 
-// This lane's MFMA operands of a staged operand: 16-m block b (of the kX / 16), k 32 s .. + 31.
-template <int kX, bool kMContig>
+// This lane's MFMA operands of a staged operand.  kStride: 16-m blocks between two of the
+// wavefront's, 1 (from a multiple of 4 on) or 2 (from 0 or 1 on).
+template <int kX, bool kMContig, int kStride>
 struct Reader {
-  uint32_t at[kMContig ? 4 : 2];
-  // first: the lane's first block; blocks follow at a step of kStride blocks
-  __device__ __forceinline__ void start(int first, int stride, int lane) {
+  uint32_t at;
+  __device__ __forceinline__ void start(int first, int lane) {
     const int i = lane & 15, q = lane >> 4;
     if constexpr (!kMContig) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) at[s] = (uint32_t)((first * 16 + i) * 128 + 16 * ((4 * s + q) ^ (i & 7)));
+      at = (uint32_t)((first * 16 + i) * 64 + 16 * (q ^ row_swizzle(i)));
     } else {
-      const int k = 8 * q + (i >> 2), s = (k & 3) | ((k >> 1) & 4);
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        at[v] = (uint32_t)(k * kX * 2 + 32 * ((first + v * stride) ^ s) + 8 * (i & 3));
+      const int k = 8 * q + (i >> 2);
+      at = (uint32_t)(k * kX * 2 + 32 * (first ^ pair_swizzle(k)) + 8 * (i & 3));
     }
   }
-  // k contiguous: the block `blocks` behind the lane's first one; m contiguous: the lane's
-  // block number `blocks`, with kStride blocks between two (1: of four, 2: of eight).  s: half of the step.
-  template <int kStride>
-  __device__ __forceinline__ u32x4_t get(const char* stage, int blocks, int s) const {
+  // block b (a constant) of the operand staged at `stage` in LDS.  k contiguous: any block; m
+  // contiguous: b < 4, or 8 with a stride of 2.  There the pair of block b is that of block 0 with
+  // bits of b changed (the swizzle and the stage's address leave them alone).
+  __device__ __forceinline__ u32x4_t get(uint32_t stage, int b) const {
     if constexpr (!kMContig) {
-      return *reinterpret_cast<const u32x4_t*>(stage + at[s] + blocks * 2048);
+      return *(const MOE_LDS u32x4_t*)(stage + at + b * kStride * 1024);
     } else {
-      // (blocks 4 and up lie eight pairs behind 0 to 3)
-      const char* p = stage + at[blocks & 3] + (blocks >> 2) * 256 + s * (32 * kX * 2);
+      const uint32_t p = ((stage + at) ^ ((b & 3) * kStride * 32)) + (b >> 2) * 256;
       typedef MOE_LDS s16x4_t* lds_ptr;
       const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p)));
       const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * kX * 2)));
