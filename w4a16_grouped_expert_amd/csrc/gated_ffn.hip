@@ -72,9 +72,6 @@ __device__ __forceinline__ u32x4_t pack8(const float (&v)[8]) {
   return pack<S>(v).w[0];
 }
 
-// Stages of a workgroup: as many as fit beside the table of the experts' first tiles.
-constexpr int product_depth(int mi) { return mi == 8 ? 4 : 6; }
-
 // The lane's number as a value that the compiler does not see through: what follows from it is
 // computed where it is used, in place of registers held through the products.
 __device__ __forceinline__ int fresh_lane() {
@@ -88,52 +85,66 @@ struct Tile {
   int e, row0, m0, n0, m_left, K;
 };
 
-// Persistent workgroups, each with its tiles in turn.  All loads are issued kDepth steps ahead of
-// the products by a cursor of its own, which runs into the next tile while this one ends.
-template <typename S, int kKind, int kMI>
-__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_product(ProductDev p) {
-  constexpr int kTileM = kMI * 32;
+// Persistent workgroups, each with its tiles in turn.  All loads are issued kUnits - 1 units ahead
+// of the products by a cursor of its own, which runs into the next tiles while this one ends.
+//
+// Tile shapes: rows of a tile, by wavefronts in m and blocks of 16 rows and columns of each.
+struct Shape256 {
+  static constexpr int kWM = 2, kMI = 8, kNI = 4, kUnits = 2;
+};
+struct Shape128 {
+  static constexpr int kWM = 2, kMI = 4, kNI = 4, kUnits = 3;
+};
+struct Shape64 {
+  static constexpr int kWM = 2, kMI = 2, kNI = 4, kUnits = 3;
+};
+
+template <typename S, int kKind, typename Shape>
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_product(ProductDev p) {
+  constexpr int kWM = Shape::kWM, kMI = Shape::kMI, kNI = Shape::kNI, kUnits = Shape::kUnits;
+  constexpr int kTileM = kWM * kMI * 16;
+  static_assert(kWaves / kWM * kNI * 16 == kTileN, "");
   constexpr bool kDual = kKind == kGateUp;
   constexpr bool kAMContig = kKind == kWeightBack;
   constexpr bool kBMContig = kKind >= kGateBack;
   constexpr int kCols = kDual ? kTileN / 2 : kTileN;
-  constexpr int kDepth = product_depth(kMI);
+  constexpr int kHalf = kDual ? kNI / 2 : kNI;  // blocks of a wavefront within a tensor
   typedef Stager<kTileM, kAMContig> StageA;
   typedef Stager<kTileN, kBMContig, kDual> StageB;
   constexpr int kStage = StageA::kBytes + StageB::kBytes;
   constexpr int kIssues = StageA::kIssues + StageB::kIssues;
-  constexpr int kPending = (kDepth - 2) * kIssues;
-  constexpr int kAhead = 4;  // tiles that the cursor may be ahead, and one
+  constexpr int kPending = (kUnits - 2) * kIssues;
+  constexpr int kAhead = kUnits + 1;  // the tiles that the cursor may be ahead, and this one
   // stores of a tile's epilogue per wavefront (without those of g and u, which may be missing)
-  constexpr int kStores = kKind == kGateUp ? kMI : kKind == kGateBack ? 4 * kMI : 2 * kMI;
+  constexpr int kPairs = kNI / 2;  // pairs of column blocks
+  constexpr int kStores = (kKind == kGateUp ? 1 : kKind == kGateBack ? 2 * kPairs : kPairs) * kMI;
   static_assert(kPending + kStores < 64, "the counter's six bits");
-  static_assert(kDepth % 2 == 0 && kDepth / 2 < kAhead, "a tile has two steps at least");
-  __shared__ __attribute__((aligned(1024))) char s_stage[kDepth * kStage];
+  __shared__ __attribute__((aligned(1024))) char s_stage[kUnits * kStage];
   __shared__ int s_first[kKind == kWeightBack ? 1 : MOE_MAX_EXPERTS + 1];  // first m tile of each expert
-  __shared__ Tile s_tile[kTileWaves][kAhead];  // each wavefront's own copy of the tiles ahead
+  __shared__ Tile s_tile[kWaves][kAhead];  // each wavefront's own copy of the tiles ahead
 
   const int tid = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
+  const int wm = wave % kWM, wn = wave / kWM;
   const int NT = (p.N + kCols - 1) / kCols;
 
   // ---- the tiles: m tiles of each expert, one expert behind the other.  Each XCD takes a
   // contiguous run of them, so that those that share operands meet in its L2, of an equal share of
-  // the work: for the weights' gradients, whose experts have unequal K, steps and the store.
+  // the work: for the weights' gradients, whose experts have unequal K, units and the store.
   int m_tiles;
   const int xcd = blockIdx.x % kXcds, per_xcd = gridDim.x / kXcds;
   int from_tile, last_tile;
   if constexpr (kKind == kWeightBack) {
     m_tiles = (p.M + kTileM - 1) / kTileM;
     const int per_expert = m_tiles * NT;
-    // (a tile's store costs about as much as kStoreSteps steps)
-    constexpr int kStoreSteps = 8;
+    // (a tile's store costs about as much as kStoreUnits units)
+    constexpr int kStoreUnits = 4;
     auto cost_of = [&](int e) {
       int row0, count = 0;
       if (e < p.E) expert_rows(p, e, row0, count);
-      return e < p.E ? (count + kStepK - 1) / kStepK + kStoreSteps : 0;
+      return e < p.E ? (count + kUnitK - 1) / kUnitK + kStoreUnits : 0;
     };
-    int whole = 0;  // cost of one tile of every expert: below 2^24 / 32 + 9 E
+    int whole = 0;  // cost of one tile of every expert: below 2^24 / 64 + 5 E
     for (int base = 0; base < p.E; base += 64) whole += cost_of(base + lane);
     for (int off = 32; off; off >>= 1) whole += __shfl_xor(whole, off);
     whole = __builtin_amdgcn_readfirstlane(whole);
@@ -191,11 +202,11 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2,
   auto tile_at = [&](int tile) {
     int e = 0, idx, mts;
     if constexpr (kKind == kWeightBack) {
-      e = tile / (m_tiles * NT);
+      e = __builtin_amdgcn_readfirstlane(tile / (m_tiles * NT));
       idx = tile - e * m_tiles * NT;
       mts = m_tiles;
     } else {
-      const int mtile = tile / NT;
+      const int mtile = __builtin_amdgcn_readfirstlane(tile / NT);
       // the last expert whose first tile is not behind: the experts with a first tile up to it, less one
       for (int base = 1; base <= p.E; base += 64)
         e += __popcll(__ballot(base + lane <= p.E && s_first[min(base + lane, p.E)] <= mtile));
@@ -209,34 +220,35 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2,
     expert_rows(p, t.e, t.row0, count);
     t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
     count = __builtin_amdgcn_readfirstlane(count);
-    const int panel = idx / (8 * NT), rest = idx - panel * 8 * NT;
+    // (divisions come out in vector registers, uniform or not)
+    const int panel = __builtin_amdgcn_readfirstlane(idx / (8 * NT)), rest = idx - panel * 8 * NT;
     const int high = min(8, mts - panel * 8);
-    const int nt = rest / high;
+    const int nt = __builtin_amdgcn_readfirstlane(rest / high);
     t.m0 = (panel * 8 + rest - nt * high) * kTileM;
     t.n0 = nt * kCols;
     t.K = kKind == kWeightBack ? count : p.K;
     t.m_left = (kKind == kWeightBack ? p.M : count) - t.m0;
     return t;
   };
-  auto pairs_of = [](int K) { return K > 0 ? (K + 2 * kStepK - 1) / (2 * kStepK) : 1; };  // of steps
+  auto units_of = [](int K) { return K > 0 ? (K + kUnitK - 1) / kUnitK : 1; };
 
   // ---- the cursor that stages
   StageA sa;
   StageB sb;
-  int ahead_tile = first_tile, ahead_steps = 0, ahead_slot = 0;
+  int ahead_tile = first_tile, ahead_units = 0, ahead_slot = 0;
   auto advance = [&] {  // to the next tile
     if (ahead_tile >= last_tile) {
       sa.stop();
       sb.stop();
-      ahead_steps = 1 << 30;
+      ahead_units = 1 << 30;
       return;
     }
     const Tile t = tile_at(ahead_tile);
     ahead_tile += per_xcd;
     const int lane = fresh_lane();
     if (lane == 0) s_tile[wave][ahead_slot] = t;
-    ahead_slot = (ahead_slot + 1) % kAhead;
-    ahead_steps = 2 * pairs_of(t.K);
+    ahead_slot = ahead_slot + 1 == kAhead ? 0 : ahead_slot + 1;
+    ahead_units = units_of(t.K);
     if constexpr (kKind == kWeightBack) {
       sa.start({p.a + ((int64_t)t.row0 * p.lda + t.m0) * 2, p.lda, t.m_left}, t.K, wave, lane);
       sb.start({p.b + ((int64_t)t.row0 * p.ldb + t.n0) * 2, p.ldb, p.N - t.n0}, t.K, wave, lane);
@@ -254,23 +266,27 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2,
     }
   };
   const uint32_t lds = (uint32_t)(uintptr_t)s_stage;
-  int stage = 0;  // of the step that is multiplied: the step that is staged goes there, kDepth further
-  auto issue = [&](int at) {
-    sa.issue(lds + at * kStage, wave);
-    sb.issue(lds + at * kStage + StageA::kBytes, wave);
-    --ahead_steps;
+  int stage = 0;  // of the unit that is multiplied: the unit kUnits further goes there
+  auto issue = [&](int j, int at) {  // the j-th of a unit's DMA instructions
+    if (j < StageA::kIssues)
+      sa.issue(j, lds + at * kStage, wave);
+    else
+      sb.issue(j - StageA::kIssues, lds + at * kStage + StageA::kBytes, wave);
+    if (j + 1 == kIssues) --ahead_units;
   };
 
-  Reader<kTileM, kAMContig, 2> ra;
+  const int wave_cols = kHalf * 16 * wn;  // this wavefront's first column within the tile
+  Reader<kTileM, kAMContig, kWM> ra;
   Reader<kTileN, kBMContig, 1> rb;
   ra.start(wm, lane);
-  rb.start(kDual ? 2 * wn : 4 * wn, lane);
+  rb.start(kHalf * wn, lane);
 
-  for (int i = 0; i < kDepth; ++i) {
-    if (ahead_steps == 0) advance();
-    issue(i);
+  for (int i = 0; i < kUnits; ++i) {
+    if (ahead_units == 0) advance();
+#pragma unroll
+    for (int j = 0; j < kIssues; ++j) issue(j, i);
   }
-  stage_barrier<(kDepth - 1) * kIssues>();
+  stage_barrier<(kUnits - 1) * kIssues>();
 
   int slot = 0;
   for (int tile = first_tile; tile < last_tile; tile += per_xcd) {
@@ -281,7 +297,7 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2,
     t.n0 = __builtin_amdgcn_readfirstlane(t.n0);
     t.m_left = __builtin_amdgcn_readfirstlane(t.m_left);
     t.K = __builtin_amdgcn_readfirstlane(t.K);
-    slot = (slot + 1) % kAhead;
+    slot = slot + 1 == kAhead ? 0 : slot + 1;
 
     f32x4_t acc[kMI][kNI];
 #pragma unroll
@@ -290,64 +306,72 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2,
       for (int j = 0; j < kNI; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
     // blocks of 16 rows that this wavefront has at all
-    const int blocks = (min((t.m_left + 15) / 16, 2 * kMI) - wm + 1) / 2;
+    const int blocks = (min((t.m_left + 15) / 16, kWM * kMI) - wm + kWM - 1) / kWM;
     auto run = [&](auto count_c) {
       constexpr int kCount = decltype(count_c)::value;
       u32x4_t fa[2][kCount], fb[2][kNI];
-      auto read = [&](int which, int at, int i) {  // the i-th of kNI + kCount operands
+      constexpr int kReads = kNI + kCount;
+      auto read = [&](int half, int at, int i) {  // the i-th of half a unit's operands
         const uint32_t st = lds + at * kStage;
         if (i < kNI)
-          fb[which][i] = rb.get(st + StageA::kBytes, kDual ? (i & 1) + 8 * (i >> 1) : i);
+          fb[half][i] = rb.get(st + StageA::kBytes, i < kHalf ? i : i - kHalf + 8, half);
         else
-          fa[which][i - kNI] = ra.get(st, i - kNI);
+          fa[half][i - kNI] = ra.get(st, i - kNI, half);
       };
-      // One step: groups of four products, in their gaps the reads of the next step's operands and,
-      // last, the DMA into this step's stage.  The order is pinned: left to itself the compiler
-      // moves the products behind the barrier, where they wait for the reads of the step after.
-      auto step = [&](int which) {
-        constexpr int kReads = kNI + kCount, kPerGap = kCount > 4 ? 2 : (kReads + 1) / 2;
+      // Half a unit: groups of products of one row block, in their gaps the reads of the next
+      // half's operands.  In the second half also the barrier (the next unit has landed, and every
+      // wavefront has read this one) and the DMA into this unit's stage.  The barrier stands behind
+      // the first groups: the matrix cores have work while the wavefronts meet.  The order is
+      // pinned: left to itself the compiler moves the products behind the barrier and the reads in
+      // front of the products.
+      auto step = [&](auto half_c, bool behind) {
+        constexpr int half = decltype(half_c)::value;
+        constexpr int kFirst = half && kCount > 2 ? kCount / 4 : 0;  // groups in front of the barrier, less one
+        constexpr int kGaps = kCount - kFirst, kReadGaps = kGaps > 2 ? kGaps - 1 : 1;
         const int here = stage;
-        stage = stage + 1 == kDepth ? 0 : stage + 1;
+        if (half) stage = stage + 1 == kUnits ? 0 : stage + 1;
 #pragma unroll
         for (int i = 0; i < kCount; ++i) {
 #pragma unroll
-          for (int j = 0; j < kNI; ++j) acc[i][j] = mfma16<S>(fb[which][j], fa[which][i], acc[i][j]);
+          for (int j = 0; j < kNI; ++j) acc[i][j] = mfma16<S>(fb[half][j], fa[half][i], acc[i][j]);
           __builtin_amdgcn_sched_barrier(0);
+          if (i < kFirst) continue;
+          const int gap = i - kFirst;
+          if (half && gap == 0) {
+            if (ahead_units == 0) advance();
+            if (behind)
+              stage_barrier<kPending + kStores>();
+            else
+              stage_barrier<kPending>();
+            __builtin_amdgcn_sched_barrier(0);
+          }
 #pragma unroll
-          for (int r = i * kPerGap; r < (i + 1) * kPerGap && r < kReads; ++r) read(1 - which, stage, r);
-          if (i == kCount - 2) sa.issue(lds + here * kStage, wave);
-          if (i == kCount - 1) sb.issue(lds + here * kStage + StageA::kBytes, wave);
+          for (int r = gap * kReads / kReadGaps; r < (gap + 1) * kReads / kReadGaps && r < kReads; ++r)
+            read(1 - half, stage, r);
+          if (half) {
+#pragma unroll
+            for (int j = gap * kIssues / kGaps; j < (gap + 1) * kIssues / kGaps; ++j) issue(j, here);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
-        --ahead_steps;
       };
 #pragma unroll
-      for (int r = 0; r < kNI + kCount; ++r) read(0, stage, r);
-      bool behind = tile != first_tile;  // the last tile's stores may still be in flight
-      for (int pair = pairs_of(t.K); pair > 0; --pair) {
-        // At the barrier of a step the next one has landed, and every wavefront has read this one.
-        // (The last step of a tile reads the next tile's first, which that tile reads again.)
-        // The steps that a tile's first two wait for were staged before the last tile's stores.
-        if (ahead_steps == 0) advance();
-        if (behind)
-          stage_barrier<kPending + kStores>();
-        else
-          stage_barrier<kPending>();
-        __builtin_amdgcn_sched_barrier(0);
-        step(0);
-        if (behind)
-          stage_barrier<kPending + kStores>();
-        else
-          stage_barrier<kPending>();
-        __builtin_amdgcn_sched_barrier(0);
-        step(1);
+      for (int r = 0; r < kReads; ++r) read(0, stage, r);
+      // (The last unit of a tile reads the next tile's first, which that tile reads again.  The
+      // unit that a tile's first one waits for was staged before the last tile's stores.)
+      bool behind = tile != first_tile;
+      for (int unit = units_of(t.K); unit > 0; --unit) {
+        step(std::integral_constant<int, 0>{}, behind);
+        step(std::integral_constant<int, 1>{}, behind);
         behind = false;
       }
     };
     if (blocks > kMI / 2)
       run(std::integral_constant<int, kMI>{});
-    else
+    else if (kMI < 4 || blocks > kMI / 4)
       run(std::integral_constant<int, kMI / 2>{});
+    else
+      run(std::integral_constant<int, (kMI < 4 ? 1 : kMI / 4)>{});
 
     // ---- epilogue: eight consecutive columns of a row per lane and pair of blocks; all lanes
     // execute all loads and stores, those outside at kOutside
@@ -357,8 +381,8 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2,
     const int64_t row0 = kKind == kWeightBack ? (int64_t)t.e * p.M + t.m0 : (int64_t)t.row0 + t.m0;
     const __amdgpu_buffer_rsrc_t out = open_resource(p.out + (row0 * p.ldo + t.n0) * 2);
     const int here = fresh_lane();
-    const int col0 = (kDual ? 32 : 64) * wn + eight_column(here);  // within the tile
-    auto row_of = [&](int i) { return 16 * (2 * i + wm) + (here & 15); };
+    const int col0 = wave_cols + eight_column(here);  // within the tile
+    auto row_of = [&](int i) { return 16 * (kWM * i + wm) + (here & 15); };
     auto offset_of = [&](int row, int col, int ld) {
       return row < t.m_left && t.n0 + col < p.N ? ((uint32_t)row * (uint32_t)ld + (uint32_t)col) * 2u : kOutside;
     };
@@ -441,21 +465,26 @@ __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2,
   stage_barrier<0>();  // no DMA outlives the workgroup's LDS
 }
 
-// Tiles of 256 rows where the experts' rows fill them, else of 128.
 template <int kKind>
 static void launch_product(const ProductDev& p, int dtype, hipStream_t s) {
   const int64_t cols = kKind == kGateUp ? kTileN / 2 : kTileN;
-  const bool big = kKind == kWeightBack ? p.M > 128 : (int64_t)p.R >= (int64_t)p.E * 192;
-  const int64_t tm = big ? 256 : 128;
+#ifdef MOE_SHAPE
+  const int tm = kKind == kWeightBack ? std::max(MOE_SHAPE, 128) : MOE_SHAPE;
+#else
+  const int tm = kKind == kWeightBack ? 256 : p.R >= p.E * 192 ? 256 : p.R >= p.E * 32 ? 128 : 64;
+#endif
   const int64_t m_tiles = kKind == kWeightBack ? p.E * ceil_div(p.M, tm) : p.R / tm + std::min(p.E, p.R);
   const int64_t tiles = m_tiles * ceil_div(p.N, cols);
   const unsigned grid = (unsigned)std::min<int64_t>(256, ceil_div(tiles, kXcds) * kXcds);
+  auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * kWaves), 0, s, p); };
   auto go = [&](auto type) {
     using S = decltype(type);
-    if (big)
-      hipLaunchKernelGGL((k_product<S, kKind, 8>), dim3(grid), dim3(kTileThreads), 0, s, p);
-    else
-      hipLaunchKernelGGL((k_product<S, kKind, 4>), dim3(grid), dim3(kTileThreads), 0, s, p);
+    if (tm == 256)
+      launch(k_product<S, kKind, Shape256>);
+    else if (kKind == kWeightBack || tm == 128)
+      launch(k_product<S, kKind, Shape128>);
+    else if constexpr (kKind != kWeightBack)
+      launch(k_product<S, kKind, Shape64>);
   };
   if (dtype == MOE_BF16)
     go(bf16_row_t{});

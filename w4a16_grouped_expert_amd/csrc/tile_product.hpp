@@ -1,11 +1,13 @@
 // Products of 16-bit matrices on the matrix cores, C[m][n] = sum_k A(m, k) B(n, k) with
-// float32 sums, tiled for one workgroup of eight wavefronts: 128 or 256 m by 256 n.
+// float32 sums, tiled for one workgroup of eight wavefronts: 256, 128 or 64 m by 256 n.
 //
-// Either operand may have its k or its m (n) contiguous in memory.  Steps of 32 k are staged
-// in a ring in LDS by DMA (buffer_load ... lds, no registers), several steps ahead and across
-// the tiles of a workgroup: the first steps of a tile land while the tile before it is stored.
-// Each wavefront reads a step's operands into registers while it multiplies the step before.
-//  - k contiguous: rows of 32 k, 64 bytes; 16-byte chunk c of row r at slot c ^ row_swizzle(r),
+// Either operand may have its k or its m (n) contiguous in memory.  Units of 64 k are staged
+// in a ring in LDS by DMA (buffer_load ... lds, no registers), ahead of the products and across
+// the tiles of a workgroup: the first units of a tile land while the tile before it is stored.
+// Each wavefront reads the operands of one half of a unit into registers while it multiplies
+// the half before.
+//  - k contiguous: rows of 64 k, 128 bytes, whole cache lines (rows of 64 bytes come at half the
+//    rate: 70 against 130 GB/s per CU out of the L2); 16-byte chunk c of row r at slot c ^ (r & 7),
 //    so that the lanes of a phase of ds_read_b128 hit different banks.
 //  - m contiguous: rows of one k; 32-byte pair p of row k at slot p ^ pair_swizzle(k).
 //    ds_read_b64_tr_b16 reads four k by 16 m per 16 lanes and hands each lane the four k of its
@@ -19,11 +21,9 @@
 
 namespace moe {
 
-constexpr int kTileN = 256;       // n per workgroup
-constexpr int kStepK = 32;        // k per stage
-constexpr int kTileWaves = 8;     // 2 in m (rows of 16 in turn) x 4 in n (64 each)
-constexpr int kTileThreads = 64 * kTileWaves;
-constexpr int kNI = 4;            // 16-column blocks of a wavefront
+constexpr int kTileN = 256;   // n per workgroup
+constexpr int kUnitK = 64;    // k per unit, two MFMA steps
+constexpr int kWaves = 8;     // per workgroup
 constexpr uint32_t kOutside = 0x80000000u;  // an offset past every resource
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -67,7 +67,6 @@ __device__ __forceinline__ void store16(const u32x4_t& v, __amdgpu_buffer_rsrc_t
 __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t offset) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0);
 }
-__device__ __forceinline__ int row_swizzle(int r) { return ((r >> 3) & 1) | ((((r >> 2) ^ (r >> 3)) & 1) << 1); }
 __device__ __forceinline__ int pair_swizzle(int k) { return (k & 3) | ((k >> 1) & 4); }
 __device__ __forceinline__ i32x4_t resource(const void* base, uint32_t bytes) {
   const uint64_t a = (uint64_t)(uintptr_t)base;
@@ -83,90 +82,92 @@ struct OperandTile {
   int rows;          // m that are there from m0 on (at least 1)
 };
 
-// The staging of one operand of kX m (128 or 256) by the wavefronts of a workgroup, one step
-// after the other.
+// The staging of one operand of kX m (64, 128 or 256) by the wavefronts of a workgroup, one
+// unit after the other.
 // kDual: two tensors of kX / 2 rows each, one behind the other in the stage (k contiguous).
 template <int kX, bool kMContig, bool kDual = false>
 struct Stager {
-  static constexpr int kBytes = kX * kStepK * 2;
-  static constexpr int kIssues = kBytes / 1024 / kTileWaves;  // DMA instructions per wavefront and step
-  static constexpr int kChunks = kX / 8;                      // m contiguous: 16-byte chunks of a row,
-  static constexpr int kRows = 64 / kChunks;                  // rows of k per instruction
+  static constexpr int kBytes = kX * kUnitK * 2;
+  static constexpr int kIssues = kBytes / 1024 / kWaves;  // DMA instructions per wavefront and unit
+  static constexpr int kChunks = kX / 8;                  // m contiguous: 16-byte chunks of a row,
+  static constexpr int kRows = 64 / kChunks;              // rows of k per instruction
   static_assert(!(kMContig && kDual), "two tensors lie one behind the other with k contiguous only");
-  static_assert(kIssues <= 2, "");
-  const char* base;  // m contiguous: moves on with the steps
+  static_assert(kIssues * kWaves * 1024 == kBytes && kRows * kIssues == 8, "eight k per wavefront");
+  const char* base;  // m contiguous: moves on with the units
   int ld2;           // bytes between rows
-  int left;          // k from the next step on
+  int left;          // k from the next unit on
   uint32_t edge;     // k contiguous: size of the resource; m contiguous: bytes of a row
-  uint32_t off[2];   // this lane's offset in the next step; m contiguous: of both instructions
-  int kc8;           // k contiguous: first k of this lane's chunk within a step
+  uint32_t off[2];   // this lane's offset in the next unit; m contiguous: of even and odd instructions
+  int kc8;           // k contiguous: first k of this lane's chunk within a unit
 
   // t: the operand's tile; for kDual t2 is the second tensor's
   __device__ __forceinline__ void start(const OperandTile& t, int k_total, int wave, int lane,
                                         const OperandTile* t2 = nullptr) {
-    const OperandTile& mine = kDual && wave >= kTileWaves / 2 ? *t2 : t;
+    const OperandTile& mine = kDual && wave >= kWaves / 2 ? *t2 : t;
     base = mine.base;
     ld2 = mine.ld * 2;
     left = k_total;
     if constexpr (!kMContig) {
-      // instruction j of a wavefront fills 16 rows from 16 (wave kIssues + j): lane l the slot l & 3 of row l >> 2
-      const int first = 16 * kIssues * (kDual ? wave & (kTileWaves / 2 - 1) : wave) + (lane >> 2);
-      kc8 = 8 * ((lane & 3) ^ row_swizzle(lane >> 2));
+      // instruction j of a wavefront fills 8 rows from 8 (wave kIssues + j): lane l the slot l & 7 of row l >> 3
+      const int first = 8 * kIssues * (kDual ? wave & (kWaves / 2 - 1) : wave) + (lane >> 3);
+      kc8 = 8 * ((lane & 7) ^ (lane >> 3));
       off[0] = (uint32_t)first * (uint32_t)ld2 + 2u * kc8;
-      edge = (uint32_t)(min(mine.rows, kDual ? kX / 2 : kX) - 1) * (uint32_t)ld2 + 2u * k_total;
+      edge = __builtin_amdgcn_readfirstlane((min(mine.rows, kDual ? kX / 2 : kX) - 1) * ld2 + 2 * k_total);
     } else {
       const int pos = lane & (kChunks - 1);
 #pragma unroll
-      for (int v = 0; v < kIssues; ++v) {
-        const int k = (wave * kIssues + v) * kRows + lane / kChunks;
+      for (int v = 0; v < 2; ++v) {
+        const int k = 8 * wave + v * kRows + lane / kChunks;
         off[v] = (uint32_t)k * (uint32_t)ld2 + 16u * (pos ^ (2 * pair_swizzle(k)));
       }
       edge = 2u * mine.rows;
     }
   }
-  // nothing more to stage: the steps from here on are zeros
+  // nothing more to stage: the units from here on are zeros
   __device__ __forceinline__ void stop() { left = 0; }
-  // stage the next step
-  __device__ __forceinline__ void issue(uint32_t lds, int wave) {
-    const uint32_t to = lds + wave * kIssues * 1024;
+  // instruction j (a constant, in order) of the staging of the next unit; the last one moves on
+  __device__ __forceinline__ void issue(int j, uint32_t lds, int wave) {
+    const uint32_t to = lds + (wave * kIssues + j) * 1024;
     if constexpr (!kMContig) {
-      const i32x4_t r = resource(base, edge);
       const uint32_t from = kc8 < left ? off[0] : kOutside;
-#pragma unroll
-      for (int j = 0; j < kIssues; ++j) dma16(r, from + (uint32_t)(16 * j * ld2), to + 1024 * j);
-      off[0] += 2 * kStepK;
+      dma16(resource(base, edge), from + (uint32_t)(8 * j * ld2), to);
     } else {
-      const i32x4_t r = resource(base, left > 0 ? (uint32_t)(min(left, kStepK) - 1) * (uint32_t)ld2 + edge : 0u);
-#pragma unroll
-      for (int j = 0; j < kIssues; ++j) dma16(r, off[j], to + 1024 * j);
-      base += (int64_t)kStepK * ld2;
+      const i32x4_t r = resource(base, left > 0 ? (uint32_t)(min(left, kUnitK) - 1) * (uint32_t)ld2 + edge : 0u);
+      // (an even number of instructions further is four rows, if there are that many: the swizzle repeats)
+      dma16(r, off[j & 1] + (uint32_t)((j & ~1) * kRows * ld2), to);
     }
-    left -= kStepK;
+    if (j + 1 < kIssues) return;
+    if constexpr (!kMContig)
+      off[0] += 2 * kUnitK;
+    else
+      base += (int64_t)kUnitK * ld2;
+    left -= kUnitK;
   }
 };
 
-// This lane's MFMA operands of a staged operand.  kStride: 16-m blocks between two of the
-// wavefront's, 1 (from a multiple of 4 on) or 2 (from 0 or 1 on).
+// This lane's MFMA operands of a staged operand: blocks of 16 m, kStride between two of them.
 template <int kX, bool kMContig, int kStride>
 struct Reader {
-  uint32_t at;
+  uint32_t at[2];  // of the two halves of a unit
   __device__ __forceinline__ void start(int first, int lane) {
     const int i = lane & 15, q = lane >> 4;
-    if constexpr (!kMContig) {
-      at = (uint32_t)((first * 16 + i) * 64 + 16 * (q ^ row_swizzle(i)));
-    } else {
-      const int k = 8 * q + (i >> 2);
-      at = (uint32_t)(k * kX * 2 + 32 * (first ^ pair_swizzle(k)) + 8 * (i & 3));
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if constexpr (!kMContig) {
+        at[s] = (uint32_t)((first * 16 + i) * 128 + 16 * ((4 * s + q) ^ (i & 7)));
+      } else {
+        const int k = 32 * s + 8 * q + (i >> 2);
+        at[s] = (uint32_t)(k * kX * 2 + 32 * (first ^ pair_swizzle(k)) + 8 * (i & 3));
+      }
     }
   }
-  // block b (a constant) of the operand staged at `stage` in LDS.  k contiguous: any block; m
-  // contiguous: b < 4, or 8 with a stride of 2.  There the pair of block b is that of block 0 with
-  // bits of b changed (the swizzle and the stage's address leave them alone).
-  __device__ __forceinline__ u32x4_t get(uint32_t stage, int b) const {
+  // block b (a constant) of half s of the operand staged at `stage` in LDS.  m contiguous: the pair
+  // of block b is that of block 0 with bits changed that are zero in the first block's number.
+  __device__ __forceinline__ u32x4_t get(uint32_t stage, int b, int s) const {
     if constexpr (!kMContig) {
-      return *(const MOE_LDS u32x4_t*)(stage + at + b * kStride * 1024);
+      return *reinterpret_cast<const MOE_LDS u32x4_t*>((uintptr_t)(stage + at[s] + b * kStride * 2048));
     } else {
-      const uint32_t p = ((stage + at) ^ ((b & 3) * kStride * 32)) + (b >> 2) * 256;
+      const uintptr_t p = ((stage + at[s]) ^ (((b * kStride) & 7) * 32)) + ((b * kStride) >> 3) * 256;
       typedef MOE_LDS s16x4_t* lds_ptr;
       const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p)));
       const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * kX * 2)));
