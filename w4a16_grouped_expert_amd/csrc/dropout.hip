@@ -49,14 +49,6 @@ __device__ __forceinline__ float col_of(const u32x4_t& w, int i) {
     return (float)__builtin_bit_cast(f16x2_t, word)[i & 1];
   }
 }
-template <typename S>
-__device__ __forceinline__ void store_one(S* p, float v) {
-  if constexpr (std::is_same<S, bf16_row_t>::value)
-    p->bits = (uint16_t)f32_to_bf16_bits(v);
-  else
-    *p = (S)v;
-}
-
 // A dropped element is selected away, not multiplied by zero: infinities and NaN in it do
 // not reach the output.
 __device__ __forceinline__ float dropped(float x, bool keep, float scale, float r) {

@@ -15,6 +15,8 @@
 //   dx        A = [dg, du], B = W13 with n contiguous
 //   dW13, dWd A and B with the rows as k, per expert
 // h, dg and du are rounded to the tensors' type once, as the operands of the next product.
+#include <cmath>
+
 #include "philox.hpp"
 #include "tile_product.hpp"
 
@@ -88,29 +90,29 @@ struct Tile {
 // Persistent workgroups, each with its tiles in turn.  All loads are issued kUnits - 1 units ahead
 // of the products by a cursor of its own, which runs into the next tiles while this one ends.
 //
-// Tile shapes: rows of a tile, by wavefronts in m and blocks of 16 rows and columns of each.
-struct Shape256 {
-  static constexpr int kWM = 2, kMI = 8, kNI = 4, kUnits = 2;
+// Tile shapes: wavefronts, those of them in m, blocks of 16 rows and columns of each, units of the
+// ring and workgroups per CU.
+template <int waves, int wm, int mi, int ni, int units, int per_cu>
+struct Shape {
+  static constexpr int kWaves = waves, kWM = wm, kMI = mi, kNI = ni, kUnits = units, kPerCu = per_cu;
+  static constexpr int kTileM = wm * mi * 16, kTileN = waves / wm * ni * 16;
 };
-struct Shape128 {
-  static constexpr int kWM = 2, kMI = 4, kNI = 4, kUnits = 3;
-};
-struct Shape64 {
-  static constexpr int kWM = 2, kMI = 2, kNI = 4, kUnits = 3;
-};
+typedef Shape<8, 2, 8, 4, 2, 1> Shape256;   // 256 x 256
+typedef Shape<8, 2, 4, 4, 3, 1> Shape128;   // 128 x 256
+typedef Shape<8, 2, 2, 4, 3, 1> Shape64;    // 64 x 256
+typedef Shape<4, 2, 4, 4, 2, 2> ShapeHalf;  // 128 x 128, two workgroups per CU
 
-template <typename S, int kKind, typename Shape>
-__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_product(ProductDev p) {
-  constexpr int kWM = Shape::kWM, kMI = Shape::kMI, kNI = Shape::kNI, kUnits = Shape::kUnits;
-  constexpr int kTileM = kWM * kMI * 16;
-  static_assert(kWaves / kWM * kNI * 16 == kTileN, "");
+template <typename S, int kKind, typename Sh>
+__global__ __launch_bounds__(64 * Sh::kWaves) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_product(ProductDev p) {
+  constexpr int kWaves = Sh::kWaves, kWM = Sh::kWM, kMI = Sh::kMI, kNI = Sh::kNI, kUnits = Sh::kUnits;
+  constexpr int kTileM = Sh::kTileM, kTileN = Sh::kTileN;
   constexpr bool kDual = kKind == kGateUp;
   constexpr bool kAMContig = kKind == kWeightBack;
   constexpr bool kBMContig = kKind >= kGateBack;
   constexpr int kCols = kDual ? kTileN / 2 : kTileN;
   constexpr int kHalf = kDual ? kNI / 2 : kNI;  // blocks of a wavefront within a tensor
-  typedef Stager<kTileM, kAMContig> StageA;
-  typedef Stager<kTileN, kBMContig, kDual> StageB;
+  typedef Stager<kTileM, kWaves, kAMContig> StageA;
+  typedef Stager<kTileN, kWaves, kBMContig, kDual> StageB;
   constexpr int kStage = StageA::kBytes + StageB::kBytes;
   constexpr int kIssues = StageA::kIssues + StageB::kIssues;
   constexpr int kPending = (kUnits - 2) * kIssues;
@@ -314,7 +316,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
       auto read = [&](int half, int at, int i) {  // the i-th of half a unit's operands
         const uint32_t st = lds + at * kStage;
         if (i < kNI)
-          fb[half][i] = rb.get(st + StageA::kBytes, i < kHalf ? i : i - kHalf + 8, half);
+          fb[half][i] = rb.get(st + StageA::kBytes, i < kHalf ? i : i - kHalf + kTileN / 32, half);
         else
           fa[half][i - kNI] = ra.get(st, i - kNI, half);
       };
@@ -465,26 +467,145 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
   stage_barrier<0>();  // no DMA outlives the workgroup's LDS
 }
 
+// Few rows per expert: gate/up or down by workgroups of 16 columns (16 gate and 16 up columns), whose
+// eight wavefronts share K and add their sums in LDS in wavefront order.  Weights go from memory to
+// the matrix cores' registers, with four 64-k pieces of each wavefront requested before the first
+// is used; nothing is staged.  Bound by latency at one expert (a row of d = 2048, I = 1024: 10.8 us
+// for the call, 31 by tiles of 64 rows, which stage 32 units one behind the other), by memory at
+// large ones (d = 4096, I = 14336: 75 us, 4.7 TB/s).
+template <typename S, bool kDual>
+__global__ __launch_bounds__(512) void k_few(ProductDev p) {
+  constexpr int kBlocks = kDual ? 2 : 1, kAtOnce = 4, kWaves = 8;
+  __shared__ float s_part[kWaves][kBlocks][16][17];
+  const int lane = lane_id(), i = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int row0, count;
+  const int e = blockIdx.y, n0 = blockIdx.x * 16;
+  expert_rows(p, e, row0, count);
+  const char* w[kBlocks];
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b)  // columns past the last one read that one
+    w[b] = p.b + e * p.b_expert + ((int64_t)b * p.N + min(n0 + i, p.N - 1)) * p.ldb * 2;
+  DropKey key{};
+  const bool drops = kDual && p.drop.threshold;
+  if (drops) key = drop_key(p.drop);
+  for (int m0 = 0; m0 < count; m0 += 16) {
+    const char* x = p.a + ((int64_t)row0 + min(m0 + i, count - 1)) * p.lda * 2;
+    f32x4_t acc[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) acc[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int k0 = wave * kUnitK; k0 < p.K; k0 += kAtOnce * kWaves * kUnitK) {
+      u32x4_t fx[kAtOnce][2], fw[kAtOnce][2][kBlocks];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = k0 + u * kWaves * kUnitK + 32 * h + 8 * q;
+          const int64_t at = 2 * (int64_t)min(k, p.K - 8);
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) fw[u][h][b] = *reinterpret_cast<const u32x4_t*>(w[b] + at);
+          fx[u][h] = *reinterpret_cast<const u32x4_t*>(x + at);
+        }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t inside = k0 + u * kWaves * kUnitK + 32 * h + 8 * q < p.K ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+            acc[b] = mfma16<S>(fw[u][h][b] & inside, fx[u][h] & inside, acc[b]);
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s_part[wave][b][i][4 * q + r] = acc[b][r];
+    __syncthreads();
+    const int m = threadIdx.x >> 4, n = threadIdx.x & 15, col = n0 + n;
+    if (threadIdx.x < 256 && m0 + m < count && col < p.N) {
+      float v[kBlocks];
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        v[b] = 0.f;
+#pragma unroll
+        for (int o = 0; o < kWaves; ++o) v[b] += s_part[o][b][m][n];
+      }
+      const int64_t row = (int64_t)row0 + m0 + m;
+      if constexpr (kDual) {
+        if (p.gu) {
+          S* at = reinterpret_cast<S*>(p.gu) + row * p.ldgu + col;
+          store_one(at, v[0]);
+          store_one(at + p.N, v[1]);
+        }
+        float slope;
+        v[0] = activate(p.activation, v[0], slope) * v[1];
+        if (drops) {
+          const u32x4_t numbers = drop_numbers(key, p.drop.site, (uint32_t)row, (uint32_t)col >> 3);
+          const uint32_t word = (col & 4) ? ((col & 2) ? numbers[3] : numbers[2]) : ((col & 2) ? numbers[1] : numbers[0]);
+          v[0] = ((col & 1) ? word >> 16 : word & 0xFFFFu) >= p.drop.threshold ? v[0] * p.drop.scale : 0.f;
+        }
+      }
+      store_one(reinterpret_cast<S*>(p.out) + row * p.ldo + col, v[0]);
+    }
+    __syncthreads();
+  }
+}
+
+// The time of a product by tiles of a shape, in microseconds: tiles in rounds, a round of so much
+// per unit of k and so much for its start and end (fitted to the shapes' times on products of one
+// to 64 experts, 64 to 16384 k; where rows, columns or experts leave CUs idle the smaller tiles win:
+// E = 13, R = 2331, d = 1000, I = 712 35 us by 256 x 256, 26 by 128 x 256, 21 by 64 x 256; one
+// expert, R = 4096, K = 16384, N = 2048 388, 279 and 376; E = 64, R = 32768, K = 2048, N = 1024
+// gated 383, 390 and 473).
+template <typename Sh>
+static double product_us(const ProductDev& p, bool weights, bool gated) {
+  const double per_unit = Sh::kTileM == 256 ? 1.5 : Sh::kTileM == 64 ? 0.7 : Sh::kTileN == 256 ? 1.05 : 1.15;
+  const double ends = Sh::kTileM == 256 ? 14 : Sh::kTileM == 64 ? 5 : 7;
+  const double used = std::min(p.E, p.R), rows = (double)p.R / Sh::kTileM;
+  const double m_tiles = weights    ? (double)p.E * ceil_div(p.M, Sh::kTileM)
+                         : p.E == 1 ? std::ceil(rows)
+                                    : std::max(rows + 0.5 * used, 0.9 * used);
+  const double k = weights ? (double)p.R / p.E : p.K;
+  const double rounds = m_tiles * ceil_div(p.N, gated ? Sh::kTileN / 2 : Sh::kTileN) / (256 * Sh::kPerCu);
+  return (rounds <= 1 ? 1 : rounds + 0.5) * (std::ceil(k / kUnitK) * per_unit + ends);
+}
+
 template <int kKind>
 static void launch_product(const ProductDev& p, int dtype, hipStream_t s) {
-  const int64_t cols = kKind == kGateUp ? kTileN / 2 : kTileN;
-#ifdef MOE_SHAPE
-  const int tm = kKind == kWeightBack ? std::max(MOE_SHAPE, 128) : MOE_SHAPE;
-#else
-  const int tm = kKind == kWeightBack ? 256 : p.R >= p.E * 192 ? 256 : p.R >= p.E * 32 ? 128 : 64;
-#endif
-  const int64_t m_tiles = kKind == kWeightBack ? p.E * ceil_div(p.M, tm) : p.R / tm + std::min(p.E, p.R);
-  const int64_t tiles = m_tiles * ceil_div(p.N, cols);
-  const unsigned grid = (unsigned)std::min<int64_t>(256, ceil_div(tiles, kXcds) * kXcds);
-  auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * kWaves), 0, s, p); };
+  constexpr bool weights = kKind == kWeightBack, gated = kKind == kGateUp;
+  auto launch = [&](auto type, auto shape) {
+    using S = decltype(type);
+    using Sh = decltype(shape);
+    const int64_t cols = gated ? Sh::kTileN / 2 : Sh::kTileN, tm = Sh::kTileM;
+    const int64_t m_tiles = weights ? p.E * ceil_div(p.M, tm) : p.R / tm + std::min(p.E, p.R);
+    const int64_t tiles = m_tiles * ceil_div(p.N, cols);
+    const unsigned grid = (unsigned)std::min<int64_t>(256 * Sh::kPerCu, ceil_div(tiles, kXcds) * kXcds);
+    hipLaunchKernelGGL((k_product<S, kKind, Sh>), dim3(grid), dim3(64 * Sh::kWaves), 0, s, p);
+  };
+  const double t256 = product_us<Shape256>(p, weights, gated), t128 = product_us<Shape128>(p, weights, gated);
+  const double half = product_us<ShapeHalf>(p, weights, gated);
+  const double t64 = weights ? 1e30 : product_us<Shape64>(p, weights, gated);
+  const double best = std::min(std::min(t256, t128), std::min(half, t64));
   auto go = [&](auto type) {
     using S = decltype(type);
-    if (tm == 256)
-      launch(k_product<S, kKind, Shape256>);
-    else if (kKind == kWeightBack || tm == 128)
-      launch(k_product<S, kKind, Shape128>);
-    else if constexpr (kKind != kWeightBack)
-      launch(k_product<S, kKind, Shape64>);
+    if constexpr (kKind == kGateUp || kKind == kDown) {
+      // At most 16 rows per expert on average: where tiles of 64 rows leave CUs idle, or where a
+      // workgroup has 256 KB of weights to read (E = 8, R = 16, d = 4096, I = 14336 324 us, 377 by
+      // tiles; E = 64, R = 128, d = 2048, I = 1024 159 us, 145 by tiles).
+      const int64_t tiles = std::min(p.E, p.R) * ceil_div(p.N, gated ? Shape64::kTileN / 2 : Shape64::kTileN);
+      if (p.R <= 16 * (int64_t)p.E && (tiles <= 256 || (gated ? 32 : 16) * (int64_t)p.K >= 1 << 17)) {
+        hipLaunchKernelGGL((k_few<S, gated>), dim3((unsigned)ceil_div(p.N, 16), p.E), dim3(512), 0, s, p);
+        return;
+      }
+    }
+    if (t256 == best)
+      launch(type, Shape256{});
+    else if (t128 == best)
+      launch(type, Shape128{});
+    else if (half == best)
+      launch(type, ShapeHalf{});
+    else if constexpr (!weights)
+      launch(type, Shape64{});
   };
   if (dtype == MOE_BF16)
     go(bf16_row_t{});

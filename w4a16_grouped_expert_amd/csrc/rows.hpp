@@ -212,6 +212,14 @@ __device__ __forceinline__ float load_one(const S* p) {
     return (float)*(const MOE_GLOBAL S*)p;
 }
 
+template <typename S>
+__device__ __forceinline__ void store_one(S* p, float v) {
+  if constexpr (std::is_same<S, bf16_row_t>::value)
+    p->bits = (uint16_t)f32_to_bf16_bits(v);
+  else
+    *p = (S)v;
+}
+
 template <bool kTiny, bool kStream = true, typename S>
 __device__ __forceinline__ void store_piece(S* row, const Piece& p, int d, const float (&v)[kPiece]) {
   store_raw<kTiny, kStream>(row, p, d, pack<S>(v));

@@ -1,5 +1,5 @@
 // Products of 16-bit matrices on the matrix cores, C[m][n] = sum_k A(m, k) B(n, k) with
-// float32 sums, tiled for one workgroup of eight wavefronts: 256, 128 or 64 m by 256 n.
+// float32 sums, by tiles of up to 256 m by 256 n per workgroup.
 //
 // Either operand may have its k or its m (n) contiguous in memory.  Units of 64 k are staged
 // in a ring in LDS by DMA (buffer_load ... lds, no registers), ahead of the products and across
@@ -21,9 +21,7 @@
 
 namespace moe {
 
-constexpr int kTileN = 256;   // n per workgroup
-constexpr int kUnitK = 64;    // k per unit, two MFMA steps
-constexpr int kWaves = 8;     // per workgroup
+constexpr int kUnitK = 64;  // k per unit, two MFMA steps
 constexpr uint32_t kOutside = 0x80000000u;  // an offset past every resource
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -82,22 +80,22 @@ struct OperandTile {
   int rows;          // m that are there from m0 on (at least 1)
 };
 
-// The staging of one operand of kX m (64, 128 or 256) by the wavefronts of a workgroup, one
-// unit after the other.
+// The staging of one operand of kX m (64, 128 or 256) by the kWaves wavefronts of a workgroup,
+// one unit after the other.
 // kDual: two tensors of kX / 2 rows each, one behind the other in the stage (k contiguous).
-template <int kX, bool kMContig, bool kDual = false>
+template <int kX, int kWaves, bool kMContig, bool kDual = false>
 struct Stager {
   static constexpr int kBytes = kX * kUnitK * 2;
   static constexpr int kIssues = kBytes / 1024 / kWaves;  // DMA instructions per wavefront and unit
   static constexpr int kChunks = kX / 8;                  // m contiguous: 16-byte chunks of a row,
   static constexpr int kRows = 64 / kChunks;              // rows of k per instruction
   static_assert(!(kMContig && kDual), "two tensors lie one behind the other with k contiguous only");
-  static_assert(kIssues * kWaves * 1024 == kBytes && kRows * kIssues == 8, "eight k per wavefront");
+  static_assert(kIssues * kWaves * 1024 == kBytes, "");
   const char* base;  // m contiguous: moves on with the units
   int ld2;           // bytes between rows
   int left;          // k from the next unit on
   uint32_t edge;     // k contiguous: size of the resource; m contiguous: bytes of a row
-  uint32_t off[2];   // this lane's offset in the next unit; m contiguous: of even and odd instructions
+  uint32_t off[kMContig ? kIssues : 1];  // this lane's offset in the next unit; m contiguous: of each instruction
   int kc8;           // k contiguous: first k of this lane's chunk within a unit
 
   // t: the operand's tile; for kDual t2 is the second tensor's
@@ -116,9 +114,9 @@ struct Stager {
     } else {
       const int pos = lane & (kChunks - 1);
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int k = 8 * wave + v * kRows + lane / kChunks;
-        off[v] = (uint32_t)k * (uint32_t)ld2 + 16u * (pos ^ (2 * pair_swizzle(k)));
+      for (int j = 0; j < kIssues; ++j) {
+        const int k = (wave * kIssues + j) * kRows + lane / kChunks;
+        off[j] = (uint32_t)k * (uint32_t)ld2 + 16u * (pos ^ (2 * pair_swizzle(k)));
       }
       edge = 2u * mine.rows;
     }
@@ -133,8 +131,7 @@ struct Stager {
       dma16(resource(base, edge), from + (uint32_t)(8 * j * ld2), to);
     } else {
       const i32x4_t r = resource(base, left > 0 ? (uint32_t)(min(left, kUnitK) - 1) * (uint32_t)ld2 + edge : 0u);
-      // (an even number of instructions further is four rows, if there are that many: the swizzle repeats)
-      dma16(r, off[j & 1] + (uint32_t)((j & ~1) * kRows * ld2), to);
+      dma16(r, off[j], to);
     }
     if (j + 1 < kIssues) return;
     if constexpr (!kMContig)
