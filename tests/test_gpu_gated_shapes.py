@@ -1,0 +1,59 @@
+"""Gated feed-forward blocks at sizes that take each tile shape in each product: 256 x 256,
+128 x 256, 128 x 128 and 64 x 256 tiles, and the products of few rows."""
+import numpy as np
+import pytest
+
+from gated_helpers import inputs, offsets_of
+from gpu_helpers import say
+from test_gpu_gated_ffn import check_backward, check_forward
+
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def uneven(R, E):
+    """R rows on E experts, some with none, the first ones with the most."""
+    rng = np.random.default_rng(R + E)
+    p = 1.0 / np.sqrt(np.arange(1, E + 1))
+    p[rng.permutation(E)[:E // 5]] = 0
+    return rng.multinomial(R, p / p.sum()).tolist()
+
+
+@pytest.mark.parametrize("R,E,d,I", [(9000, 4, 1032, 1544), (12000, 5, 264, 2056), (2000, 40, 264, 520),
+                                     (40, 13, 264, 8200), (4096, 1, 512, 2048), (32, 40, 56, 1032),
+                                     (3860, 40, 1336, 32), (36, 3, 32, 32)])
+@pytest.mark.parametrize("dtype,act,p", [("bf16", "silu", 0.2), ("fp16", "gelu", 0.0)])
+def test_tile_shapes(R, E, d, I, dtype, act, p):
+    say(f"gated ffn R={R} E={E} d={d} I={I} {dtype}")
+    off = None if E == 1 else offsets_of(uneven(R, E))
+    x = inputs(R, E, d, I, dtype, seed=R)
+    _, h, gu = check_forward(x, off, act, p, dtype)
+    check_backward(x, gu, h, off, act, p, dtype)
+
+
+@pytest.mark.parametrize("counts", [[300] + [0] * 39, [0] * 39 + [300], [1] * 20 + [0] * 19 + [280],
+                                    [17, 16, 15, 33, 0, 1]])
+def test_few_rows_on_average_many_on_one(counts):
+    """The products of few rows where one expert has more than sixteen."""
+    say(f"gated ffn counts={str(counts)[:40]}")
+    x = inputs(sum(counts), len(counts), 72, 40, "bf16", seed=21)
+    _, h, gu = check_forward(x, offsets_of(counts), "silu", 0.3, "bf16")
+    check_backward(x, gu, h, offsets_of(counts), "silu", 0.3, "bf16")
+
+
+def test_same_bits_every_time():
+    """Twenty calls at sizes with every kind of wait between tiles, the same bits each time."""
+    import w4a16_grouped_expert_amd as moe
+    say("gated ffn repeated")
+    counts = [700, 0, 260, 1, 999, 40]
+    off = torch.from_numpy(offsets_of(counts)).cuda()
+    x = inputs(sum(counts), 6, 520, 264, "bf16", seed=22)
+    first = None
+    for _ in range(20):
+        y, h, gu = moe.moe_gated_ffn(x["rows"], x["w13"], x["w2"], off, save=True)
+        g = moe.moe_gated_ffn_backward(x["dy"], x["rows"], x["w13"], x["w2"], gu, h, off)
+        now = [y, h, gu, g.drows, g.dw13, g.dw2]
+        first = first or now
+        for a, b in zip(first, now):
+            assert torch.equal(a, b)
