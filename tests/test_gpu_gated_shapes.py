@@ -57,3 +57,48 @@ def test_same_bits_every_time():
         first = first or now
         for a, b in zip(first, now):
             assert torch.equal(a, b)
+
+
+def test_rows_far_apart():
+    """Rows at the largest stride, 2^20 elements: offsets past 2^32 bytes in every row tensor."""
+    import w4a16_grouped_expert_amd as moe
+    from gated_helpers import backward_bounds, forward_bounds
+    from rows_helpers import assert_near, f64
+    counts, d, I = [1500, 0, 900], 72, 40
+    say("gated ffn rows far apart")
+    R, off = sum(counts), offsets_of(counts)
+    x = inputs(R, 3, d, I, "bf16", seed=23)
+
+    def far(n, values=None):
+        t = torch.empty((R, 1 << 20), dtype=torch.bfloat16, device="cuda")[:, :n]
+        if values is not None:
+            t.copy_(values)
+        return t
+
+    rows, dy = far(d, x["rows"]), far(d, x["dy"])
+    y, h, gu, drows = far(d), far(I), far(2 * I), far(d)
+    dev_off = torch.from_numpy(off).cuda()
+    moe.moe_gated_ffn_into(rows, x["w13"], x["w2"], y, h, dev_off, gu)
+    grads = moe.GatedFfnGrads(drows, torch.empty_like(x["w13"]), torch.empty_like(x["w2"]))
+    ws = moe.alloc_gated_ffn_workspace(R, d, I, 3, "cuda")
+    moe.moe_gated_ffn_backward_into(dy, rows, x["w13"], x["w2"], gu, h, grads, ws, dev_off)
+    ref, bound = forward_bounds(x, off, "silu", None, "bf16")
+    for name, got, r, b in zip(("y", "h", "gu"), (y, h, gu), ref, bound):
+        assert_near(name, got, r, b)
+    ref, bound = backward_bounds(x, f64(gu), f64(h), off, "silu", None, "bf16")
+    for name, r, b in zip(("drows", "dw13", "dw2"), ref, bound):
+        assert_near(name, getattr(grads, name), r, b)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_saturated_activations(act):
+    """Projections where the activation and its slope are 0, 1 or the projection itself."""
+    say(f"gated ffn saturated {act}")
+    x = inputs(40, 1, 64, 72, "bf16", seed=24)
+    _, h, gu = check_forward(x, None, act, 0.0, "bf16")
+    values = torch.tensor([-1e30, -1e9, -3e4, -90.0, -20.0, -4.0, -0.5, 0.0, 1e-30, 0.5, 4.0, 20.0, 90.0, 3e4, 1e9, 1e20],
+                          device="cuda").bfloat16()
+    gu[:, :72] = values.repeat(180)[:2880].reshape(40, 72)
+    gu[:, 72:] = 0.25
+    x["dy"] = x["dy"] * 2.0 ** -60  # (gradients of u up to 1e20 times it stay in range)
+    check_backward(x, gu, h, None, act, 0.0, "bf16")
