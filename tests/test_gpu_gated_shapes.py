@@ -102,3 +102,48 @@ def test_saturated_activations(act):
     gu[:, 72:] = 0.25
     x["dy"] = x["dy"] * 2.0 ** -60  # (gradients of u up to 1e20 times it stay in range)
     check_backward(x, gu, h, None, act, 0.0, "bf16")
+
+
+def test_two_streams_at_once():
+    """Forward and backward calls on two streams at the same time, each with its own buffers."""
+    import w4a16_grouped_expert_amd as moe
+    say("gated ffn on two streams")
+    counts = [[300, 0, 900], [17, 640, 1]]
+    cases = []
+    for i, c in enumerate(counts):
+        x = inputs(sum(c), 3, 264, 520, "bf16", seed=30 + i)
+        off = torch.from_numpy(offsets_of(c)).cuda()
+        drop = moe.Dropout(0.2, torch.tensor([5 + i, 7], device="cuda"), i)
+        y, h, gu = moe.moe_gated_ffn(x["rows"], x["w13"], x["w2"], off, dropout=drop, save=True)
+        g = moe.moe_gated_ffn_backward(x["dy"], x["rows"], x["w13"], x["w2"], gu, h, off, dropout=drop)
+        cases.append((x, off, drop, (y, h, gu), (g.drows, g.dw13, g.dw2)))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, (x, off, drop, fwd, _) in enumerate(cases):
+            out = moe.moe_gated_ffn(x["rows"], x["w13"], x["w2"], off, dropout=drop, save=True, stream=streams[i])
+            g = moe.moe_gated_ffn_backward(x["dy"], x["rows"], x["w13"], x["w2"], fwd[2], fwd[1], off, dropout=drop,
+                                           stream=streams[i])
+            got[i].append((*out, g.drows, g.dw13, g.dw2))
+    torch.cuda.synchronize()
+    for i, case in enumerate(cases):
+        for outputs in got[i]:
+            for a, b in zip(outputs, (*case[3], *case[4])):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("R,E", [(20, 3), (100, 1), (5000, 2)])
+def test_rows_that_no_expert_has(R, E):
+    """Offsets of zeros: nothing is written but the weights' gradients, which are zero."""
+    import w4a16_grouped_expert_amd as moe
+    say(f"gated ffn R={R} without an expert")
+    x = inputs(R, E, 136, 72, "bf16", seed=40)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    out = [torch.full((R, n), 5.0, dtype=torch.bfloat16, device="cuda") for n in (136, 72, 144, 136)]
+    moe.moe_gated_ffn_into(x["rows"], x["w13"], x["w2"], out[0], out[1], off, out[2])
+    grads = moe.GatedFfnGrads(out[3], torch.full_like(x["w13"], 5.0), torch.full_like(x["w2"], 5.0))
+    ws = moe.alloc_gated_ffn_workspace(R, 136, 72, E, "cuda")
+    moe.moe_gated_ffn_backward_into(x["dy"], x["rows"], x["w13"], x["w2"], out[2], out[1], grads, ws, off)
+    assert all(bool((t == 5.0).all()) for t in out)
+    assert not grads.dw13.any() and not grads.dw2.any()
