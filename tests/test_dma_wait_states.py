@@ -1,7 +1,8 @@
 """The loads from memory to LDS that are written as assembly, as the compiler places them
 (compiled for gfx950, nothing is run).  The compiler does not look into such a load, so what
-the hardware asks in front of it has to be there by construction: five wait states between a
-vector instruction that writes a scalar register and a vector memory instruction that reads it."""
+the hardware asks around it has to be there by construction: five wait states between a vector
+instruction that writes a scalar register and a vector memory instruction that reads it, and M0
+set again before another instruction that reads it."""
 import re
 import subprocess
 
@@ -20,6 +21,17 @@ __global__ void k_resource(const char* const* p, uint32_t* out) {
   const uint32_t lds = (uint32_t)(uintptr_t)s;
   const int lane = threadIdx.x;
   dma16(resource(p[lane], 4096u), 16u * lane, lds);
+  stage_barrier<0>();
+  out[lane] = *(const MOE_LDS uint32_t*)(uintptr_t)(lds + 4 * lane);
+}
+// the compiler's own loads to LDS in front and behind, which read M0 too
+__global__ void k_m0(const uint32_t* g, const char* p, uint32_t* out) {
+  __shared__ __attribute__((aligned(1024))) char s[8192];
+  const uint32_t lds = (uint32_t)(uintptr_t)s;
+  const int lane = threadIdx.x;
+  __builtin_amdgcn_global_load_lds((const MOE_GLOBAL uint32_t*)(g + lane), (MOE_LDS uint32_t*)s, 4, 0, 0);
+  dma16(resource(p, 4096u), 16u * lane, lds + 1024);
+  __builtin_amdgcn_global_load_lds((const MOE_GLOBAL uint32_t*)(g + 64 + lane), (MOE_LDS uint32_t*)s, 4, 256, 0);
   stage_barrier<0>();
   out[lane] = *(const MOE_LDS uint32_t*)(uintptr_t)(lds + 4 * lane);
 }
@@ -81,3 +93,12 @@ def test_wait_states_in_front_of_a_resource(tmp_path):
     assert len(loads) == 1
     states = wait_states(body, loads[0])
     assert states is not None and states >= WAIT_STATES, body
+
+
+def test_m0_is_set_again(tmp_path):
+    """(The compiler keeps M0 between its own two loads where it sees nothing else write it.)"""
+    body = kernel(instructions(TILE_PRODUCT, tmp_path), "k_m0")
+    loads = loads_to_lds(body)
+    assert len(loads) == 3
+    for before, load in zip(loads, loads[1:]):
+        assert any(operands[:1] == ["m0"] for _, operands, _ in body[before + 1:load]), body

@@ -41,11 +41,11 @@ __device__ __forceinline__ f32x4_t mfma16(const u32x4_t& a, const u32x4_t& b, f3
 // counts these loads nor knows what they write: every reader waits for them itself
 // (stage_barrier below).  Nor does it keep their distances: a vector instruction that writes the
 // resource (v_readfirstlane, a scalar register that comes back from a lane) has to lie five wait
-// states in front of the load, one of s_mov and four of s_nop.  (M0 is left as it is: no other
-// instruction here reads it.)
+// states in front of the load, one of s_mov and four of s_nop.  M0 is declared as written: what
+// else reads it sets it again.
 __device__ __forceinline__ void dma16(const i32x4_t& rsrc, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               :: "v"(offset), "s"(rsrc), "s"(lds) : "memory");
+               :: "v"(offset), "s"(rsrc), "s"(lds) : "memory", "m0");
 }
 // At most kPending of this wavefront's vector memory operations are in flight (they end in
 // order) and its LDS reads are done; then the workgroup meets.
