@@ -37,6 +37,26 @@ __global__ void k_m0(const uint32_t* g, const char* p, uint32_t* out) {
 }
 """
 
+PREFILL = r"""
+#include "ffn_prefill.hip"
+using namespace moe;
+template <typename F>
+__device__ void one_load(const char* const* p, uint32_t* out, F&& load) {
+  __shared__ __attribute__((aligned(1024))) char s[8192];
+  const uint32_t lds = lds_addr(s);
+  const int lane = threadIdx.x;
+  load(raw_rsrc(p[lane]), lane, lds);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  out[lane] = reinterpret_cast<volatile uint32_t*>(s)[lane];
+}
+__global__ void k_resource16(const char* const* p, uint32_t* out) {
+  one_load(p, out, [](i32x4_t r, int lane, uint32_t lds) { buf_dma16(r, 16u * lane, 0, lds); });
+}
+__global__ void k_resource4(const char* const* p, uint32_t* out) {
+  one_load(p, out, [](i32x4_t r, int lane, uint32_t lds) { buf_dma4(r, 4u * lane, 0, lds); });
+}
+"""
+
 
 def instructions(source, tmp_path):
     """(mnemonic, operands) of each instruction, by kernel."""
@@ -87,8 +107,10 @@ def kernel(found, name):
     return next(body for label, body in found.items() if name in label)
 
 
-def test_wait_states_in_front_of_a_resource(tmp_path):
-    body = kernel(instructions(TILE_PRODUCT, tmp_path), "k_resource")
+@pytest.mark.parametrize("source,name", [(TILE_PRODUCT, "k_resource"), (PREFILL, "k_resource16"),
+                                         (PREFILL, "k_resource4")], ids=["tile_product", "prefill 16", "prefill 4"])
+def test_wait_states_in_front_of_a_resource(source, name, tmp_path):
+    body = kernel(instructions(source, tmp_path), name)
     loads = loads_to_lds(body)
     assert len(loads) == 1
     states = wait_states(body, loads[0])

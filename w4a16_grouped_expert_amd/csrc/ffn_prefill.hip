@@ -83,6 +83,9 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(
 
 // The same through a buffer resource: the address is base + voff (per lane) + soff
 // (wave-uniform), so advancing a stream by one K group costs no vector ALU work.
+// A vector instruction that writes the resource or soff (v_readfirstlane, a scalar
+// register that comes back from a lane) has to lie five wait states in front of such
+// a load, and the compiler does not look into the asm: two of s_mov, three of s_nop.
 __device__ __forceinline__ i32x4_t raw_rsrc(const void* base) {
   const uint64_t a = (uint64_t)(uintptr_t)base;
   return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)a), __builtin_amdgcn_readfirstlane((int)((a >> 32) & 0xFFFF)),
@@ -90,12 +93,12 @@ __device__ __forceinline__ i32x4_t raw_rsrc(const void* base) {
 }
 __device__ __forceinline__ void buf_dma16(i32x4_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds_base) {
   uint32_t saved;
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %4 offen lds\n\ts_mov_b32 m0, %0"
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 2\n\tbuffer_load_dwordx4 %1, %2, %4 offen lds\n\ts_mov_b32 m0, %0"
                : "=&s"(saved) : "v"(voff), "s"(rsrc), "s"(lds_base), "s"(soff) : "memory");
 }
 __device__ __forceinline__ void buf_dma4(i32x4_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds_base) {
   uint32_t saved;
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %4 offen lds\n\ts_mov_b32 m0, %0"
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 2\n\tbuffer_load_dword %1, %2, %4 offen lds\n\ts_mov_b32 m0, %0"
                : "=&s"(saved) : "v"(voff), "s"(rsrc), "s"(lds_base), "s"(soff) : "memory");
 }
 
