@@ -588,6 +588,7 @@ int moe_dropout(const void* x, int64_t x_stride, const void* residual, int64_t r
  *    dh = drop(dy W2), dg = dh u act'(g), du = dh act(g)
  *    drows = [dg, du] W13, dw13[e] = [dg, du]^T rows, dw2[e] = dy^T h   (over e's rows)
  *
+ *  A dropped element has dg = du = 0 whatever its g and u are, infinities and NaN among them.
  *  drows [num_rows][d], dw13 [E][2I][d], dw2 [E][d][I]: NULL where not wanted; inputs that
  *  only they need may be NULL then.  Gradients of experts without rows are zero.
  *  Float32 sums; dg and du are rounded to dtype as the operands of their products, the

@@ -3,7 +3,8 @@ from a counter-based generator.
 
 Readings: with W13 = [Wg; Wu] of a row's expert, g = x Wg^T, u = x Wu^T,
 h = drop(act(g) u), y = h W2^T; rows of expert e are offsets[e] .. offsets[e + 1] - 1, rows
-behind the last expert's stay as they were (zeros here).  Dropout keeps element (r, c) where
+behind the last expert's stay as they were (zeros here).  A dropped element is zero, and so are
+its gradients, whatever its g and u are (infinities and NaN).  Dropout keeps element (r, c) where
 its 16-bit number of Philox-4x32-10 is at least round(p 2^16) and scales it by 1 / (1 - p)
 at that rounded p.
 (ExactMoE, page "Every Expert Counts: ExactMoE for Memory-Efficient W4A16 Inference",
@@ -84,6 +85,11 @@ def _experts(offsets, num_rows, E):
     return [(e, int(offsets[e]), int(offsets[e + 1])) for e in range(E)]
 
 
+def _times(values, factor, a, b):
+    """Rows a .. b - 1 of a mask on their values; what is dropped is zero, not times zero."""
+    return values if factor is None else np.where(factor[a:b] > 0, values * factor[a:b], 0.0)
+
+
 def gated_ffn(rows, w13, w2, offsets=None, act="silu", factor=None):
     """(y, h, gu); weights [E, 2I, d] and [E, d, I]."""
     rows = np.asarray(rows, dtype=np.float64)
@@ -92,7 +98,7 @@ def gated_ffn(rows, w13, w2, offsets=None, act="silu", factor=None):
     y, h, gu = np.zeros((R, d)), np.zeros((R, I)), np.zeros((R, twoI))
     for e, a, b in _experts(offsets, R, E):
         gu[a:b] = rows[a:b] @ w13[e].T
-        h[a:b] = activation(act, gu[a:b, :I])[0] * gu[a:b, I:] * (1.0 if factor is None else factor[a:b])
+        h[a:b] = _times(activation(act, gu[a:b, :I])[0] * gu[a:b, I:], factor, a, b)
         y[a:b] = h[a:b] @ w2[e].T
     return y, h, gu
 
@@ -105,10 +111,10 @@ def gated_ffn_backward(dy, rows, w13, w2, gu, h, offsets=None, act="silu", facto
     drows, dgu = np.zeros((R, d)), np.zeros((R, twoI))
     dw13, dw2 = np.zeros((E, twoI, d)), np.zeros((E, d, I))
     for e, a, b in _experts(offsets, R, E):
-        dh = dy[a:b] @ w2[e] * (1.0 if factor is None else factor[a:b])
+        dh = dy[a:b] @ w2[e]
         value, slope = activation(act, gu[a:b, :I])
-        dgu[a:b, :I] = dh * gu[a:b, I:] * slope
-        dgu[a:b, I:] = dh * value
+        dgu[a:b, :I] = _times(dh * gu[a:b, I:] * slope, factor, a, b)
+        dgu[a:b, I:] = _times(dh * value, factor, a, b)
         drows[a:b] = dgu[a:b] @ w13[e]
         dw13[e] = dgu[a:b].T @ rows[a:b]
         dw2[e] = dy[a:b].T @ h[a:b]

@@ -451,11 +451,13 @@ __global__ __launch_bounds__(64 * Sh::kWaves) __attribute__((amdgpu_waves_per_eu
             if (drops) n = drop_numbers(key, p.drop.site, (uint32_t)(row0 + row), (uint32_t)(t.n0 + col) >> 3);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              if (drops) v[c] = drop_keeps(n, c, p.drop.threshold) ? v[c] * p.drop.scale : 0.f;
+              // (what is dropped is selected away: its g and u may be infinite)
+              const bool keep = !drops || drop_keeps(n, c, p.drop.threshold);
+              if (drops) v[c] *= p.drop.scale;
               float slope;
               const float act = activate(p.activation, g[c], slope);
-              g[c] = v[c] * u[c] * slope;
-              u[c] = v[c] * act;
+              g[c] = keep ? v[c] * u[c] * slope : 0.f;
+              u[c] = keep ? v[c] * act : 0.f;
             }
             const uint32_t to = offset_of(row, col, p.ldo);
             store16(pack8<S>(g), out, to);
