@@ -579,6 +579,8 @@ int moe_dropout(const void* x, int64_t x_stride, const void* residual, int64_t r
  *  2^20; pointers 16-byte aligned.  Outputs may not overlap inputs or each other.
  *  Sums, activation and dropout in float32; g, u, h and y rounded once each; y is computed
  *  from the rounded h (the operand of its product).  Deterministic.
+ *  MOE_FP16: an element of h beyond 65504 is infinite, and so is, or NaN, its row of y; one
+ *  below 2^-25 is zero.
  *  Limits: d and I multiples of 8 up to 65536, E <= 1024, num_rows <= 2^24.  num_rows == 0
  *  is a no-op.
  *
@@ -593,6 +595,9 @@ int moe_dropout(const void* x, int64_t x_stride, const void* residual, int64_t r
  *  only they need may be NULL then.  Gradients of experts without rows are zero.
  *  Float32 sums; dg and du are rounded to dtype as the operands of their products, the
  *  gradients once.  Deterministic.  dy and drows may not be the same tensor.
+ *  MOE_FP16: dg and du have that type's range too.  An element beyond 65504 is infinite, and
+ *  its row of drows and its row of dw13 infinite or NaN; one below 2^-25 is zero, one below
+ *  2^-14 has fewer bits.  A caller scales dy so that they lie in between.
  *  workspace moe_gated_ffn_backward_workspace_bytes(num_rows, d, I, E) bytes, 256-byte
  *            aligned (-1 for sizes outside the limits); needed for drows and dw13.
  *  num_rows == 0: dw13 and dw2 are set to zero.

@@ -919,7 +919,9 @@ def moe_gated_ffn_backward_into(dy, rows, w13, w2, gu, h, grads: GatedFfnGrads, 
                                 offsets: Optional[torch.Tensor] = None, activation=ACT_SILU,
                                 dropout: Optional[Dropout] = None, stream=None) -> GatedFfnGrads:
     """Gradient of moe_gated_ffn from dy [R, d], at the gu and h of the forward call and with
-    its dropout.  The workspace (alloc_gated_ffn_workspace) is needed for drows and dw13."""
+    its dropout.  The workspace (alloc_gated_ffn_workspace) is needed for drows and dw13.
+    In fp16 the gradients of gu are held in fp16 in between: dy is scaled so that they lie
+    between 2^-14 and 65504."""
     a, dtype, R, d, I, E, dev = _gated_ffn_args(rows, w13, w2, offsets, activation, dropout)
     g = _lib.GatedFfnGradArgs()
     g.dy, g.dy_stride = _rows(dy, "dy", dtype, R, d, dev)
