@@ -523,8 +523,8 @@ int moe_block_norm_backward(const moe_block_norm_args* args, const moe_block_nor
 
 /*
  * moe_dropout -- dropout from a counter-based generator, with the residual's addition; no
- * mask is stored.  (ExactMoE, Abstract: the layers around the routed experts stay in 16
- * bits; in training they are regularised between the blocks.)
+ * mask is stored.  For training the blocks whose layers around the routed experts stay in
+ * BF16 (ExactMoE, Abstract; of training and dropout it says nothing).
  *
  *    out[r][c] = residual[r][c] + (keep(r, c) ? x[r][c] / (1 - p) : 0)
  *
@@ -557,8 +557,8 @@ int moe_dropout(const void* x, int64_t x_stride, const void* residual, int64_t r
 /*
  * moe_gated_ffn -- gated feed-forward blocks with 16-bit weights over rows sorted by expert
  * (from moe_permute), or one dense block over all rows: experts in training, a shared expert
- * beside the routed ones.  (ExactMoE, Abstract: SwiGLU experts, every selected expert of a
- * step through fused grouped kernels.)  With W13 = [Wg; Wu] of the row's expert:
+ * beside the routed ones.  (ExactMoE, Abstract: every selected expert runs through fused
+ * grouped kernels; it names no activation and no training.)  With W13 = [Wg; Wu] of the row's expert:
  *
  *    g = x Wg^T, u = x Wu^T, h = drop(act(g) u), y = h W2^T
  *

@@ -8,7 +8,8 @@ its gradients, whatever its g and u are (infinities and NaN).  Dropout keeps ele
 its 16-bit number of Philox-4x32-10 is at least round(p 2^16) and scales it by 1 / (1 - p)
 at that rounded p.
 (ExactMoE, page "Every Expert Counts: ExactMoE for Memory-Efficient W4A16 Inference",
-Abstract: SwiGLU experts, every selected expert of a step through fused grouped kernels.)
+Abstract: every selected expert runs through fused grouped kernels; it names no activation and
+no training.)
 """
 import math
 

@@ -1,6 +1,6 @@
-// Dropout of row tensors with the residual's addition (ExactMoE, page "Every Expert Counts:
-// ExactMoE for Memory-Efficient W4A16 Inference", Abstract: the layers around the routed
-// experts stay in 16 bits; in training they are regularised between the blocks).
+// Dropout of row tensors with the residual's addition, for training the blocks whose layers
+// around the routed experts stay in BF16 (ExactMoE, page "Every Expert Counts: ExactMoE for
+// Memory-Efficient W4A16 Inference", Abstract; of training and dropout the page says nothing).
 //
 //   out[r][c] = residual[r][c] + (keep(r, c) ? x[r][c] / (1 - p) : 0)
 //

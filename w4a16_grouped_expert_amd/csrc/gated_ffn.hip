@@ -1,7 +1,7 @@
 // Gated feed-forward blocks with 16-bit weights, and their gradient: the experts of a
 // training step over rows sorted by expert, or one dense block over all rows (ExactMoE, page
-// "Every Expert Counts: ExactMoE for Memory-Efficient W4A16 Inference", Abstract: SwiGLU
-// experts; every selected expert of a step runs through fused grouped kernels).
+// "Every Expert Counts: ExactMoE for Memory-Efficient W4A16 Inference", Abstract: every selected
+// expert runs through fused grouped kernels; it names no activation and no training).
 //
 //   g = x Wg^T, u = x Wu^T, h = drop(act(g) u), y = h Wd^T
 //   dh = drop(dy Wd), dg = dh u act'(g), du = dh act(g)
