@@ -19,12 +19,16 @@
 // that is a range as well: beyond 65504 they are infinite, below 2^-25 zero.
 //
 // What bounds them, at 1.2 to 1.45 PFLOP/s that large library products reach here: one dense
-// block (R = 4096, d = 2048, I = 8192, gradient) runs at 1.14 PFLOP/s; per unit of 64 k a tile of
+// block (R = 4096, d = 2048, I = 8192, gradient) runs at 1.12 PFLOP/s; per unit of 64 k a tile of
 // 256 x 256 needs its matrix cores for 2048 cycles, its LDS for as many (192 KB read, 64 KB
-// written) and its DMA for half of them, and they do not overlap fully.  Over 64 experts of some
-// 512 rows (d = 2048, I = 1024) 860 forward and 780 backward: the weights are read from memory for
-// two tiles of rows each, the last tile of an expert is partly empty, and 2 bytes per weight of
-// gradients are stored behind eight units of products.
+// written) and its DMA for half of them, and they do not overlap fully (matrix cores busy for 0.57
+// to 0.64 of the weights' gradients' time).  Over 64 experts of some 512 rows (d = 2048, I = 1024)
+// 815 TFLOP/s forward and 755 backward, matrix cores busy for 0.27 to 0.40: each workgroup has an
+// equal number of tiles, not equal work (gate/up: six at most where the mean by products is 4.4;
+// the CUs have a wavefront for 0.77 of its time), the last tile of an expert is partly empty (1.08
+// times the products), the weights are read from memory for two tiles of rows each, and 2 bytes
+// per weight of gradients are stored behind eight units of products.  dg and du: g and u are
+// requested behind a tile's last product (matrix cores 0.34 of the time dense, 0.27 grouped).
 #include <cmath>
 
 #include "philox.hpp"
@@ -481,10 +485,12 @@ __global__ __launch_bounds__(64 * Sh::kWaves) __attribute__((amdgpu_waves_per_eu
 
 // Few rows per expert: gate/up or down by workgroups of 16 columns (16 gate and 16 up columns), whose
 // eight wavefronts share K and add their sums in LDS in wavefront order.  Weights go from memory to
-// the matrix cores' registers, with four 64-k pieces of each wavefront requested before the first
-// is used; nothing is staged.  Bound by latency at one expert (a row of d = 2048, I = 1024: 10.8 us
-// for the call, 31 by tiles of 64 rows, which stage 32 units one behind the other), by memory at
-// large ones (d = 4096, I = 14336: 75 us, 4.7 TB/s).
+// the matrix cores' registers, nothing is staged.  A pass takes four 64-k pieces of each wavefront;
+// the compiler puts their products between their loads, so that three loads are in flight at its
+// start (gated; four otherwise) and nine at most, in 90 registers.  Bound by that latency at one
+// expert (a row of d = 2048, I = 1024: 7.1 and 4.5 us, 10.8 for the call; 20 and 11 by tiles of 64
+// rows, which stage 32 units one behind the other), by memory at large ones (d = 4096, I = 14336: 50
+// and 24 us, 4.7 TB/s).  An expert's weights are read again for every 16 of its rows.
 template <typename S, bool kDual>
 __global__ __launch_bounds__(512) void k_few(ProductDev p) {
   constexpr int kBlocks = kDual ? 2 : 1, kAtOnce = 4, kWaves = 8;
@@ -564,11 +570,16 @@ __global__ __launch_bounds__(512) void k_few(ProductDev p) {
 }
 
 // The time of a product by tiles of a shape, in microseconds: tiles in rounds, a round of so much
-// per unit of k and so much for its start and end (fitted to the shapes' times on products of one
-// to 64 experts, 64 to 16384 k; where rows, columns or experts leave CUs idle the smaller tiles win:
-// E = 13, R = 2331, d = 1000, I = 712 35 us by 256 x 256, 26 by 128 x 256, 21 by 64 x 256; one
-// expert, R = 4096, K = 16384, N = 2048 388, 279 and 376; E = 64, R = 32768, K = 2048, N = 1024
-// gated 383, 390 and 473).
+// per unit of k and so much for its start and end.  Measured, by 256 x 256, 128 x 256, 128 x 128 and
+// 64 x 256, the chosen one in brackets:
+//   E = 13, R = 2331, d = 1000, I = 712    gate/up  41 (31) 34 37     dx  39 27 23 (20)
+//   E = 1, R = 4096, d = 2048, I = 8192    gate/up  (250) 296 338 417   dx  374 (259) 285 343
+//   E = 64, R = 32768, d = 2048, I = 1024  gate/up  (340) 305 365 420   down  (186) 171 204 230
+//   E = 8, R = 2048, d = 4096, I = 14336   gate/up  (588) 558 680 760   down  (390) 420 485 505
+//   E = 1, R = 32768, d = 1024, I = 512    dW13  601 (372) 428          dWd  673 (420) 433
+// Where rows, columns or experts leave CUs idle the smaller tiles win.  The experts' unequal rows are
+// not in the model: there 128 x 256 wins where 256 x 256 is chosen, by an eighth at most above, by a
+// fifth at E = 8, R = 32768, d = 1024, I = 512 (dh 99 us by 256 x 256, 88 by 128 x 256, 82 by 128 x 128).
 template <typename Sh>
 static double product_us(const ProductDev& p, bool weights, bool gated) {
   const double per_unit = Sh::kTileM == 256 ? 1.5 : Sh::kTileM == 64 ? 0.7 : Sh::kTileN == 256 ? 1.05 : 1.15;
@@ -602,8 +613,14 @@ static void launch_product(const ProductDev& p, int dtype, hipStream_t s) {
     using S = decltype(type);
     if constexpr (kKind == kGateUp || kKind == kDown) {
       // At most 16 rows per expert on average: where tiles of 64 rows leave CUs idle, or where a
-      // workgroup has 256 KB of weights to read (E = 8, R = 16, d = 4096, I = 14336 324 us, 377 by
-      // tiles; E = 64, R = 128, d = 2048, I = 1024 159 us, 145 by tiles).
+      // workgroup has 256 KB of weights to read.  Measured, gate/up and down in us, this kernel
+      // against tiles of 64 rows: one row of d = 2048, I = 1024 7 and 5 against 20 and 11; E = 8,
+      // R = 16, d = 4096, I = 14336 310 and 151 against 316 and 192; E = 8, d = 2048, I = 1024, 2, 8 and
+      // 16 rows per expert on average 19 and 13, 22 and 15, 30 and 22 against 27, 28, 28 and 15; E = 64,
+      // 2 rows each (tiles are taken) 96 and 66 against 102 and 40.  What the rule does not see: rows
+      // on one expert, read 16 at a time (all 128 rows on one of the eight 50 and 33 against 22 and
+      // 13), and many experts with a long K, where tiles win (E = 64, d = 4096, gate/up, 2 and 16 rows
+      // per expert 163 and 304 against 150 and 223, all 1024 rows on one 710 against 40).
       const int64_t tiles = std::min(p.E, p.R) * ceil_div(p.N, gated ? Shape64::kTileN / 2 : Shape64::kTileN);
       if (p.R <= 16 * (int64_t)p.E && (tiles <= 256 || (gated ? 32 : 16) * (int64_t)p.K >= 1 << 17)) {
         hipLaunchKernelGGL((k_few<S, gated>), dim3((unsigned)ceil_div(p.N, 16), p.E), dim3(512), 0, s, p);
